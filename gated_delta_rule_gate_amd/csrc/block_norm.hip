@@ -1,0 +1,406 @@
+// The norms round an attention block (include/kda_norm.h), forward and
+// backward:
+//
+//   n = w x rho,  rho = (mean x^2 + eps)^-1/2 (L2: sum);   y = res + s n act(gate)
+//   z = w2 y rho2,  rho2 = (mean y^2 + eps)^-1/2
+//
+// and, with t the total gradient of y,
+//
+//   t  = dy + rho2 (w2 dz - y rho2^2 mean(w2 dz y))
+//   dres = t,  dgate = s t n act'(gate),  dn = s t act(gate)
+//   dx = rho (w dn - x rho^2 mean(w dn x))       (L2: sum)
+//   dw = sum over rows of dn x rho,  ds = of t n act(gate),  dw2 = of dz y rho2
+//
+// Bound by the bytes of the rows: each input is read once into registers, the
+// row sums are taken there, and each output is written once. A row of D values
+// is held by LPR lanes, NV vectors of eight values each (at most two: the
+// backward holds eight such sets): up to 1024 values by part of a wave or a
+// wave (no barrier), longer rows by a whole workgroup of 256 to 1024 threads. Parameter gradients stay in registers while a workgroup walks its
+// rows; its sums go to the workspace and are added over workgroups in order.
+#include "kda_device.h"
+#include "linear_launch.h"
+
+namespace kda {
+
+namespace {
+
+template <typename T>
+__device__ __forceinline__ void load8(const void *p, int64_t at, float (&x)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    const bf16x8_t v = *reinterpret_cast<const bf16x8_t *>(reinterpret_cast<const bf16_t *>(p) + at);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = static_cast<float>(v[e]);
+  } else {
+    const f32x4_t *v = reinterpret_cast<const f32x4_t *>(reinterpret_cast<const float *>(p) + at);
+    const f32x4_t a = v[0], b = v[1];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = a[e];
+      x[e + 4] = b[e];
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(void *p, int64_t at, const float (&x)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<bf16x8_t *>(reinterpret_cast<bf16_t *>(p) + at) = pack_bf16x8(x);
+  } else {
+    f32x4_t *v = reinterpret_cast<f32x4_t *>(reinterpret_cast<float *>(p) + at);
+    v[0] = f32x4_t{x[0], x[1], x[2], x[3]};
+    v[1] = f32x4_t{x[4], x[5], x[6], x[7]};
+  }
+}
+__device__ __forceinline__ void fill8(float (&x)[8], float v) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = v;
+}
+
+// Sums of a row's lanes: within the wave by shuffles, over a workgroup's waves
+// through LDS (two buffers in turn, so one barrier a sum is enough).
+constexpr int block_threads(int lpr) { return lpr > 256 ? lpr : 256; }
+
+template <int LPR, int NS>
+__device__ __forceinline__ void row_sums(float (&s)[NS], float (*red)[2][16], int &turn) {
+#pragma unroll
+  for (int off = (LPR < 64 ? LPR : 64) / 2; off > 0; off >>= 1)
+#pragma unroll
+    for (int i = 0; i < NS; ++i) s[i] += __shfl_xor(s[i], off);
+  if constexpr (LPR > 64) {
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int i = 0; i < NS; ++i) red[turn][i][wave] = s[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      s[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < LPR / 64; ++w) s[i] += red[turn][i][w];
+    }
+    turn ^= 1;
+  }
+}
+
+__device__ __forceinline__ float act_of(bool silu, float g) {
+  const float s = sigmoid_f32(g);
+  return silu ? g * s : s;
+}
+
+template <typename Tx, typename Tr, int LPR, int NV>
+__global__ __launch_bounds__(block_threads(LPR)) void block_norm_fwd_kernel(BlockNorm p) {
+  constexpr int RPB = block_threads(LPR) / LPR;  // rows of a workgroup at a time
+  __shared__ float red[2][2][16];
+  int turn = 0;
+  const int lane = threadIdx.x % LPR;
+  const float inv = p.l2 ? 1.0f : 1.0f / (float)p.D, inv2 = 1.0f / (float)p.D;
+  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.rows; row0 += (int64_t)gridDim.x * RPB) {
+    const int64_t row = row0 + threadIdx.x / LPR;
+    const bool live = row < p.rows;
+    const int64_t base = row * p.D;
+    float x[NV][8], gt[NV][8], y[NV][8];
+    float s[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * LPR + lane) * 8;
+      const bool ok = live && c < p.D;
+      fill8(x[v], 0.f);
+      fill8(gt[v], 0.f);
+      fill8(y[v], 0.f);
+      if (ok) {
+        load8<Tx>(p.x, base + c, x[v]);
+        if (p.gate) load8<Tx>(p.gate, base + c, gt[v]);
+        if (p.residual) load8<Tr>(p.residual, base + c, y[v]);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[0] += x[v][e] * x[v][e];
+    row_sums<LPR, 1>(s, red, turn);
+    const float rho = 1.0f / sqrtf(s[0] * inv + p.eps);
+    float s2[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * LPR + lane) * 8;
+      if (!live || c >= p.D) continue;
+      float w[8], sc[8];
+      if (p.weight) load8<float>(p.weight, c, w);
+      else fill8(w, 1.f);
+      if (p.scale_vec) load8<float>(p.scale_vec, c, sc);
+      else fill8(sc, p.scale);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float n = x[v][e] * rho * w[e];
+        if (p.gate) n *= act_of(p.silu, gt[v][e]);
+        y[v][e] += n * sc[e];
+        s2[0] += y[v][e] * y[v][e];
+      }
+      store8<Tr>(p.y, base + c, y[v]);
+    }
+    if (!p.z) continue;
+    row_sums<LPR, 1>(s2, red, turn);
+    const float rho2 = 1.0f / sqrtf(s2[0] * inv2 + p.eps);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * LPR + lane) * 8;
+      if (!live || c >= p.D) continue;
+      float w[8];
+      if (p.next_weight) load8<float>(p.next_weight, c, w);
+      else fill8(w, 1.f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] *= y[v][e] * rho2;
+      store8<Tx>(p.z, base + c, w);
+    }
+  }
+}
+
+template <typename Tx, typename Tr, int LPR, int NV>
+__global__ __launch_bounds__(block_threads(LPR)) void block_norm_bwd_kernel(BlockNorm p) {
+  constexpr int RPB = block_threads(LPR) / LPR;
+  __shared__ float red[2][2][16];
+  int turn = 0;
+  const int lane = threadIdx.x % LPR;
+  const float inv = p.l2 ? 1.0f : 1.0f / (float)p.D, inv2 = 1.0f / (float)p.D;
+  float aw[NV][8], as[NV][8], an[NV][8];  // sums over this lane's rows
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    fill8(aw[v], 0.f);
+    fill8(as[v], 0.f);
+    fill8(an[v], 0.f);
+  }
+  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.rows; row0 += (int64_t)gridDim.x * RPB) {
+    const int64_t row = row0 + threadIdx.x / LPR;
+    const bool live = row < p.rows;
+    const int64_t base = row * p.D;
+    float x[NV][8], gt[NV][8], t[NV][8], y[NV][8], dz[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * LPR + lane) * 8;
+      fill8(x[v], 0.f);
+      fill8(gt[v], 0.f);
+      fill8(t[v], 0.f);
+      fill8(y[v], 0.f);
+      fill8(dz[v], 0.f);
+      if (live && c < p.D) {
+        load8<Tx>(p.x, base + c, x[v]);
+        if (p.gate) load8<Tx>(p.gate, base + c, gt[v]);
+        if (p.dy) load8<Tr>(p.dy, base + c, t[v]);
+        if (p.dz) {
+          load8<Tx>(p.dz, base + c, dz[v]);
+          if (p.residual) load8<Tr>(p.residual, base + c, y[v]);
+        }
+      }
+    }
+    float rho = 0.f;
+    if (p.dz) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[0] += x[v][e] * x[v][e];
+      row_sums<LPR, 1>(s, red, turn);
+      rho = 1.0f / sqrtf(s[0] * inv + p.eps);
+      float s2[2] = {0.f, 0.f};
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = (v * LPR + lane) * 8;
+        if (!live || c >= p.D) continue;
+        float w[8], sc[8], w2[8];
+        if (p.weight) load8<float>(p.weight, c, w);
+        else fill8(w, 1.f);
+        if (p.scale_vec) load8<float>(p.scale_vec, c, sc);
+        else fill8(sc, p.scale);
+        if (p.next_weight) load8<float>(p.next_weight, c, w2);
+        else fill8(w2, 1.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float n = x[v][e] * rho * w[e];
+          if (p.gate) n *= act_of(p.silu, gt[v][e]);
+          y[v][e] += n * sc[e];
+          s2[0] += y[v][e] * y[v][e];
+          s2[1] += y[v][e] * dz[v][e] * w2[e];
+        }
+      }
+      row_sums<LPR, 2>(s2, red, turn);
+      const float rho2 = 1.0f / sqrtf(s2[0] * inv2 + p.eps), m = s2[1] * inv2 * rho2 * rho2;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = (v * LPR + lane) * 8;
+        if (!live || c >= p.D) continue;
+        float w2[8];
+        if (p.next_weight) load8<float>(p.next_weight, c, w2);
+        else fill8(w2, 1.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          an[v][e] += dz[v][e] * y[v][e] * rho2;
+          t[v][e] += rho2 * (dz[v][e] * w2[e] - y[v][e] * m);
+        }
+      }
+    }
+    // t is the whole gradient of y from here on; what follows turns it into dn
+    float s3[2] = {0.f, 0.f};
+    float dgv[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * LPR + lane) * 8;
+      if (!live || c >= p.D) continue;
+      if (p.dresidual) store8<Tr>(p.dresidual, base + c, t[v]);
+      float w[8], sc[8];
+      if (p.weight) load8<float>(p.weight, c, w);
+      else fill8(w, 1.f);
+      if (p.scale_vec) load8<float>(p.scale_vec, c, sc);
+      else fill8(sc, p.scale);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float act = 1.f, dact = 0.f;
+        if (p.gate) {
+          const float g = gt[v][e], sg = sigmoid_f32(g), ds = sg * (1.0f - sg);
+          act = p.silu ? g * sg : sg;
+          dact = p.silu ? sg + g * ds : ds;
+        }
+        const float xw = x[v][e] * w[e];  // n / rho
+        dgv[v][e] = t[v][e] * sc[e] * xw * dact;  // dgate / rho
+        y[v][e] = t[v][e] * xw * act;             // d scale / rho
+        t[v][e] *= sc[e] * act;                   // dn
+        s3[0] += x[v][e] * x[v][e];
+        s3[1] += t[v][e] * xw;
+      }
+    }
+    row_sums<LPR, 2>(s3, red, turn);
+    if (!p.dz) rho = 1.0f / sqrtf(s3[0] * inv + p.eps);
+    const float m = s3[1] * inv * rho * rho;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * LPR + lane) * 8;
+      if (!live || c >= p.D) continue;
+      float w[8];
+      if (p.weight) load8<float>(p.weight, c, w);
+      else fill8(w, 1.f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        aw[v][e] += t[v][e] * x[v][e] * rho;
+        as[v][e] += y[v][e] * rho;
+        dgv[v][e] *= rho;
+        w[e] = rho * (t[v][e] * w[e] - x[v][e] * m);
+      }
+      if (p.dgate) store8<Tx>(p.dgate, base + c, dgv[v]);
+      store8<Tx>(p.dx, base + c, w);
+    }
+  }
+
+  // ---- parameter gradients: rows of this workgroup, then the workspace ----
+  float *part = p.part + (int64_t)blockIdx.x * 3 * p.D;
+  __shared__ float sums[RPB > 1 ? 256 : 1][8];
+  float *const wanted[3] = {p.dweight, p.dscale_vec, p.dnext_weight};
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (!wanted[i]) continue;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float(&a)[8] = i == 0 ? aw[v] : (i == 1 ? as[v] : an[v]);
+      const int c = (v * LPR + lane) * 8;
+      if constexpr (RPB > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sums[threadIdx.x][e] = a[e];
+        __syncthreads();
+        if ((int)threadIdx.x < LPR && c < p.D) {
+          for (int r = 1; r < RPB; ++r)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[e] += sums[r * LPR + threadIdx.x][e];
+          store8<float>(part, (int64_t)i * p.D + c, a);
+        }
+      } else if (c < p.D) {
+        store8<float>(part, (int64_t)i * p.D + c, a);
+      }
+    }
+  }
+}
+
+// Sums over the workgroups' parts: 64 columns a workgroup, four waves each
+// taking every fourth part.
+__global__ __launch_bounds__(256) void block_norm_params_kernel(BlockNorm p, int blocks) {
+  __shared__ double red[4][64];
+  float *const wanted[3] = {p.dweight, p.dscale_vec, p.dnext_weight};
+  float *out = wanted[blockIdx.y];
+  if (!out) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  double s = 0.0;
+  if (c < p.D)
+    for (int b = wave; b < blocks; b += 4) s += (double)p.part[((int64_t)b * 3 + blockIdx.y) * p.D + c];
+  red[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < p.D) out[c] = (float)((red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]));
+}
+
+// Lanes a row.
+int row_lanes(int D) {
+  if (D > 1024) return D <= 2048 ? 256 : (D <= 8192 ? 512 : 1024);
+  int lpr = 1;
+  while (lpr < 64 && lpr * 8 < D) lpr *= 2;
+  return lpr;
+}
+
+// Workgroups of the backward: enough to fill the device, few enough that their
+// parts stay small beside the rows.
+int bwd_blocks(int64_t rows, int D) {
+  const int lpr = row_lanes(D), rpb = block_threads(lpr) / lpr;
+  const int64_t need = (rows + rpb - 1) / rpb;
+  const int64_t most = (int64_t)device_cus() * (D > 2048 ? 2 : 4);
+  return (int)(need < most ? (need > 0 ? need : 1) : most);
+}
+
+template <typename Tx, typename Tr, int LPR, int NV>
+hipError_t launch_nv(const BlockNorm &p, bool bwd, hipStream_t st) {
+  constexpr int RPB = block_threads(LPR) / LPR;
+  const int64_t need = (p.rows + RPB - 1) / RPB;
+  if (bwd) {
+    const int blocks = bwd_blocks(p.rows, p.D);
+    hipLaunchKernelGGL((block_norm_bwd_kernel<Tx, Tr, LPR, NV>), dim3(blocks), dim3(block_threads(LPR)), 0, st, p);
+  } else {
+    if (need == 0) return hipSuccess;
+    const int64_t grid = need < 0x7fffffff ? need : 0x7fffffff;
+    hipLaunchKernelGGL((block_norm_fwd_kernel<Tx, Tr, LPR, NV>), dim3((unsigned)grid), dim3(block_threads(LPR)), 0, st, p);
+  }
+  return hipGetLastError();
+}
+
+template <typename Tx, typename Tr>
+hipError_t launch_rows(const BlockNorm &p, bool bwd, hipStream_t st) {
+  switch (row_lanes(p.D)) {
+    case 1: return launch_nv<Tx, Tr, 1, 1>(p, bwd, st);
+    case 2: return launch_nv<Tx, Tr, 2, 1>(p, bwd, st);
+    case 4: return launch_nv<Tx, Tr, 4, 1>(p, bwd, st);
+    case 8: return launch_nv<Tx, Tr, 8, 1>(p, bwd, st);
+    case 16: return launch_nv<Tx, Tr, 16, 1>(p, bwd, st);
+    case 32: return launch_nv<Tx, Tr, 32, 1>(p, bwd, st);
+    case 64: return p.D <= 512 ? launch_nv<Tx, Tr, 64, 1>(p, bwd, st) : launch_nv<Tx, Tr, 64, 2>(p, bwd, st);
+    case 256: return launch_nv<Tx, Tr, 256, 1>(p, bwd, st);
+    case 512: return p.D <= 4096 ? launch_nv<Tx, Tr, 512, 1>(p, bwd, st) : launch_nv<Tx, Tr, 512, 2>(p, bwd, st);
+    default: return launch_nv<Tx, Tr, 1024, 2>(p, bwd, st);
+  }
+}
+
+hipError_t launch_types(const BlockNorm &p, bool bwd, hipStream_t st) {
+  if (!p.is_bf16) return launch_rows<float, float>(p, bwd, st);
+  return p.res_f32 ? launch_rows<bf16_t, float>(p, bwd, st) : launch_rows<bf16_t, bf16_t>(p, bwd, st);
+}
+
+}  // namespace
+
+size_t block_norm_bwd_part_bytes(int64_t rows, int D) {
+  return (size_t)bwd_blocks(rows, D) * 3 * (size_t)D * sizeof(float);
+}
+
+hipError_t launch_block_norm_fwd(const BlockNorm &p, hipStream_t st) { return launch_types(p, false, st); }
+
+hipError_t launch_block_norm_bwd(const BlockNorm &p, hipStream_t st) {
+  hipError_t e = launch_types(p, true, st);
+  if (e != hipSuccess || !(p.dweight || p.dscale_vec || p.dnext_weight)) return e;
+  hipLaunchKernelGGL(block_norm_params_kernel, dim3((p.D + 63) / 64, 3), dim3(256), 0, st, p,
+                     bwd_blocks(p.rows, p.D));
+  return hipGetLastError();
+}
+
+}  // namespace kda

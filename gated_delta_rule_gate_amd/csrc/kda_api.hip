@@ -11,16 +11,23 @@
 #include "../../include/kda.h"
 #include "../../include/kda_stages.h"
 #include "kda_launch.h"
+#include "linear_launch.h"
 
 namespace {
 
 thread_local char g_last_error[256] = "";
 
-kda_status hip_status(hipError_t e) {
+}  // namespace
+
+kda_status kda::report_hip(hipError_t e) {
   if (e == hipSuccess) return KDA_OK;
   snprintf(g_last_error, sizeof(g_last_error), "%s: %s", hipGetErrorName(e), hipGetErrorString(e));
   return KDA_ERR_HIP;
 }
+
+namespace {
+
+kda_status hip_status(hipError_t e) { return kda::report_hip(e); }
 
 bool aligned16(const void *p) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

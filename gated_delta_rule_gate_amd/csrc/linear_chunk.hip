@@ -1,0 +1,208 @@
+// Linear attention with one decay per head: the passes round the chunk walk
+// (linear_walk.h) -- chaining segments, summing the gradients of shared q/k
+// heads, the decay's gradient -- and the choice of segments.
+#include "chunk_fused_tiles.h"
+#include "linear_launch.h"
+#include "linear_segments.h"
+
+namespace kda {
+
+namespace {
+
+// The segments' own state changes chained into the state at every boundary, in
+// place and in the walk's order: S_j += 2^{decay of the segment before j} S_{j-1}.
+// Four elements a thread; a boundary's next state is in flight while one is added.
+__global__ __launch_bounds__(256) void linear_chain_kernel(LinearWalk p, bool rev, int64_t elems) {
+  const int64_t per = (elems / 4 + 255) / 256;
+  const int n = (int)(blockIdx.x / (per * p.H));
+  const int h = (int)(blockIdx.x / per % p.H);
+  const int64_t el = ((int64_t)(blockIdx.x % per) * 256 + threadIdx.x) * 4;
+  const SlotRange sr = slot_range(p.cu, n, p.T);
+  const int64_t nb = sr.len > 0 ? (sr.len - 1) / p.seg : 0;  // boundaries inside the sequence
+  if (nb < 2 || el >= elems) return;
+  const int64_t first = sr.t0 / p.seg + 1, step = (int64_t)p.H * elems;
+  float *at = p.seg_state + (int64_t)h * elems + el;
+  int64_t j = rev ? first + nb - 1 : first;
+  const int64_t d = rev ? -1 : 1;
+  f32x4_t s = *reinterpret_cast<const f32x4_t *>(at + j * step);
+  f32x4_t next = *reinterpret_cast<const f32x4_t *>(at + (j + d) * step);
+  for (int64_t i = 1; i < nb; ++i) {
+    j += d;
+    const f32x4_t own = next;
+    if (i + 1 < nb) next = *reinterpret_cast<const f32x4_t *>(at + (j + d) * step);
+    const float f = fast_exp2((float)p.seg_decay[j * p.H + h]);
+    s = own + f * s;
+    *reinterpret_cast<f32x4_t *>(at + j * step) = s;
+  }
+}
+
+// Gradients of shared q/k heads: the group's fp32 parts added in order.
+template <typename T>
+__global__ __launch_bounds__(256) void linear_group_sum_kernel(const float *in, T *out, const int32_t *cu, int N,
+                                                               int64_t rows, int H, int Hk, int D) {
+  const int G = H / Hk;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // of [rows, Hk, D / 4]
+  const int64_t rk = i / (D / 4), row = rk / Hk;
+  if (row >= rows) return;
+  if (cu && (row < cu[0] || row >= cu[N])) return;
+  const float *src = in + (rk * G) * D + (i % (D / 4)) * 4;
+  f32x4_t s = *reinterpret_cast<const f32x4_t *>(src);
+  for (int g = 1; g < G; ++g) s += *reinterpret_cast<const f32x4_t *>(src + (int64_t)g * D);
+  T *dst = out + rk * D + (i % (D / 4)) * 4;
+  if constexpr (sizeof(T) == 2) *reinterpret_cast<bf16x4_t *>(dst) = to_bf16x4(s);
+  else *reinterpret_cast<f32x4_t *>(dst) = s;
+}
+
+// dg over one anchored stretch of one (sequence, head): a decay at token t
+// scales every later use of everything before it, which is the sum of
+// q.dq - k.dk from t on; from the stretch's end that sum is <h, dh> there. A
+// wave takes the stretch, a lane anchor / 64 neighbouring tokens; sums in fp64.
+constexpr int kDgPer = kLinearAnchor / 64;
+__global__ __launch_bounds__(256) void linear_dg_kernel(LinearDg p) {
+  const int h = (int)(blockIdx.x % ((p.H + 3) / 4)) * 4 + (threadIdx.x >> 6);
+  const int64_t item = blockIdx.x / ((p.H + 3) / 4);
+  if (h >= p.H) return;
+  const int lane = threadIdx.x & 63;
+  LinearWalk w{};
+  w.cu = p.cu;
+  w.B = p.B;
+  w.T = p.T;
+  w.N = p.N;
+  w.seg = p.anchor;
+  SegLoc sg;
+  const bool ok = locate_segment(w, item, false, sg);
+  double sum = 0.0;
+  if (ok) {
+    const int64_t rows = (int64_t)p.B * p.T;
+    double carry = 0.0;
+    for (int cb = 0; cb < p.ncb; ++cb) {
+      if (sg.out >= 0) carry += p.anchor_dot[(sg.out * p.H + h) * p.ncb + cb];
+      else if (p.end_dot) carry += p.end_dot[((int64_t)sg.n * p.H + h) * p.ncb + cb];
+    }
+    double x[kDgPer];
+    double own = 0.0;
+#pragma unroll
+    for (int i = 0; i < kDgPer; ++i) {
+      const int64_t t = sg.lo + lane * kDgPer + i;
+      x[i] = 0.0;
+      if (t < sg.hi)
+        for (int cb = 0; cb < p.ncb; ++cb) {
+          const int64_t at = ((int64_t)cb * p.H + h) * rows + t;
+          x[i] += (double)p.a[at] - (double)p.b[at];
+        }
+      own += x[i];
+    }
+    double after = own;  // of this lane's tokens and all later ones
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double dn = __shfl_down(after, off);
+      if (lane + off < 64) after += dn;
+    }
+    double run = after - own + carry;
+#pragma unroll
+    for (int i = kDgPer - 1; i >= 0; --i) {
+      run += x[i];
+      const int64_t t = sg.lo + lane * kDgPer + i;
+      if (t < sg.hi) {
+        sum += run;
+        if (!p.g_head) p.dg[t * p.H + h] = (float)run;
+      }
+    }
+  }
+  if (p.g_head) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
+    if (lane == 0) p.part[item * p.H + h] = sum;
+  }
+}
+
+// Head decays: the stretches' sums added in a fixed order, one workgroup a head.
+__global__ __launch_bounds__(256) void linear_dg_head_kernel(const double *part, float *dg, int64_t items, int H) {
+  __shared__ double red[256];
+  const int h = blockIdx.x;
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < items; i += 256) s += part[i * H + h];
+  red[threadIdx.x] = s;
+  __syncthreads();
+  for (int off = 128; off > 0; off >>= 1) {
+    if ((int)threadIdx.x < off) red[threadIdx.x] += red[threadIdx.x + off];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) dg[h] = (float)red[0];
+}
+
+}  // namespace
+
+int linear_tile(int width) { return width <= 64 ? 64 : (width <= 128 ? 128 : 256); }
+
+int linear_cols(int width, int *ncb) {
+  const int qt = width <= 64 ? 64 : 128;
+  *ncb = (width + qt - 1) / qt;
+  return qt;
+}
+
+// Segments pay where whole sequences leave compute units idle: the state pass
+// reads two of the walk's three inputs once more (about 0.6 of a chunk's
+// time), and the two extra launches cost about as much as eight chunks.
+int linear_segment(int T, int slots, int H, int Q, bool packed) {
+  int ncb;
+  const int qt = linear_cols(Q, &ncb);
+  const int64_t room = (int64_t)device_cus() * (qt == 64 ? 2 : 1);
+  const int64_t pairs = (int64_t)(packed ? 1 : slots) * H * ncb;
+  const int64_t chunks = (T + 63) / 64;
+  if (pairs < 1 || chunks < 8) return 0;
+  double best = (double)((pairs + room - 1) / room) * chunks;
+  int64_t take = 1;
+  for (int64_t s = 2; s <= 64 && chunks / s >= 4; ++s) {
+    const double cost = (double)((pairs * s + room - 1) / room) * ((chunks + s - 1) / s) * 1.6 + 8;
+    if (cost < 0.95 * best) {
+      best = cost;
+      take = s;
+    }
+  }
+  return take == 1 ? 0 : (int)((chunks + take - 1) / take * 64);
+}
+
+hipError_t launch_linear_chain(const LinearWalk &p, bool rev, int64_t elems, hipStream_t st) {
+  const int64_t grid = (elems / 4 + 255) / 256 * p.H * p.N;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(linear_chain_kernel, dim3((unsigned)grid), dim3(256), 0, st, p, rev, elems);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_walk(const LinearWalk &p, hipStream_t st) {
+  if (p.N == 0) return hipSuccess;
+  if (p.is_bf16) return p.reverse ? launch_linear_walk_bf16_rev(p, st) : launch_linear_walk_bf16_fwd(p, st);
+  return p.reverse ? launch_linear_walk_f32_rev(p, st) : launch_linear_walk_f32_fwd(p, st);
+}
+
+hipError_t launch_linear_group_sum(const float *in, void *out, bool is_bf16, const int32_t *cu, int N, int64_t rows,
+                                   int H, int Hk, int D, hipStream_t st) {
+  const int64_t grid = (rows * Hk * (D / 4) + 255) / 256;
+  if (grid == 0) return hipSuccess;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (is_bf16)
+    hipLaunchKernelGGL(linear_group_sum_kernel<bf16_t>, dim3((unsigned)grid), dim3(256), 0, st, in,
+                       reinterpret_cast<bf16_t *>(out), cu, N, rows, H, Hk, D);
+  else
+    hipLaunchKernelGGL(linear_group_sum_kernel<float>, dim3((unsigned)grid), dim3(256), 0, st, in,
+                       reinterpret_cast<float *>(out), cu, N, rows, H, Hk, D);
+  return hipGetLastError();
+}
+
+int64_t linear_dg_items(int B, int T, int N, int anchor) { return N + ((int64_t)B * T) / anchor; }
+
+hipError_t launch_linear_dg(const LinearDg &p, hipStream_t st) {
+  const int64_t items = linear_dg_items(p.B, p.T, p.N, p.anchor);
+  const int64_t grid = items * ((p.H + 3) / 4);
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (grid > 0) {
+    hipLaunchKernelGGL(linear_dg_kernel, dim3((unsigned)grid), dim3(256), 0, st, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (p.g_head) hipLaunchKernelGGL(linear_dg_head_kernel, dim3(p.H), dim3(256), 0, st, p.part, p.dg, items, p.H);
+  return hipGetLastError();
+}
+
+}  // namespace kda

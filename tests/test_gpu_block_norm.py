@@ -1,0 +1,295 @@
+"""The block norm (norm, gate, residual and scale, next norm) and its gradients on the GPU against
+the 64-bit definition, differentiated, over row widths, types and every combination of its parts.
+
+Tolerances count fp32 roundings: a row's statistic is a sum of D squares (D + 8 roundings of its
+relative size, halved by the root), an activation is off by a few more; every value then passes
+about a dozen products. The terms' sizes come with the reference."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import linear_ref as ref
+from kda_testlib import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+def make(rows, D, dtype, res, gate, scale, nxt, weights=True, seed=0):
+    r = np.random.Generator(np.random.PCG64(seed + D + rows))
+    f = lambda *s: torch.from_numpy(r.standard_normal(s).astype(np.float32))  # noqa: E731
+    rt = res if res is not None else dtype
+    return dict(x=f(rows, D).to(dtype), weight=1 + 0.1 * f(D) if weights else None,
+                gate=f(rows, D).to(dtype) if gate else None,
+                residual=f(rows, D).to(res) if res is not None else None,
+                scale=0.5 + 0.1 * f(D) if scale == "channel" else scale,
+                next_weight=1 + 0.1 * f(D) if nxt and weights else None,
+                dy=f(rows, D).to(rt), dz=f(rows, D).to(dtype) if nxt else None)
+
+
+def on(d, dev="cuda"):
+    return {k: v.to(dev) if isinstance(v, torch.Tensor) else v for k, v in d.items()}
+
+
+NAMES = ("x", "weight", "gate", "residual", "scale", "next_weight")
+
+
+def reference(d, act, nxt, eps, kind):
+    """Outputs and gradients by name in float64, and the sizes of the terms behind the gradients."""
+    t = {k: d[k].double().requires_grad_(True) for k in NAMES if isinstance(d[k], torch.Tensor)}
+    g = lambda k: t.get(k)  # noqa: E731
+    scale = t["scale"] if "scale" in t else (1.0 if d["scale"] is None else d["scale"])
+    outs = ref.norm(t["x"], g("weight"), g("gate"), act, g("residual"), scale, g("next_weight"), nxt, eps, kind)
+    grads = torch.autograd.grad(sum((o * d[n].double()).sum() for o, n in zip(outs, ("dy", "dz")) if d[n] is not None),
+                                list(t.values()))
+    return [o.detach() for o in outs], dict(zip(("d" + k for k in t), grads))
+
+
+def sizes(d, act, nxt, eps, kind):
+    """Sums of the absolute terms behind each gradient, by the formulas of the backward."""
+    D = d["x"].shape[-1]
+    a = lambda k: d[k].double().abs() if isinstance(d[k], torch.Tensor) else 1.0  # noqa: E731
+    x, w, w2 = a("x"), a("weight"), a("next_weight")
+    c = a("scale") if isinstance(d["scale"], torch.Tensor) else abs(1.0 if d["scale"] is None else d["scale"])
+    m = D if kind == "rms" else 1
+    rho = 1 / torch.sqrt((x * x).sum(-1, keepdim=True) / m + eps)
+    gate = d["gate"].double() if d["gate"] is not None else None
+    sig = torch.sigmoid(gate) if gate is not None else 1.0
+    actv = sig * (gate.abs() if act == "silu" else 1.0) if gate is not None else 1.0
+    dact = (sig * (1 + gate.abs()) if act == "silu" else sig) if gate is not None else 0.0
+    n = x * rho * w
+    y = a("residual") * (1.0 if d["residual"] is not None else 0.0) + c * n * actv
+    t = a("dy") if d["dy"] is not None else torch.zeros_like(x)
+    out = {}
+    if nxt:
+        real = reference(d, act, nxt, eps, kind)[0][0]
+        rho2 = 1 / torch.sqrt((real * real).mean(-1, keepdim=True) + eps)
+        dz = a("dz")
+        out["dnext_weight"] = (dz * y * rho2).sum(0)
+        t = t + rho2 * (dz * w2 + y * rho2 ** 2 * (w2 * dz * y).mean(-1, keepdim=True))
+    out["dresidual"] = t
+    out["dscale"] = (t * n * actv).sum(0)
+    out["dgate"] = t * c * n * dact
+    dn = t * c * actv
+    out["dweight"] = (dn * x * rho).sum(0)
+    out["dx"] = rho * (w * dn + x * rho ** 2 * (w * dn * x).sum(-1, keepdim=True) / m)
+    return out, (y, y * (rho2 if nxt else 1.0) * w2)
+
+
+def check(got, want, size, dtype, n, what):
+    got, want = got.detach().cpu().double(), want
+    assert got.shape == want.shape and torch.isfinite(got).all(), what
+    tol = ref.HALF[dtype] * want.abs() + n * ref.ULP32 * size * 1.01
+    off = (got - want).abs()
+    assert (off <= tol).all(), "%s: off by %.3g times the tolerance" % (what, (off / tol.clamp_min(1e-300)).max())
+
+
+def count(D, rows, nxt):
+    """Roundings: a statistic over D values (twice with the next norm), about 32 products, a sum over rows."""
+    return (D + 32) * (2 if nxt else 1) + 32
+
+
+def run_both(d, act, nxt, eps=1e-6, kind="rms"):
+    from gated_delta_rule_gate_amd import block_norm, block_norm_bwd
+
+    g = on(d)
+    kw = dict(gate=g["gate"], gate_act=act, residual=g["residual"], scale=g["scale"], next_weight=g["next_weight"],
+              eps=eps, norm=kind)
+    rows, D = d["x"].shape
+    outs = block_norm(g["x"], g["weight"], next_norm=nxt, **kw)
+    outs = list(outs) if nxt else [outs]
+    want, grads = reference(d, act, nxt, eps, kind)
+    size, osize = sizes(d, act, nxt, eps, kind)
+    n = count(D, rows, nxt)
+    rt = d["residual"].dtype if d["residual"] is not None else d["x"].dtype
+    for o, w, s, t in zip(outs, want, osize, (rt, d["x"].dtype)):
+        check(o, w, s, t, n, "y or z")
+    got = block_norm_bwd(g["x"], g["dy"], g["weight"], dz=g["dz"], **kw)
+    for name, w in grads.items():
+        t = got[name].dtype
+        extra = rows if name in ("dweight", "dscale", "dnext_weight") else 0
+        check(got[name], w, size[name], t, n + extra, name)
+    assert {k for k, v in got.items() if v is not None} == set(grads)
+    return outs, got
+
+
+@pytest.mark.parametrize("D", [8, 16, 24, 40, 64, 128, 200, 256, 512, 520, 1024, 1032, 2048, 2056, 4096, 5000, 8192, 8200,
+                               16384])
+def test_widths(D):
+    need_gpu()
+    d = make(37, D, BF16, FP32, True, "channel", True)
+    run_both(d, "silu", True)
+
+
+@pytest.mark.parametrize("dtype,res", [(BF16, None), (BF16, BF16), (BF16, FP32), (FP32, None), (FP32, FP32)])
+@pytest.mark.parametrize("gate,scale,nxt", list(itertools.product([False, True], [None, 0.25, "channel"], [False, True])))
+def test_parts(dtype, res, gate, scale, nxt):
+    need_gpu()
+    act = "silu" if scale == 0.25 else "sigmoid"
+    run_both(make(19, 128, dtype, res, gate, scale, nxt), act, nxt)
+
+
+@pytest.mark.parametrize("kind", ["rms", "l2"])
+@pytest.mark.parametrize("rows,D", [(1, 64), (5, 72), (3, 4096), (3000, 128), (70001, 8), (1200, 2056)])
+def test_rows_without_weights(rows, D, kind):
+    need_gpu()
+    run_both(make(rows, D, FP32, None, True, None, True, weights=False), "sigmoid", True, eps=1e-5, kind=kind)
+
+
+def test_only_the_next_gradient():
+    """dy may be left out beside dz."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import block_norm_bwd
+
+    d = make(40, 256, BF16, BF16, False, None, True)
+    d["dy"] = None
+    want = reference(d, "sigmoid", True, 1e-6, "rms")[1]
+    size = sizes(d, "sigmoid", True, 1e-6, "rms")[0]
+    g = on(d)
+    got = block_norm_bwd(g["x"], None, g["weight"], dz=g["dz"], residual=g["residual"], next_weight=g["next_weight"])
+    for name, w in want.items():
+        check(got[name], w, size[name], got[name].dtype, count(256, 40, True) + 40, name)
+
+
+def test_zero_rows_and_zero_values():
+    need_gpu()
+    from gated_delta_rule_gate_amd import block_norm, block_norm_bwd
+
+    x = torch.zeros(0, 64, dtype=BF16, device="cuda")
+    w = torch.ones(64, device="cuda")
+    assert block_norm(x, w).shape == (0, 64)
+    got = block_norm_bwd(x, x, w)
+    assert got["dx"].shape == (0, 64) and (got["dweight"] == 0).all()
+    x = torch.zeros(5, 64, dtype=BF16, device="cuda")
+    y, z = block_norm(x, w, next_norm=True)
+    assert (y == 0).all() and (z == 0).all()
+
+
+def test_in_place_residual():
+    need_gpu()
+    from gated_delta_rule_gate_amd import block_norm
+
+    g = on(make(33, 2304, BF16, FP32, False, 0.5, True))
+    kw = dict(scale=0.5, next_weight=g["next_weight"])
+    y, z = block_norm(g["x"], g["weight"], residual=g["residual"], **kw)
+    y2, z2 = block_norm(g["x"], g["weight"], residual=g["residual"], out=g["residual"], **kw)
+    assert y2 is g["residual"] and torch.equal(y, y2) and torch.equal(z, z2)
+
+
+def test_one_row_does_not_touch_another():
+    """NaN in one row stays there."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import block_norm
+
+    for D in (40, 128, 1024, 4096):
+        g = on(make(33, D, BF16, None, True, None, False))
+        y = block_norm(g["x"], g["weight"], gate=g["gate"])
+        g["x"][7, 3] = float("nan")
+        y2 = block_norm(g["x"], g["weight"], gate=g["gate"])
+        keep = torch.arange(33, device="cuda") != 7
+        assert torch.equal(y[keep], y2[keep]) and torch.isnan(y2[7]).all()
+
+
+def test_graph_replays():
+    need_gpu()
+    from gated_delta_rule_gate_amd import block_norm, block_norm_bwd
+
+    g = on(make(300, 1032, BF16, BF16, True, "channel", True))
+    kw = dict(gate=g["gate"], residual=g["residual"], scale=g["scale"], next_weight=g["next_weight"])
+
+    def step():
+        y, z = block_norm(g["x"], g["weight"], **kw)
+        b = block_norm_bwd(g["x"], g["dy"], g["weight"], dz=g["dz"], **kw)
+        return [y, z] + [b[k] for k in sorted(b)]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for _ in range(3):
+        g["x"].copy_(torch.randn(300, 1032, device="cuda").to(BF16))
+        want = step()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want))
+
+
+def test_gradient_against_differences():
+    """Along a direction d, L(x + h d) - L(x - h d) over 2h differs from <dx, d> by h^2 / 6 of L's third
+    derivative and the losses' rounding over h. The third derivative along d is taken from the 64-bit
+    definition by differentiating three times, at its largest over the step."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import block_norm, block_norm_bwd
+
+    d = make(6, 64, FP32, FP32, True, "channel", True, seed=3)
+    g = on(d)
+    kw = dict(gate_act="silu", gate=g["gate"], residual=g["residual"], scale=g["scale"], next_weight=g["next_weight"])
+    got = block_norm_bwd(g["x"], g["dy"], g["weight"], dz=g["dz"], **kw)
+    h = 2.0 ** -7
+    for which in ("x", "gate", "residual"):
+        step = torch.from_numpy(np.random.Generator(np.random.PCG64(4)).standard_normal((6, 64)).astype(np.float32))
+
+        def loss(s):
+            m = dict(g, **{which: g[which] + s * h * step.cuda()})
+            y, z = block_norm(m["x"], m["weight"], **dict(kw, gate=m["gate"], residual=m["residual"]))
+            return ((y.double() * m["dy"].double()).sum() + (z.double() * m["dz"].double()).sum()).item()
+
+        def third(at):
+            u = torch.tensor(at, dtype=torch.float64, requires_grad=True)
+            m = {k: v.double() if isinstance(v, torch.Tensor) else v for k, v in d.items()}
+            m[which] = m[which] + u * step.double()
+            y, z = ref.norm(m["x"], m["weight"], m["gate"], "silu", m["residual"], m["scale"], m["next_weight"], True,
+                            1e-6, "rms")
+            L = (y * m["dy"]).sum() + (z * m["dz"]).sum()
+            for _ in range(3):
+                (L,) = torch.autograd.grad(L, u, create_graph=True)
+            return abs(L.item())
+
+        cubic = 2 * max(third(i * h / 4) for i in range(-4, 5))  # twice the largest of nine points
+        (sy, sz) = sizes(d, "silu", True, 1e-6, "rms")[1]
+        size = ((sy * d["dy"].double().abs()).sum() + (sz * d["dz"].double().abs()).sum()).item()
+        gsize = (sizes(d, "silu", True, 1e-6, "rms")[0]["d" + which] * step.double().abs()).sum().item()
+        n = count(64, 6, True)
+        tol = h * h / 6 * cubic + n * ref.ULP32 * (1.1 * size / h + gsize)
+        diff = (loss(1) - loss(-1)) / (2 * h)
+        along = (got["d" + which].double() * step.cuda().double()).sum().item()
+        assert abs(diff - along) <= tol, (which, diff, along, tol)
+
+
+def test_layer_as_used():
+    """A run of the operators as a layer calls them: l2-normalised q and k rows, linear attention (and KDA
+    on the same rows), the gated output norm, the residual stream with the next norm, against 64 bits."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import block_norm, chunk_kda, chunk_linear_attn
+
+    B, T, H, K = 2, 70, 2, 64
+    r = np.random.Generator(np.random.PCG64(5))
+    f = lambda *s: torch.from_numpy(r.standard_normal(s).astype(np.float32))  # noqa: E731
+    q, k, v, gate = (f(B, T, H, K) for _ in range(4))
+    g, w, w1, w2, x = -0.3 * f(B, T, H).abs(), 1 + 0.1 * f(K), 1 + 0.1 * f(H * K), 1 + 0.1 * f(H * K), f(B, T, H * K)
+    c = lambda t: t.cuda()  # noqa: E731
+    qn, kn = block_norm(c(q), norm="l2"), block_norm(c(k), norm="l2")
+    o, _ = chunk_linear_attn(qn, kn, c(v), c(g))
+    n = block_norm(o, c(w), gate=c(gate))
+    y, z = block_norm(n.view(B, T, H * K), c(w1), residual=c(x), scale=0.5, next_weight=c(w2))
+    d = lambda t: t.double()  # noqa: E731
+    qr, kr = (ref.norm(d(t), None, None, "sigmoid", None, 1.0, None, False, 1e-6, "l2")[0] for t in (q, k))
+    orf, _ = ref.attn(qr, kr, d(v), d(g), None)
+    nr = ref.norm(orf, d(w), d(gate), "sigmoid", None, 1.0, None, False, 1e-6, "rms")[0]
+    yr, zr = ref.norm(nr.reshape(B, T, H * K), d(w1), None, "sigmoid", d(x), 0.5, d(w2), True, 1e-6, "rms")
+    # attention rows whose terms cancel are small beside them: their norm takes that relative error on
+    osize, _ = ref.attn_sizes(qr, kr, d(v), d(g), None)
+    rel = (ref.roundings(K, K, T) + 3 * (K + 40)) * ref.ULP32 * osize.norm(dim=-1) / orf.norm(dim=-1)
+    worst = rel.max().item() + 3 * count(H * K, 1, True) * ref.ULP32
+    for got, want in ((y, yr), (z, zr)):
+        off = (got.cpu().double() - want).norm(dim=-1)
+        assert (off <= 4 * worst * (nr.reshape(B, T, H * K).norm(dim=-1) + want.norm(dim=-1))).all()
+    # the same rows through KDA: the norms feed it as they feed linear attention
+    A, dt = torch.zeros(H, device="cuda"), torch.zeros(H, K, device="cuda")
+    ok, _ = chunk_kda(qn, kn, c(v), c(f(B, T, H, K)), torch.sigmoid(c(f(B, T, H))), A_log=A, dt_bias=dt)
+    assert torch.isfinite(block_norm(ok, c(w), gate=c(gate))).all()

@@ -1,0 +1,173 @@
+"""What linear attention and the block norm refuse, without a GPU: status codes of the C entry points
+before any launch, workspace queries, and the Python checks."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+FAKE = ctypes.c_void_p(0x100000)  # aligned, never dereferenced: every call here is refused before a launch
+
+
+@pytest.fixture(scope="module")
+def L():
+    from gated_delta_rule_gate_amd import _binding, _linear, build
+
+    if not os.path.exists(_binding.LIB_PATH):
+        build.build()
+    return _linear._lib()
+
+
+def lin(**kw):
+    from gated_delta_rule_gate_amd._linear import LinearArgs
+
+    a = LinearArgs(1, 64, 2, 128, 128, 1, 0, 0, 0, 0.0)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def nrm(**kw):
+    from gated_delta_rule_gate_amd._linear import NormArgs
+
+    a = NormArgs(4, 128, 0, 0, 0, 0, 1.0, 1e-6)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+BAD = [
+    (dict(dtype=7), 3), (dict(decay=2), 5), (dict(K=44), 8), (dict(V=264), 8), (dict(K=0), 2), (dict(B=2), 2),
+    (dict(H=0), 2), (dict(H=4097), 2), (dict(H=3, Hk=2), 2), (dict(Hk=-1), 2), (dict(T=-1), 2), (dict(N=-1), 2),
+]
+
+
+@pytest.mark.parametrize("kw,code", BAD)
+def test_linear_arguments(L, kw, code):
+    a = lin(**kw)
+    assert L.kda_linear_recurrent_fwd(a, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, None) == code
+    assert L.kda_linear_chunk_fwd(a, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE, 1 << 40, None) == code
+    assert L.kda_linear_chunk_bwd(a, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE, FAKE, FAKE, FAKE, None, FAKE,
+                                  1 << 40, None) == code
+    if "B" not in kw:  # N != B is a packed query's right
+        assert L.kda_linear_chunk_workspace_bytes(a) == 0 and L.kda_linear_chunk_bwd_workspace_bytes(a) == 0
+
+
+def test_linear_pointers(L):
+    a, odd = lin(), ctypes.c_void_p(0x100004)
+    for i in (0, 1, 2, 3, 6):
+        p = [FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None]
+        p[i] = None
+        assert L.kda_linear_recurrent_fwd(a, *p, None) == 1, i
+        assert L.kda_linear_chunk_fwd(a, *p, FAKE, 1 << 40, None) == 1, i
+    for i in (0, 1, 2, 3, 4, 6, 7):
+        p = [FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None]
+        p[i] = odd
+        assert L.kda_linear_recurrent_fwd(a, *p, None) == 6, i
+        assert L.kda_linear_chunk_fwd(a, *p, FAKE, 1 << 40, None) == 6, i
+    for i in range(4):  # dq, dk, dv, dg are required
+        p = [FAKE] * 4
+        p[i] = None
+        assert L.kda_linear_chunk_bwd(a, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, *p, None, FAKE, 1 << 40,
+                                      None) == 1
+    assert L.kda_linear_recurrent_fwd(None, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, None) == 1
+    assert L.kda_linear_chunk_fwd(lin(B=2, N=2), FAKE, FAKE, FAKE, FAKE, None, FAKE, FAKE, None, FAKE, 1 << 40, None) == 2
+
+
+def test_linear_workspaces(L):
+    a = lin(T=8192, H=2)
+    need = L.kda_linear_chunk_workspace_bytes(a)
+    assert need > 0  # two heads: the sequence is cut into segments
+    for ws, n in ((None, need), (FAKE, need - 1)):
+        assert L.kda_linear_chunk_fwd(a, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, ws, n, None) == 7
+    assert L.kda_linear_chunk_fwd(a, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, ctypes.c_void_p(0x100010), need,
+                                  None) == 6
+    assert L.kda_linear_chunk_workspace_bytes(lin(T=64)) == 0
+    need = L.kda_linear_chunk_bwd_workspace_bytes(a)
+    for ws, n in ((None, need), (FAKE, need - 1)):
+        assert L.kda_linear_chunk_bwd(a, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE, FAKE, FAKE, FAKE, None, ws,
+                                      n, None) == 7
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), 2), (dict(D=0), 2), (dict(eps=-1.0), 2), (dict(eps=float("nan")), 2), (dict(dtype=2), 3),
+    (dict(dtype=1, res_dtype=0), 3), (dict(res_dtype=1), 3), (dict(norm=2), 5), (dict(gate_act=2), 5), (dict(D=100), 8),
+    (dict(D=16392), 8),
+])
+def test_norm_arguments(L, kw, code):
+    a = nrm(**kw)
+    assert L.kda_block_norm_fwd(a, FAKE, None, None, None, None, None, FAKE, None, None) == code
+    assert L.kda_block_norm_bwd(a, FAKE, None, None, None, None, None, FAKE, None, FAKE, None, None, None, None, None,
+                                FAKE, 1 << 40, None) == code
+
+
+def test_norm_pointers(L):
+    a, odd = nrm(), ctypes.c_void_p(0x100008)
+    assert L.kda_block_norm_fwd(a, None, None, None, None, None, None, FAKE, None, None) == 1
+    assert L.kda_block_norm_fwd(a, FAKE, None, None, None, None, None, None, None, None) == 1
+    for i in range(8):
+        p = [FAKE, None, None, None, None, None, FAKE, None]
+        p[i] = odd
+        assert L.kda_block_norm_fwd(a, *p, None) == 6
+    bwd = lambda dy, dz, dx, gate=None, dgate=None, dw=None, ws=FAKE, n=1 << 40: L.kda_block_norm_bwd(  # noqa: E731
+        a, FAKE, None, gate, None, None, None, dy, dz, dx, dgate, None, dw, None, None, ws, n, None)
+    assert bwd(None, None, FAKE) == 1 and bwd(FAKE, None, None) == 1 and bwd(FAKE, None, FAKE, gate=FAKE) == 1
+    assert bwd(FAKE, None, FAKE, dw=FAKE, ws=None) == 7 and bwd(FAKE, None, FAKE, dw=FAKE, n=16) == 7
+
+
+def test_python_checks():
+    from gated_delta_rule_gate_amd import block_norm, block_norm_bwd, chunk_linear_attn, recurrent_linear_attn
+
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    g = torch.zeros(1, 4, 2)
+    for f in (chunk_linear_attn, recurrent_linear_attn):
+        with pytest.raises(ValueError, match="must be on"):
+            f(q, q, q, g)
+        with pytest.raises(ValueError, match="multiple of q's heads"):
+            f(q, q, torch.zeros(1, 4, 3, 64, dtype=torch.bfloat16), g)
+        with pytest.raises(ValueError, match="dtype"):
+            f(q.half(), q.half(), q.half(), g)
+        with pytest.raises(ValueError, match="need batch 1"):
+            f(q.expand(2, 4, 2, 64), q, q.expand(2, 4, 2, 64), g, cu_seqlens=torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError, match="must be on"):
+        block_norm(q)
+    with pytest.raises(ValueError, match="norm must be"):
+        block_norm(q, norm="mean")
+    with pytest.raises(ValueError, match="gate_act"):
+        block_norm(q, gate_act="tanh")
+    with pytest.raises(ValueError, match="residual"):
+        block_norm(q.float(), residual=q)
+    with pytest.raises(ValueError, match="next_weight"):
+        block_norm(q, next_weight=torch.ones(64), next_norm=False)
+    with pytest.raises(ValueError, match="dy or dz"):
+        block_norm_bwd(q, None)
+
+
+@pytest.mark.gpu
+def test_python_checks_on_the_device():
+    from kda_testlib import need_gpu
+
+    need_gpu()
+    from gated_delta_rule_gate_amd import KdaError, block_norm, chunk_linear_attn, chunk_linear_attn_bwd
+
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(1, 4, 2, device="cuda")
+    with pytest.raises(RuntimeError, match="requires grad"):
+        chunk_linear_attn(q.clone().requires_grad_(True), q, q, g)
+    with pytest.raises(ValueError, match="g must be"):
+        chunk_linear_attn(q, q, q, g.double())
+    with pytest.raises(ValueError, match="contiguous"):
+        chunk_linear_attn(q.transpose(1, 2).contiguous().transpose(1, 2), q, q, g)
+    with pytest.raises(ValueError, match="out must be"):
+        chunk_linear_attn(q, q, q, g, out=q.float())
+    with pytest.raises(ValueError, match="final_state"):
+        chunk_linear_attn(q, q, q, g, final_state=torch.zeros(1, 2, 64, 32, device="cuda"))
+    with pytest.raises(ValueError, match="cu_seqlens must be"):
+        chunk_linear_attn(q, q, q, g, cu_seqlens=torch.zeros(2, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError, match="workspace"):
+        chunk_linear_attn_bwd(q, q, q, g, q, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(KdaError, match="UNSUPPORTED"):
+        z = torch.zeros(1, 4, 2, 12, dtype=torch.bfloat16, device="cuda")
+        chunk_linear_attn(z, z, q, g)
+    with pytest.raises(KdaError, match="UNSUPPORTED"):
+        block_norm(torch.zeros(3, 12, device="cuda"))
