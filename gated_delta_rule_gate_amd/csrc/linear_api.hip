@@ -152,7 +152,7 @@ extern "C" kda_status kda_linear_chunk_fwd(const kda_linear_args *a, const void 
   w.z = k;
   w.w = v;
   w.y = o;
-  w.Hx = w.Hz = qk_heads(a);
+  w.Hx = qk_heads(a);
   w.Hw = w.Hu = a->H;
   w.P = a->K;
   w.Q = a->V;
@@ -212,7 +212,7 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   w.y = shared ? static_cast<void *>(heads) : dq;
   w.y_f32 = shared;
   w.dot = dot_q;
-  w.Hx = w.Hz = a->H;
+  w.Hx = a->H;
   w.Hw = w.Hu = Hk;
   w.P = a->V;
   w.Q = a->K;
@@ -254,7 +254,7 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   r.z = q;
   r.w = d_o;
   r.y = dv;
-  r.Hx = r.Hz = Hk;
+  r.Hx = Hk;
   r.Hw = r.Hu = a->H;
   r.P = a->K;
   r.Q = a->V;

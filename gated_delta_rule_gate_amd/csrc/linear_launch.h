@@ -25,11 +25,11 @@ kda_status report_hip(hipError_t e);
 //     o:  x = q,   z = k,   w = v    S = h           dq: x = d_o, z = v,   w = k   S = h^T
 //     dv: x = k,   z = q,   w = d_o  S = dh, reverse  dk: x = v,   z = d_o, w = q   S = dh^T, reverse
 struct LinearWalk {
-  const void *x, *z, *w;  // [rows, Hx, P], [rows, Hz, P], [rows, Hw, Q]
+  const void *x, *z, *w;  // [rows, Hx, P], [rows, Hx, P], [rows, Hw, Q]
   const void *u;          // [rows, Hu, Q] or null: partner of the row dots
   void *y;                // [rows, H, Q]
   float *dot;             // [ncb][H][rows]: y_r . u_r in fp32, before y is rounded (with u)
-  int Hx, Hz, Hw, Hu;
+  int Hx, Hw, Hu;
   bool y_f32;             // y is fp32 whatever the type (a head's part, summed over heads later)
   const float *g;
   bool g_head;            // g [H] instead of [rows, H]

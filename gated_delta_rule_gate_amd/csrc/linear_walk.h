@@ -60,75 +60,100 @@ __device__ __forceinline__ f32x4_t mma_parts(const bf16x8_t (&a)[NA], const bf16
   return acc;
 }
 
-template <typename T, int PT_, int NW_, int OPL_>
+// Geometry of one walk. MODE 0: the whole walk; 1: the state only, left at the
+// boundary behind the segment.
+template <typename T, int PT_, int NW_, int OPL_, int MODE_>
 struct WalkCfg {
   static constexpr bool F32 = sizeof(T) == 4;
-  static constexpr int PT = PT_, NW = NW_, OPL = OPL_;
+  static constexpr int PT = PT_, NW = NW_, OPL = OPL_, MODE = MODE_;
   static constexpr int IN = F32 ? 3 : 1;  // bf16 parts of an input
   static constexpr int C = (F32 || PT == 256) ? 32 : 64;
   static constexpr int NC = C / 16, KS = C / 32, PS = PT / 32, NT = PT / 16, QT = 16 * NW, THREADS = 64 * NW;
-  // row strides: 16 bytes past a multiple of 256, so the 16 rows of an operand read lie in 16 bank groups
-  static constexpr int LDX = PT + 8, LDW = QT + 8, LDP = C + 8, LDY = QT + 4;
+  // row strides: 16 bytes past a multiple of 128, so the 16 rows of an operand read start in 16 bank groups
+  static constexpr int LDX = PT + 8, LDW = QT + 8, LDP = C + 8;
   static constexpr int XPL = C * LDX, WPL = C * LDW, PPL = C * LDP;  // elements of one part
-  static constexpr unsigned oX = 0, oZ = oX + 2u * IN * XPL, oW = oZ + 2u * IN * XPL, oP = oW + 2u * IN * WPL,
-                            oY = oP + 2u * OPL * PPL, oTab = oY + 4u * C * LDY, oRed = oTab + 4u * 4 * 64 + 16,
-                            total = oRed + 4u * 2 * NW + 16;
+  static constexpr unsigned nX = MODE == 0 ? 2u * IN * XPL : 0u, nZ = 2u * IN * XPL, nW = 2u * IN * WPL;
+  static constexpr unsigned rows = nX + nZ + nW;  // one chunk's rows
+  static constexpr unsigned nP = MODE == 0 ? 2u * OPL * PPL : 0u;
+  static constexpr unsigned tab = 4u * (4 * 64 + 4);  // hi, lo, a, c of every row, and the chunk's decay
+  static constexpr unsigned red = 4u * NW * 64 + 64;  // row dots of every wave, and its part of <h, dh>
+  static constexpr unsigned fixed = nP + 2 * tab + red;
+  // two chunks' rows where they fit: the next chunk is written while this one is read
+  static constexpr int NBUF = 2 * rows + fixed <= 160 * 1024 ? 2 : 1;
+  static constexpr unsigned oP = NBUF * rows, oTab = oP + nP, oRed = oTab + 2 * tab, total = oRed + red;
+  static_assert(total <= 160 * 1024, "LDS");
 };
 
-// Rows fetched into registers, written to LDS as bf16 parts.
+// Rows of one chunk on their way to LDS: 16-byte loads at offsets that do not
+// change from chunk to chunk (the resource's base does), columns past the
+// width at an offset that reads zeros, rows past the chunk past its end.
 template <typename T, int NT, int ROWS, int COLS>
-struct PartsFetch : RowsFetch<T, NT, ROWS, COLS> {
-  using Base = RowsFetch<T, NT, ROWS, COLS>;
-  __device__ __forceinline__ void put_parts(bf16_t *s, int lds, int plane) const {
-    if constexpr (sizeof(T) == 2) {
-      Base::put(s, lds);
-    } else {
+struct RowsMove {
+  static constexpr int EPV = 16 / (int)sizeof(T);
+  static constexpr int VPR = COLS / EPV, NV = ROWS * VPR, IT = (NV + NT - 1) / NT;
+  static_assert(NV % NT == 0 && NT % VPR == 0, "whole rows per round");
+  static constexpr int RPI = NT / VPR;  // rows of one round
+
+  static __device__ __forceinline__ uint32_t lane_offset(int tid, int64_t ldg, int ncol) {
+    const int r = tid / VPR, c = (tid % VPR) * EPV;
+    return c < ncol ? (uint32_t)((r * ldg + c) * (int64_t)sizeof(T)) : kOffNone;
+  }
+  static __device__ __forceinline__ int lds_offset(int tid, int lds) { return (tid / VPR) * lds + (tid % VPR) * EPV; }
+  // rows [0, L) from base; `round` is RPI rows in bytes
+  static __device__ __forceinline__ void load(u32x4_t (&buf)[IT], const T *base, int64_t ldg, int L, int ncol,
+                                              uint32_t off, uint32_t round) {
+    const auto rs = tile_rsrc(base, (uint32_t)(((int64_t)(L - 1) * ldg + ncol) * (int64_t)sizeof(T)));
 #pragma unroll
-      for (int it = 0; it < Base::IT; ++it) {
-        const int idx = it * NT + tid_opaque();
-        const int r = idx / Base::VPR, c = (idx % Base::VPR) * 4;
-        if (Base::NV % NT == 0 || idx < Base::NV) {
-          f32x4_t x = __builtin_bit_cast(f32x4_t, this->buf[it]);
+    for (int it = 0; it < IT; ++it)
+      buf[it] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(off + it * round), 0, 0));
+  }
+  static __device__ __forceinline__ void put(const u32x4_t (&buf)[IT], bf16_t *s, int lds, int plane) {
 #pragma unroll
-          for (int pl = 0; pl < 3; ++pl) {
-            const bf16x4_t h = to_bf16x4(x);
-            *reinterpret_cast<bf16x4_t *>(s + pl * plane + r * lds + c) = h;
-            x -= to_f32x4(h);
-          }
+    for (int it = 0; it < IT; ++it) {
+      if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<u32x4_t *>(s + it * RPI * lds) = buf[it];
+      } else {
+        f32x4_t x = __builtin_bit_cast(f32x4_t, buf[it]);
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) {
+          const bf16x4_t h = to_bf16x4(x);
+          *reinterpret_cast<bf16x4_t *>(s + pl * plane + it * RPI * lds) = h;
+          x -= to_f32x4(h);
         }
       }
     }
   }
 };
 
-// MODE 0: the whole walk; 1: the state only, left at the boundary behind the segment.
+// Per chunk, two periods between barriers. In the first, the waves share out
+// the causal 16 x 16 blocks of the scores, write them decayed to LDS, and each
+// multiplies every row with its own columns of the state. In the second each
+// adds scores times its columns of w, stores its columns of y, updates its
+// columns of the state, and writes its share of the next chunk's rows (loaded a
+// whole chunk earlier) to the other LDS buffer; one wave forms the next chunk's
+// decays. Products that give y are taken transposed, so that a lane holds four
+// neighbouring columns of one row: scores and y leave in 8-byte pieces.
 template <typename T, int PT, int NW, bool REV, int OPL, int MODE>
 __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
-  using F = WalkCfg<T, PT, NW, OPL>;
-  constexpr int C = F::C, NC = F::NC, KS = F::KS, IN = F::IN, QT = F::QT;
+  using F = WalkCfg<T, PT, NW, OPL, MODE>;
+  constexpr int C = F::C, NC = F::NC, KS = F::KS, IN = F::IN, QT = F::QT, NB = NC * (NC + 1) / 2;
+  using MX = RowsMove<T, F::THREADS, C, PT>;
+  using MW = RowsMove<T, F::THREADS, C, QT>;
   extern __shared__ __align__(16) char smem[];
-  bf16_t *sX = reinterpret_cast<bf16_t *>(smem + F::oX);
-  bf16_t *sZ = reinterpret_cast<bf16_t *>(smem + F::oZ);
-  bf16_t *sW = reinterpret_cast<bf16_t *>(smem + F::oW);
-  bf16_t *sP = reinterpret_cast<bf16_t *>(smem + F::oP);
-  float *sY = reinterpret_cast<float *>(smem + F::oY);
-  float *sHi = reinterpret_cast<float *>(smem + F::oTab), *sLo = sHi + 64, *sA = sHi + 128, *sC = sHi + 192;
-  float *sDec = sHi + 256;
-  float *sRed = reinterpret_cast<float *>(smem + F::oRed);
 
   // Workgroups that read the same q/k rows (a group's heads, a head's column
   // blocks) go to one XCD, next to each other: ids are dealt to the eight XCDs
-  // in turn.
+  // in turn. Whole segments come before the sequences' first, which may be short.
   const int ncb = (p.Q + QT - 1) / QT;
   const int G = p.H / p.Hk, U = G * ncb;
   const int xcd = blockIdx.x & 7, sl = blockIdx.x >> 3;
   const int64_t unit = (int64_t)(sl / U) * 8 + xcd;
   const int member = sl % U;
-  const int64_t item = unit / p.Hk;
+  const int64_t n_items = p.N + (p.seg ? ((int64_t)p.B * p.T) / p.seg : 0);
+  const int64_t item = n_items - 1 - unit / p.Hk;
   const int h = (int)(unit % p.Hk) * G + member / ncb, cb = member % ncb;
   SegLoc sg;
-  const int64_t n_items = p.N + (p.seg ? ((int64_t)p.B * p.T) / p.seg : 0);
-  if (item >= n_items || !locate_segment(p, item, REV, sg)) return;
+  if (item < 0 || !locate_segment(p, item, REV, sg)) return;
   if (MODE == 1 && sg.out < 0) return;  // nothing follows the last segment
 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
@@ -139,7 +164,7 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
   const int64_t frag = ((int64_t)h * ncb + cb) * (PT * QT) + ((int64_t)wave * F::NT * 64 + lane) * 4;
   const int64_t fragH = (int64_t)p.H * ncb * (PT * QT);  // elements of one boundary
 
-  // ---- the state at the segment's start ----
+  // ---- the state at the segment's start: rows 16t + 4 grp + e of column q ----
   f32x4_t S[F::NT];
   const int64_t sbase = ((int64_t)sg.n * p.H + h) * P * Q;
   if (MODE == 0 && sg.in >= 0) {
@@ -166,61 +191,107 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
     }
   }
 
+  // ---- fixed offsets of this thread ----
+  const int64_t ldx = (int64_t)p.Hx * P, ldw = (int64_t)p.Hw * Q;
+  const uint32_t gx = MX::lane_offset(tid, ldx, P), gw = MW::lane_offset(tid, ldw, ncol);
+  const uint32_t rx = (uint32_t)(MX::RPI * ldx * (int64_t)sizeof(T)), rw = (uint32_t)(MW::RPI * ldw * (int64_t)sizeof(T));
+  const int px = MX::lds_offset(tid, F::LDX), pw = MW::lds_offset(tid, F::LDW);
+  const int ax = l16 * F::LDX;                // a row of x or z as an operand
+  const int tz = cfrag_lane_off(F::LDX), tw = cfrag_lane_off(F::LDW) + 16 * wave;
+  const int ap = l16 * F::LDP + 4 * grp;      // a row of the scores
+  bf16_t *const sP = reinterpret_cast<bf16_t *>(smem + F::oP);
+  auto rows_at = [&](int buf) { return reinterpret_cast<bf16_t *>(smem + (F::NBUF == 2 && buf ? F::rows : 0u)); };
+  auto tab_at = [&](int buf) { return reinterpret_cast<float *>(smem + F::oTab + (buf ? F::tab : 0u)); };
+  float *const sRed = reinterpret_cast<float *>(smem + F::oRed), *const sAnc = sRed + NW * 64;
+
+  const T *const xh = reinterpret_cast<const T *>(p.x) + (int64_t)(h / (p.H / p.Hx)) * P;
+  const T *const zh = reinterpret_cast<const T *>(p.z) + (int64_t)(h / (p.H / p.Hx)) * P;
+  const T *const wh = reinterpret_cast<const T *>(p.w) + (int64_t)(h / (p.H / p.Hw)) * Q + col0;
+  // y and its partner u: four neighbouring columns of row l16 of each 16
+  const int64_t ldu = (int64_t)p.Hu * Q, ldy = (int64_t)p.H * Q;
+  const T *const uh0 = reinterpret_cast<const T *>(p.u) + (int64_t)(h / (p.H / p.Hu)) * Q + col0;
+  const bool yin = 16 * wave + 4 * grp < ncol, y32 = sizeof(T) == 4 || p.y_f32;
+  const int ysz = y32 ? 4 : 2;
+  const uint32_t gu = yin ? (uint32_t)((l16 * ldu + 16 * wave + 4 * grp) * (int64_t)sizeof(T)) : kOffNone;
+  const uint32_t gy = yin ? (uint32_t)((l16 * ldy + 16 * wave + 4 * grp) * ysz) : kOffNone;
+  const uint32_t ru = (uint32_t)(16 * ldu * (int64_t)sizeof(T)), ry = (uint32_t)(16 * ldy * ysz);
   const float yscale = REV ? 1.f : p.scale, wscale = REV ? p.scale : 1.f;
   const int nch = (int)((sg.hi - sg.lo + C - 1) / C);
-  PartsFetch<T, F::THREADS, C, PT> fx, fz;
-  PartsFetch<T, F::THREADS, C, QT> fw;
+  u32x4_t fx[MODE == 0 ? MX::IT : 1], fz[MX::IT], fw[MW::IT];
   float fg = 0.f;
-  double total = 0.0;  // log2 decay of the whole segment (wave 0)
-  auto fetch = [&](int c) {
-    const int64_t t0 = sg.lo + (int64_t)c * C;
+  double total = 0.0;  // log2 decay of the whole segment (the decays' wave)
+  constexpr int DW = NW - 1;  // the wave that forms the decays
+  auto chunk_of = [&](int cc) { return REV ? nch - 1 - cc : cc; };
+  auto fetch = [&](int cc) {
+    const int64_t t0 = sg.lo + (int64_t)chunk_of(cc) * C;
     const int L = (int)min((int64_t)C, sg.hi - t0);
-    if constexpr (MODE == 0)
-      fx.fetch(reinterpret_cast<const T *>(p.x) + (t0 * p.Hx + h / (p.H / p.Hx)) * P, (int64_t)p.Hx * P, L, P);
-    fz.fetch(reinterpret_cast<const T *>(p.z) + (t0 * p.Hz + h / (p.H / p.Hz)) * P, (int64_t)p.Hz * P, L, P);
-    fw.fetch(reinterpret_cast<const T *>(p.w) + (t0 * p.Hw + h / (p.H / p.Hw)) * Q + col0, (int64_t)p.Hw * Q, L, ncol);
-    if (wave == 0) fg = lane < L ? (p.g_head ? p.g[h] : p.g[(t0 + lane) * p.H + h]) : 0.f;
+    if constexpr (MODE == 0) MX::load(fx, xh + t0 * ldx, ldx, L, P, gx, rx);
+    MX::load(fz, zh + t0 * ldx, ldx, L, P, gx, rx);
+    MW::load(fw, wh + t0 * ldw, ldw, L, ncol, gw, rw);
+    if (wave == DW) {
+      if (p.g_head) {
+        fg = lane < L ? p.g[h] : 0.f;
+      } else {
+        const auto rs = tile_rsrc(p.g + t0 * p.H + h, (uint32_t)(((L - 1) * p.H + 1) * 4));
+        fg = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, (int)(lane * p.H * 4), 0, 0));
+      }
+    }
   };
-  if (nch > 0) fetch(REV ? nch - 1 : 0);
+  auto put = [&](int buf) {
+    bf16_t *s = rows_at(buf);
+    if constexpr (MODE == 0) MX::put(fx, s + px, F::LDX, F::XPL);
+    MX::put(fz, s + F::nX / 2 + px, F::LDX, F::XPL);
+    MW::put(fw, s + (F::nX + F::nZ) / 2 + pw, F::LDW, F::WPL);
+  };
+  auto decays = [&](int buf) {
+    if (wave != DW) return;
+    // b in fp64; a decay below 2^-160 is none at all and counts as 2^-32768:
+    // differences across it give zero, those beyond it stay exact
+    double b = (double)fg * 1.4426950408889634073599;
+    if (b <= -160.0) b = -32768.0;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double up = __shfl_up(b, off);
+      if (lane >= off) b += up;
+    }
+    const double bl = __shfl(b, 63);
+    const double hi = rint(b);
+    const float first = fast_exp2((float)b), rest = fast_exp2((float)(bl - b));
+    float *t = tab_at(buf);
+    t[lane] = (float)hi;
+    t[64 + lane] = (float)(b - hi);
+    t[128 + lane] = REV ? rest : first;
+    t[192 + lane] = REV ? first * p.scale : rest;
+    if (lane == 0) t[256] = fast_exp2((float)bl);
+    total += bl;
+  };
 
+  if (nch > 0) {
+    fetch(0);
+    put(0);
+    decays(0);
+    if (nch > 1) fetch(1);
+  }
   if constexpr (MODE == 0) {
     // the blocks of the scores beyond the triangle stay zero
     for (int i = tid; i < OPL * F::PPL / 2; i += F::THREADS) reinterpret_cast<unsigned *>(sP)[i] = 0u;
   }
+  __syncthreads();
 
   for (int cc = 0; cc < nch; ++cc) {
-    const int c = REV ? nch - 1 - cc : cc;
-    const int64_t t0 = sg.lo + (int64_t)c * C;
+    const int64_t t0 = sg.lo + (int64_t)chunk_of(cc) * C;
     const int L = (int)min((int64_t)C, sg.hi - t0);
+    const int buf = cc & 1;
+    const bf16_t *const sX = rows_at(buf), *const sZ = sX + F::nX / 2, *const sW = sZ + F::nZ / 2;
+    const float *const tab = tab_at(buf);
+    const bool anchored = MODE == 0 && p.ckpt && t0 + L < sg.e && (t0 + L - sg.a) % p.anchor == 0;
 
-    // ---- this chunk's rows and decays to LDS ----
-    if constexpr (MODE == 0) fx.put_parts(sX, F::LDX, F::XPL);
-    fz.put_parts(sZ, F::LDX, F::XPL);
-    fw.put_parts(sW, F::LDW, F::WPL);
-    if (wave == 0) {
-      // b in fp64; a decay below 2^-160 is none at all and counts as 2^-32768:
-      // differences across it give zero, those beyond it stay exact
-      double b = (double)fg * 1.4426950408889634073599;
-      if (b <= -160.0) b = -32768.0;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const double up = __shfl_up(b, off);
-        if (lane >= off) b += up;
-      }
-      const double bl = __shfl(b, 63);
-      const double hi = rint(b);
-      const float first = fast_exp2((float)b), rest = fast_exp2((float)(bl - b));
-      sHi[lane] = (float)hi;
-      sLo[lane] = (float)(b - hi);
-      sA[lane] = REV ? rest : first;
-      sC[lane] = REV ? first * p.scale : rest;
-      if (lane == 0) sDec[0] = fast_exp2((float)bl);
-      total += bl;
-    }
-    if (MODE == 0 && REV && p.ckpt) {  // <h, dh> behind this chunk
-      const int64_t end = t0 + L;
-      if (end < sg.e && (end - sg.a) % p.anchor == 0) {
-        const float *src = p.ckpt + (end / p.anchor) * fragH + frag;
+    f32x4_t y[NC];
+    bf16x4_t uh[NC];
+    f32x4_t uf[NC];
+    if constexpr (MODE == 0) {
+      if (REV && anchored) {  // <h, dh> behind this chunk
+        const float *src = p.ckpt + ((t0 + L) / p.anchor) * fragH + frag;
         float d = 0.f;
 #pragma unroll
         for (int t = 0; t < F::NT; ++t) {
@@ -230,56 +301,53 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
         }
 #pragma unroll
         for (int off = 32; off > 0; off >>= 1) d += __shfl_xor(d, off);
-        if (lane == 0) sRed[wave] = d;
+        if (lane == 0) sAnc[wave] = d;
       }
-    }
-    __syncthreads();
-    if (MODE == 0 && REV && p.ckpt && tid == 0) {
-      const int64_t end = t0 + L;
-      if (end < sg.e && (end - sg.a) % p.anchor == 0) {
-        float d = 0.f;
+      if (p.u) {  // the row dots' partners: four columns of a row a lane
+        const auto rs = tile_rsrc(uh0 + t0 * ldu, (uint32_t)(((L - 1) * ldu + ncol) * (int64_t)sizeof(T)));
 #pragma unroll
-        for (int w = 0; w < NW; ++w) d += sRed[w];
-        p.anchor_dot[((end / p.anchor) * p.H + h) * ncb + cb] = d;
+        for (int i = 0; i < NC; ++i) {
+          if constexpr (sizeof(T) == 2)
+            uh[i] = __builtin_bit_cast(bf16x4_t, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)(gu + i * ru), 0, 0));
+          else
+            uf[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(gu + i * ru), 0, 0));
+        }
       }
-    }
-    if (cc + 1 < nch) fetch(REV ? c - 1 : c + 1);
-
-    f32x4_t y[NC];
-    if constexpr (MODE == 0) {
-      // ---- scores of the causal 16 x 16 blocks, dealt to the waves ----
+      // ---- scores of the causal blocks: lane has row l16 of x, four rows of z ----
 #pragma unroll
-      for (int b0 = 0; b0 < NC * (NC + 1) / 2; b0 += NW) {
+      for (int b0 = 0; b0 < NB; b0 += NW) {
         const int blk = b0 + wave;
-        if (blk < NC * (NC + 1) / 2) {
+        if (blk < NB) {
           const int i = blk < 1 ? 0 : (blk < 3 ? 1 : (blk < 6 ? 2 : 3)), j = blk - i * (i + 1) / 2;
           const int ri = REV ? j : i, cj = REV ? i : j;
+          const bf16_t *xs = sX + 16 * ri * F::LDX + ax + 8 * grp, *zs = sZ + 16 * cj * F::LDX + ax + 8 * grp;
           f32x4_t acc = zero4();
 #pragma unroll
           for (int s = 0; s < F::PS; ++s) {
             bf16x8_t a[IN], bz[IN];
 #pragma unroll
             for (int pl = 0; pl < IN; ++pl) {
-              a[pl] = *reinterpret_cast<const bf16x8_t *>(sX + pl * F::XPL + (16 * ri + l16) * F::LDX + 32 * s + 8 * grp);
-              bz[pl] = *reinterpret_cast<const bf16x8_t *>(sZ + pl * F::XPL + (16 * cj + l16) * F::LDX + 32 * s + 8 * grp);
+              a[pl] = *reinterpret_cast<const bf16x8_t *>(xs + pl * F::XPL + 32 * s);
+              bz[pl] = *reinterpret_cast<const bf16x8_t *>(zs + pl * F::XPL + 32 * s);
             }
-            acc = mma_parts(a, bz, acc);
+            acc = mma_parts(bz, a, acc);
           }
-          const f32x4_t hr = *reinterpret_cast<const f32x4_t *>(sHi + 16 * ri + 4 * grp);
-          const f32x4_t lr = *reinterpret_cast<const f32x4_t *>(sLo + 16 * ri + 4 * grp);
-          const float hs = sHi[16 * cj + l16], ls = sLo[16 * cj + l16];
+          const float hr = tab[16 * ri + l16], lr = tab[64 + 16 * ri + l16];
+          const f32x4_t hs = *reinterpret_cast<const f32x4_t *>(tab + 16 * cj + 4 * grp);
+          const f32x4_t ls = *reinterpret_cast<const f32x4_t *>(tab + 64 + 16 * cj + 4 * grp);
+          f32x4_t v;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float d = REV ? (hs - hr[e]) + (ls - lr[e]) : (hr[e] - hs) + (lr[e] - ls);
-            const int r = 4 * grp + e;
-            const bool keep = i != j || (REV ? l16 >= r : l16 <= r);
-            float v = keep ? acc[e] * fast_exp2(d) * wscale : 0.f;
+            const float d = REV ? (hs[e] - hr) + (ls[e] - lr) : (hr - hs[e]) + (lr - ls[e]);
+            const bool keep = i != j || (REV ? 4 * grp + e >= l16 : 4 * grp + e <= l16);
+            v[e] = keep ? acc[e] * fast_exp2(d) * wscale : 0.f;
+          }
+          bf16_t *dst = sP + 16 * ri * F::LDP + 16 * cj + ap;
 #pragma unroll
-            for (int pl = 0; pl < OPL; ++pl) {
-              const bf16_t hv = static_cast<bf16_t>(v);
-              sP[pl * F::PPL + (16 * ri + r) * F::LDP + 16 * cj + l16] = hv;
-              v -= static_cast<float>(hv);
-            }
+          for (int pl = 0; pl < OPL; ++pl) {
+            const bf16x4_t part = to_bf16x4(v);
+            *reinterpret_cast<bf16x4_t *>(dst + pl * F::PPL) = part;
+            if (pl + 1 < OPL) v -= to_f32x4(part);
           }
         }
       }
@@ -297,15 +365,21 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
           bf16x8_t a[IN];
 #pragma unroll
           for (int pl = 0; pl < IN; ++pl) {
-            const bf16_t *src = sX + pl * F::XPL + (16 * i + l16) * F::LDX + 32 * s + 4 * grp;
+            const bf16_t *src = sX + pl * F::XPL + 16 * i * F::LDX + ax + 32 * s + 4 * grp;
             a[pl] = join8(*reinterpret_cast<const bf16x4_t *>(src), *reinterpret_cast<const bf16x4_t *>(src + 16));
           }
-          y[i] = mma_parts(a, sb, y[i]);
+          y[i] = mma_parts(sb, a, y[i]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < NC; ++i) y[i] *= *reinterpret_cast<const f32x4_t *>(sA + 16 * i + 4 * grp);
+      for (int i = 0; i < NC; ++i) y[i] *= tab[128 + 16 * i + l16];
       __syncthreads();
+      if (REV && anchored && tid == 0) {
+        float d = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) d += sAnc[w];
+        p.anchor_dot[(((t0 + L) / p.anchor) * p.H + h) * ncb + cb] = d;
+      }
     }
 
     // ---- w as an operand, and decayed to the chunk's end in three parts ----
@@ -315,12 +389,12 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
       float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int pl = IN - 1; pl >= 0; --pl) {
-        wf[s][pl] = load_frag32(sW + pl * F::WPL, F::LDW, 32 * s, 16 * wave);
+        wf[s][pl] = load_frag32_at(sW + pl * F::WPL + 32 * s * F::LDW, F::LDW, tw);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] += static_cast<float>(wf[s][pl][e]);
       }
-      const f32x4_t c0 = *reinterpret_cast<const f32x4_t *>(sC + 32 * s + 4 * grp);
-      const f32x4_t c1 = *reinterpret_cast<const f32x4_t *>(sC + 32 * s + 16 + 4 * grp);
+      const f32x4_t c0 = *reinterpret_cast<const f32x4_t *>(tab + 192 + 32 * s + 4 * grp);
+      const f32x4_t c1 = *reinterpret_cast<const f32x4_t *>(tab + 192 + 32 * s + 16 + 4 * grp);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         x[e] *= c0[e];
@@ -330,7 +404,9 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
     }
 
     if constexpr (MODE == 0) {
-      // ---- y += scores w; staged for whole-row stores ----
+      // ---- y += scores w, out ----
+      const auto rs = tile_rsrc(reinterpret_cast<char *>(p.y) + ((t0 * p.H + h) * Q + col0) * ysz,
+                                (uint32_t)(((L - 1) * ldy + ncol) * ysz));
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
 #pragma unroll
@@ -338,18 +414,28 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
           bf16x8_t a[OPL];
 #pragma unroll
           for (int pl = 0; pl < OPL; ++pl) {
-            const bf16_t *src = sP + pl * F::PPL + (16 * i + l16) * F::LDP + 32 * s + 4 * grp;
+            const bf16_t *src = sP + pl * F::PPL + 16 * i * F::LDP + ap + 32 * s;
             a[pl] = join8(*reinterpret_cast<const bf16x4_t *>(src), *reinterpret_cast<const bf16x4_t *>(src + 16));
           }
-          y[i] = mma_parts(a, wf[s], y[i]);
+          y[i] = mma_parts(wf[s], a, y[i]);
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sY[(16 * i + 4 * grp + e) * F::LDY + 16 * wave + l16] = y[i][e] * yscale;
+        y[i] *= yscale;
+        if (y32)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y[i]), rs, (int)(gy + i * ry), 0, 0);
+        else
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, to_bf16x4(y[i])), rs, (int)(gy + i * ry), 0, 0);
+        if (p.u) {  // this wave's columns of the row's dot
+          const f32x4_t u = sizeof(T) == 2 ? to_f32x4(uh[i]) : uf[i];
+          float d = (y[i][0] * u[0] + y[i][1] * u[1]) + (y[i][2] * u[2] + y[i][3] * u[3]);
+          d += __shfl_xor(d, 16);
+          d += __shfl_xor(d, 32);
+          if (grp == 0) sRed[wave * 64 + 16 * i + l16] = d;  // columns past the width read u as zero
+        }
       }
     }
 
     // ---- the state ----
-    const float dec = sDec[0];
+    const float dec = tab[256];
 #pragma unroll
     for (int t = 0; t < F::NT; ++t) {
       S[t] *= dec;
@@ -357,58 +443,29 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
       for (int s = 0; s < KS; ++s) {
         bf16x8_t a[IN];
 #pragma unroll
-        for (int pl = 0; pl < IN; ++pl) a[pl] = load_frag32(sZ + pl * F::XPL, F::LDX, 32 * s, 16 * t);
+        for (int pl = 0; pl < IN; ++pl) a[pl] = load_frag32_at(sZ + pl * F::XPL + 32 * s * F::LDX + 16 * t, F::LDX, tz);
         S[t] = mma_parts(a, wc[s], S[t]);
       }
     }
-    if (MODE == 0 && !REV && p.ckpt) {
-      const int64_t end = t0 + L;
-      if (end < sg.e && (end - sg.a) % p.anchor == 0) {
-        float *dst = p.ckpt + (end / p.anchor) * fragH + frag;
+    if (MODE == 0 && !REV && anchored) {
+      float *dst = p.ckpt + ((t0 + L) / p.anchor) * fragH + frag;
 #pragma unroll
-        for (int t = 0; t < F::NT; ++t) *reinterpret_cast<f32x4_t *>(dst + t * 256) = S[t];
-      }
+      for (int t = 0; t < F::NT; ++t) *reinterpret_cast<f32x4_t *>(dst + t * 256) = S[t];
+    }
+
+    // ---- the next chunk's rows ----
+    if constexpr (F::NBUF == 1) __syncthreads();
+    if (cc + 1 < nch) {
+      put(buf ^ 1);
+      decays(buf ^ 1);
+      if (cc + 2 < nch) fetch(cc + 2);
     }
     __syncthreads();
-
-    if constexpr (MODE == 0) {
-      // ---- rows out, eight columns a thread, and their dots with u ----
-      constexpr int TPR = QT / 8;
+    if (MODE == 0 && p.u && tid < L) {  // behind the barrier: every wave's part is there
+      float d = 0.f;
 #pragma unroll
-      for (int i0 = 0; i0 < C * TPR; i0 += F::THREADS) {
-        const int idx = i0 + tid, r = idx / TPR, cq = 8 * (idx % TPR);
-        const bool ok = r < L && cq < ncol;
-        float v[8];
-        *reinterpret_cast<f32x4_t *>(v) = *reinterpret_cast<const f32x4_t *>(sY + r * F::LDY + cq);
-        *reinterpret_cast<f32x4_t *>(v + 4) = *reinterpret_cast<const f32x4_t *>(sY + r * F::LDY + cq + 4);
-        const int64_t at = ((t0 + r) * p.H + h) * Q + col0 + cq;
-        if (ok) {
-          if constexpr (sizeof(T) == 2) {
-            if (p.y_f32) {
-              float *dst = reinterpret_cast<float *>(p.y) + at;
-              *reinterpret_cast<f32x4_t *>(dst) = *reinterpret_cast<const f32x4_t *>(v);
-              *reinterpret_cast<f32x4_t *>(dst + 4) = *reinterpret_cast<const f32x4_t *>(v + 4);
-            } else {
-              *reinterpret_cast<bf16x8_t *>(reinterpret_cast<bf16_t *>(p.y) + at) = pack_bf16x8(v);
-            }
-          } else {
-            float *dst = reinterpret_cast<float *>(p.y) + at;
-            *reinterpret_cast<f32x4_t *>(dst) = *reinterpret_cast<const f32x4_t *>(v);
-            *reinterpret_cast<f32x4_t *>(dst + 4) = *reinterpret_cast<const f32x4_t *>(v + 4);
-          }
-        }
-        if (p.u) {
-          float d = 0.f;
-          if (ok) {
-            const T *us = reinterpret_cast<const T *>(p.u) + ((t0 + r) * p.Hu + h / (p.H / p.Hu)) * Q + col0 + cq;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d += v[e] * to_f32(us[e]);
-          }
-#pragma unroll
-          for (int off = TPR / 2; off > 0; off >>= 1) d += __shfl_xor(d, off);
-          if (ok && cq == 0) p.dot[((int64_t)cb * p.H + h) * rows + t0 + r] = d;
-        }
-      }
+      for (int w = 0; w < NW; ++w) d += sRed[w * 64 + tid];
+      p.dot[((int64_t)cb * p.H + h) * rows + t0 + tid] = d;
     }
   }
 
@@ -416,7 +473,7 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
     float *dst = p.seg_state + sg.out * fragH + frag;
 #pragma unroll
     for (int t = 0; t < F::NT; ++t) *reinterpret_cast<f32x4_t *>(dst + t * 256) = S[t];
-    if (tid == 0 && cb == 0) p.seg_decay[sg.out * p.H + h] = total;
+    if (wave == DW && lane == 0 && cb == 0) p.seg_decay[sg.out * p.H + h] = total;
   } else if (sg.out < 0) {
     if (p.sT && !(nch == 0 && p.sT == p.s0)) {
 #pragma unroll
@@ -452,7 +509,7 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
 
 template <typename T, int PT, int NW, bool REV, int OPL, int MODE>
 hipError_t launch_one(const LinearWalk &p, hipStream_t st) {
-  using F = WalkCfg<T, PT, NW, OPL>;
+  using F = WalkCfg<T, PT, NW, OPL, MODE>;
   auto kern = linear_walk_kernel<T, PT, NW, REV, OPL, MODE>;
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)F::total);
