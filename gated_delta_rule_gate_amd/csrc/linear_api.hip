@@ -89,7 +89,6 @@ kda::LinearWalk walk_base(const kda_linear_args *a, const float *g, const int32_
   w.Hk = qk_heads(a);
   w.scale = resolve_scale(a);
   w.is_bf16 = a->dtype == KDA_BF16;
-  w.OPL = a->dtype == KDA_BF16 ? 2 : 3;
   return w;
 }
 
@@ -119,7 +118,7 @@ BwdPlan bwd_plan(const kda_linear_args *a, bool packed) {
   b.adot = 4 * (size_t)b.anchors * a->H * b.ncb;
   b.edot = 4 * (size_t)a->N * a->H * b.ncb;
   b.heads = qk_heads(a) != a->H ? 4 * (size_t)rows * a->H * a->K : 0;
-  b.items = kda::linear_dg_items(a->B, a->T, a->N, kda::kLinearAnchor);
+  b.items = kda::linear_dg_items(a->B, a->T, a->N);
   b.part = a->decay == KDA_DECAY_HEAD ? 8 * (size_t)b.items * a->H : 0;
   return b;
 }
@@ -204,7 +203,6 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
 
   // dq: a walk with the state transposed, h^T; it leaves q.dq and the states that anchor dg
   kda::LinearWalk w = walk_base(a, g, cu);
-  w.OPL = 3;  // dg sums the rows' dots over many tokens
   w.x = d_o;
   w.z = v;
   w.w = k;
@@ -222,7 +220,6 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   w.s_dot = dht;
   w.end_dot = dht ? edot : nullptr;
   w.ckpt = ckpt;
-  w.anchor = kda::kLinearAnchor;
   set_segments(w, b.dq, segs, false);
   hipError_t e = kda::launch_linear_walk(w, st);
   if (e == hipSuccess && shared)
@@ -280,7 +277,6 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   d.H = a->H;
   d.N = a->N;
   d.ncb = b.ncb;
-  d.anchor = kda::kLinearAnchor;
   return kda::report_hip(kda::launch_linear_dg(d, st));
 }
 

@@ -56,7 +56,7 @@ __global__ __launch_bounds__(256) void linear_group_sum_kernel(const float *in, 
 // dg over one anchored stretch of one (sequence, head): a decay at token t
 // scales every later use of everything before it, which is the sum of
 // q.dq - k.dk from t on; from the stretch's end that sum is <h, dh> there. A
-// wave takes the stretch, a lane anchor / 64 neighbouring tokens; sums in fp64.
+// wave takes the stretch, a lane kDgPer neighbouring tokens; sums in fp64.
 constexpr int kDgPer = kLinearAnchor / 64;
 __global__ __launch_bounds__(256) void linear_dg_kernel(LinearDg p) {
   const int h = (int)(blockIdx.x % ((p.H + 3) / 4)) * 4 + (threadIdx.x >> 6);
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(256) void linear_dg_kernel(LinearDg p) {
   w.B = p.B;
   w.T = p.T;
   w.N = p.N;
-  w.seg = p.anchor;
+  w.seg = kLinearAnchor;
   SegLoc sg;
   const bool ok = locate_segment(w, item, false, sg);
   double sum = 0.0;
@@ -190,10 +190,10 @@ hipError_t launch_linear_group_sum(const float *in, void *out, bool is_bf16, con
   return hipGetLastError();
 }
 
-int64_t linear_dg_items(int B, int T, int N, int anchor) { return N + ((int64_t)B * T) / anchor; }
+int64_t linear_dg_items(int B, int T, int N) { return N + ((int64_t)B * T) / kLinearAnchor; }
 
 hipError_t launch_linear_dg(const LinearDg &p, hipStream_t st) {
-  const int64_t items = linear_dg_items(p.B, p.T, p.N, p.anchor);
+  const int64_t items = linear_dg_items(p.B, p.T, p.N);
   const int64_t grid = items * ((p.H + 3) / 4);
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
   if (grid > 0) {

@@ -13,6 +13,10 @@ namespace kda {
 // kda_status of a HIP result; a failure's text becomes kda_last_error() (kda_api.hip)
 kda_status report_hip(hipError_t e);
 
+int device_cus();  // compute units of the current device (chunk_fused.hip)
+
+constexpr int kLinearAnchor = 256;  // tokens between the states that anchor dg
+
 // One walk over the chunks of every sequence. With per-chunk cumulative decays
 // b and rows r, s of a chunk of L,
 //     y_r = scale (a_r S^T x_r + sum over s of D_rs (x_r . z_s) w_s)
@@ -38,15 +42,13 @@ struct LinearWalk {
   int64_t sp, sq;         // strides of the state's P and Q axes in s0, sT and s_dot
   const float *s_dot;     // with end_dot: state-shaped partner of the last state
   float *end_dot;         // [N, H, ncb] or null
-  float *ckpt;            // or null: states every `anchor` tokens of a sequence, written by the
+  float *ckpt;            // with u: states every kLinearAnchor tokens of a sequence, written by a
   float *anchor_dot;      // forward walk; a reverse walk leaves <ckpt, S> there, [.., H, ncb]
-  int anchor;
   const int32_t *cu;
   int B, T, H, P, Q, N;
   int Hk;                 // heads that share q/k data are walked next to each other
   float scale;
   bool is_bf16, reverse;
-  int OPL;                // bf16 parts of the scores and of the state in y (1 to 3)
   // Long sequences on few heads: cut into segments of seg tokens (0: whole
   // sequences) that are walked side by side. A first pass leaves each
   // segment's own state change (and decay) at the boundary behind it, a second
@@ -56,10 +58,6 @@ struct LinearWalk {
   double *seg_decay;      // [boundary, H] log2
   float *seg_first;       // copies of s0 where sT is s0 itself, [N, H, ncb, PT * QT], or null
 };
-
-int device_cus();  // compute units of the current device (chunk_fused.hip)
-
-constexpr int kLinearAnchor = 256;  // tokens between the states that anchor dg
 
 int linear_tile(int width);              // padded P: 64, 128 or 256
 int linear_cols(int width, int *ncb);    // columns per workgroup (64 or 128) and column blocks
@@ -78,7 +76,7 @@ hipError_t launch_linear_group_sum(const float *in, void *out, bool is_bf16, con
                                    int H, int Hk, int D, hipStream_t st);
 
 // dg from the row dots a = q.dq and b = k.dk: their difference summed from each
-// token to the end of its sequence, anchored at every `anchor` tokens.
+// token to the end of its sequence, anchored at every kLinearAnchor tokens.
 struct LinearDg {
   const float *a, *b;  // [ncb][H][rows]
   const float *anchor_dot, *end_dot;  // end_dot null: zero
@@ -86,9 +84,9 @@ struct LinearDg {
   float *dg;
   double *part;        // head decays: [items][H] sums
   bool g_head;
-  int B, T, H, N, ncb, anchor;
+  int B, T, H, N, ncb;
 };
-int64_t linear_dg_items(int B, int T, int N, int anchor);
+int64_t linear_dg_items(int B, int T, int N);
 hipError_t launch_linear_dg(const LinearDg &p, hipStream_t st);
 
 struct LinearRecurrent {

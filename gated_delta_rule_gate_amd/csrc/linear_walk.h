@@ -47,6 +47,13 @@ __device__ __forceinline__ bf16x8_t join8(const bf16x4_t &lo, const bf16x4_t &hi
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// The operand of a 32-deep step from a row-major row at src (the lane's row and
+// 4 grp): slots 0..3 hold elements 4 grp.., slots 4..7 those 16 further on, the
+// order in which the state's accumulators lie.
+__device__ __forceinline__ bf16x8_t row_frag(const bf16_t *src) {
+  return join8(*reinterpret_cast<const bf16x4_t *>(src), *reinterpret_cast<const bf16x4_t *>(src + 16));
+}
+
 // acc += A B over the parts of both that matter: with three parts on either
 // side, products of parts i and j with i + j <= 2.
 template <int NA, int NB_>
@@ -60,8 +67,12 @@ __device__ __forceinline__ f32x4_t mma_parts(const bf16x8_t (&a)[NA], const bf16
   return acc;
 }
 
-// Geometry of one walk. MODE 0: the whole walk; 1: the state only, left at the
-// boundary behind the segment.
+// What a walk does beside its state: y (kOut), y with the rows' dots and the
+// states that anchor dg (kDots), or nothing, the state being left at the
+// boundary behind the segment (kState).
+enum WalkMode : int { kOut = 0, kState = 1, kDots = 2 };
+
+// Geometry of one walk.
 template <typename T, int PT_, int NW_, int OPL_, int MODE_>
 struct WalkCfg {
   static constexpr bool F32 = sizeof(T) == 4;
@@ -72,9 +83,9 @@ struct WalkCfg {
   // row strides: 16 bytes past a multiple of 128, so the 16 rows of an operand read start in 16 bank groups
   static constexpr int LDX = PT + 8, LDW = QT + 8, LDP = C + 8;
   static constexpr int XPL = C * LDX, WPL = C * LDW, PPL = C * LDP;  // elements of one part
-  static constexpr unsigned nX = MODE == 0 ? 2u * IN * XPL : 0u, nZ = 2u * IN * XPL, nW = 2u * IN * WPL;
+  static constexpr unsigned nX = MODE != kState ? 2u * IN * XPL : 0u, nZ = 2u * IN * XPL, nW = 2u * IN * WPL;
   static constexpr unsigned rows = nX + nZ + nW;  // one chunk's rows
-  static constexpr unsigned nP = MODE == 0 ? 2u * OPL * PPL : 0u;
+  static constexpr unsigned nP = MODE != kState ? 2u * OPL * PPL : 0u;
   static constexpr unsigned tab = 4u * (4 * 64 + 4);  // hi, lo, a, c of every row, and the chunk's decay
   static constexpr unsigned red = 4u * NW * 64 + 64;  // row dots of every wave, and its part of <h, dh>
   static constexpr unsigned fixed = nP + 2 * tab + red;
@@ -154,7 +165,7 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
   const int h = (int)(unit % p.Hk) * G + member / ncb, cb = member % ncb;
   SegLoc sg;
   if (item < 0 || !locate_segment(p, item, REV, sg)) return;
-  if (MODE == 1 && sg.out < 0) return;  // nothing follows the last segment
+  if (MODE == kState && sg.out < 0) return;  // nothing follows the last segment
 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   const int grp = lane >> 4, l16 = lane & 15;
@@ -167,11 +178,11 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
   // ---- the state at the segment's start: rows 16t + 4 grp + e of column q ----
   f32x4_t S[F::NT];
   const int64_t sbase = ((int64_t)sg.n * p.H + h) * P * Q;
-  if (MODE == 0 && sg.in >= 0) {
+  if (MODE != kState && sg.in >= 0) {
     const float *src = p.seg_state + sg.in * fragH + frag;
 #pragma unroll
     for (int t = 0; t < F::NT; ++t) S[t] = *reinterpret_cast<const f32x4_t *>(src + t * 256);
-  } else if (MODE == 0 && p.seg_first && sg.out >= 0) {
+  } else if (MODE != kState && p.seg_first && sg.out >= 0) {
     const float *src = p.seg_first + sg.n * fragH + frag;
 #pragma unroll
     for (int t = 0; t < F::NT; ++t) S[t] = *reinterpret_cast<const f32x4_t *>(src + t * 256);
@@ -184,69 +195,77 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
         const int r = 16 * t + 4 * grp + e;
         S[t][e] = (from && r < P && q < Q) ? p.s0[sbase + r * p.sp + q * p.sq] : 0.f;
       }
-    if (MODE == 1 && sg.in < 0 && p.seg_first) {
+    if (MODE == kState && sg.in < 0 && p.seg_first) {
       float *dst = p.seg_first + sg.n * fragH + frag;
 #pragma unroll
       for (int t = 0; t < F::NT; ++t) *reinterpret_cast<f32x4_t *>(dst + t * 256) = S[t];
     }
   }
 
-  // ---- fixed offsets of this thread ----
-  const int64_t ldx = (int64_t)p.Hx * P, ldw = (int64_t)p.Hw * Q;
+  // ---- fixed offsets of this thread, and what moves from chunk to chunk ----
+  constexpr int SZ = sizeof(T);
+  const int ldx = p.Hx * P, ldw = p.Hw * Q, ldu = p.Hu * Q, ldy = p.H * Q;  // row strides, elements
+  const int ysz = SZ == 4 || p.y_f32 ? 4 : 2;
   const uint32_t gx = MX::lane_offset(tid, ldx, P), gw = MW::lane_offset(tid, ldw, ncol);
-  const uint32_t rx = (uint32_t)(MX::RPI * ldx * (int64_t)sizeof(T)), rw = (uint32_t)(MW::RPI * ldw * (int64_t)sizeof(T));
+  const uint32_t rx = (uint32_t)(MX::RPI * ldx * SZ), rw = (uint32_t)(MW::RPI * ldw * SZ);
   const int px = MX::lds_offset(tid, F::LDX), pw = MW::lds_offset(tid, F::LDW);
-  const int ax = l16 * F::LDX;                // a row of x or z as an operand
+  const int ax = l16 * F::LDX + 4 * grp;  // a row of x or z as an operand
   const int tz = cfrag_lane_off(F::LDX), tw = cfrag_lane_off(F::LDW) + 16 * wave;
-  const int ap = l16 * F::LDP + 4 * grp;      // a row of the scores
+  const int ap = l16 * F::LDP + 4 * grp;  // a row of the scores
+  // y and its partner u: four neighbouring columns of row l16 of each 16
+  const bool yin = 16 * wave + 4 * grp < ncol;
+  const uint32_t gu = yin ? (uint32_t)((l16 * ldu + 16 * wave + 4 * grp) * SZ) : kOffNone;
+  const uint32_t gy = yin ? (uint32_t)((l16 * ldy + 16 * wave + 4 * grp) * ysz) : kOffNone;
   bf16_t *const sP = reinterpret_cast<bf16_t *>(smem + F::oP);
   auto rows_at = [&](int buf) { return reinterpret_cast<bf16_t *>(smem + (F::NBUF == 2 && buf ? F::rows : 0u)); };
   auto tab_at = [&](int buf) { return reinterpret_cast<float *>(smem + F::oTab + (buf ? F::tab : 0u)); };
   float *const sRed = reinterpret_cast<float *>(smem + F::oRed), *const sAnc = sRed + NW * 64;
 
-  const T *const xh = reinterpret_cast<const T *>(p.x) + (int64_t)(h / (p.H / p.Hx)) * P;
-  const T *const zh = reinterpret_cast<const T *>(p.z) + (int64_t)(h / (p.H / p.Hx)) * P;
-  const T *const wh = reinterpret_cast<const T *>(p.w) + (int64_t)(h / (p.H / p.Hw)) * Q + col0;
-  // y and its partner u: four neighbouring columns of row l16 of each 16
-  const int64_t ldu = (int64_t)p.Hu * Q, ldy = (int64_t)p.H * Q;
-  const T *const uh0 = reinterpret_cast<const T *>(p.u) + (int64_t)(h / (p.H / p.Hu)) * Q + col0;
-  const bool yin = 16 * wave + 4 * grp < ncol, y32 = sizeof(T) == 4 || p.y_f32;
-  const int ysz = y32 ? 4 : 2;
-  const uint32_t gu = yin ? (uint32_t)((l16 * ldu + 16 * wave + 4 * grp) * (int64_t)sizeof(T)) : kOffNone;
-  const uint32_t gy = yin ? (uint32_t)((l16 * ldy + 16 * wave + 4 * grp) * ysz) : kOffNone;
-  const uint32_t ru = (uint32_t)(16 * ldu * (int64_t)sizeof(T)), ry = (uint32_t)(16 * ldy * ysz);
-  const float yscale = REV ? 1.f : p.scale, wscale = REV ? p.scale : 1.f;
   const int nch = (int)((sg.hi - sg.lo + C - 1) / C);
-  u32x4_t fx[MODE == 0 ? MX::IT : 1], fz[MX::IT], fw[MW::IT];
+  const int tail = (int)(sg.hi - sg.lo) - (nch - 1) * C;  // rows of the last chunk in token order
+  const int64_t first = sg.lo + (REV ? (int64_t)(nch - 1) * C : 0);
+  constexpr int STEP = REV ? -C : C;
+  const T *xf = reinterpret_cast<const T *>(p.x) + (first * p.Hx + h / (p.H / p.Hx)) * P;
+  const T *zf = reinterpret_cast<const T *>(p.z) + (first * p.Hx + h / (p.H / p.Hx)) * P;
+  const T *wf0 = reinterpret_cast<const T *>(p.w) + (first * p.Hw + h / (p.H / p.Hw)) * Q + col0;
+  const float *gf = p.g + (p.g_head ? h : first * p.H + h);
+  const T *uc = reinterpret_cast<const T *>(p.u) + (first * p.Hu + h / (p.H / p.Hu)) * Q + col0;
+  char *yc = reinterpret_cast<char *>(p.y) + ((first * p.H + h) * Q + col0) * ysz;
+  const int64_t dx = (int64_t)STEP * ldx, dw = (int64_t)STEP * ldw, du = (int64_t)STEP * ldu;
+  const int64_t dy = (int64_t)STEP * ldy * ysz, dgs = p.g_head ? 0 : (int64_t)STEP * p.H;
+  auto rows_of = [&](int cc) { return (REV ? cc == 0 : cc == nch - 1) ? tail : C; };
+
+  u32x4_t fx[MODE != kState ? MX::IT : 1], fz[MX::IT], fw[MW::IT];
   float fg = 0.f;
   double total = 0.0;  // log2 decay of the whole segment (the decays' wave)
-  constexpr int DW = NW - 1;  // the wave that forms the decays
-  auto chunk_of = [&](int cc) { return REV ? nch - 1 - cc : cc; };
-  auto fetch = [&](int cc) {
-    const int64_t t0 = sg.lo + (int64_t)chunk_of(cc) * C;
-    const int L = (int)min((int64_t)C, sg.hi - t0);
-    if constexpr (MODE == 0) MX::load(fx, xh + t0 * ldx, ldx, L, P, gx, rx);
-    MX::load(fz, zh + t0 * ldx, ldx, L, P, gx, rx);
-    MW::load(fw, wh + t0 * ldw, ldw, L, ncol, gw, rw);
+  constexpr int DW = 3;  // the wave that forms the decays: one with a single block of the scores
+  auto fetch = [&](int cc) {  // chunk cc in the walk's order, one after the other
+    const int L = rows_of(cc);
+    if constexpr (MODE != kState) MX::load(fx, xf, ldx, L, P, gx, rx);
+    MX::load(fz, zf, ldx, L, P, gx, rx);
+    MW::load(fw, wf0, ldw, L, ncol, gw, rw);
     if (wave == DW) {
-      if (p.g_head) {
-        fg = lane < L ? p.g[h] : 0.f;
-      } else {
-        const auto rs = tile_rsrc(p.g + t0 * p.H + h, (uint32_t)(((L - 1) * p.H + 1) * 4));
-        fg = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, (int)(lane * p.H * 4), 0, 0));
-      }
+      const auto rs = tile_rsrc(gf, (uint32_t)(p.g_head ? 4 : ((L - 1) * p.H + 1) * 4));
+      fg = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          rs, lane < L ? (p.g_head ? 0 : lane * p.H * 4) : (int)kOffNone, 0, 0));
     }
+    xf += dx;
+    zf += dx;
+    wf0 += dw;
+    gf += dgs;
   };
   auto put = [&](int buf) {
     bf16_t *s = rows_at(buf);
-    if constexpr (MODE == 0) MX::put(fx, s + px, F::LDX, F::XPL);
+    if constexpr (MODE != kState) MX::put(fx, s + px, F::LDX, F::XPL);
     MX::put(fz, s + F::nX / 2 + px, F::LDX, F::XPL);
     MW::put(fw, s + (F::nX + F::nZ) / 2 + pw, F::LDW, F::WPL);
   };
+  // The chunk's decays: b summed in fp64, as an integer and a fraction; a is the
+  // factor of x S, c that of z in the state. The scale goes with y, in reverse
+  // with z. A decay below 2^-160 is none at all and counts as 2^-32768:
+  // differences across it give zero, those beyond it stay exact.
   auto decays = [&](int buf) {
     if (wave != DW) return;
-    // b in fp64; a decay below 2^-160 is none at all and counts as 2^-32768:
-    // differences across it give zero, those beyond it stay exact
     double b = (double)fg * 1.4426950408889634073599;
     if (b <= -160.0) b = -32768.0;
 #pragma unroll
@@ -256,12 +275,12 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
     }
     const double bl = __shfl(b, 63);
     const double hi = rint(b);
-    const float first = fast_exp2((float)b), rest = fast_exp2((float)(bl - b));
+    const float from = fast_exp2((float)b), rest = fast_exp2((float)(bl - b));
     float *t = tab_at(buf);
     t[lane] = (float)hi;
     t[64 + lane] = (float)(b - hi);
-    t[128 + lane] = REV ? rest : first;
-    t[192 + lane] = REV ? first * p.scale : rest;
+    t[128 + lane] = REV ? rest : from * p.scale;
+    t[192 + lane] = REV ? from * p.scale : rest;
     if (lane == 0) t[256] = fast_exp2((float)bl);
     total += bl;
   };
@@ -272,26 +291,26 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
     decays(0);
     if (nch > 1) fetch(1);
   }
-  if constexpr (MODE == 0) {
+  if constexpr (MODE != kState) {
     // the blocks of the scores beyond the triangle stay zero
     for (int i = tid; i < OPL * F::PPL / 2; i += F::THREADS) reinterpret_cast<unsigned *>(sP)[i] = 0u;
   }
   __syncthreads();
 
   for (int cc = 0; cc < nch; ++cc) {
-    const int64_t t0 = sg.lo + (int64_t)chunk_of(cc) * C;
-    const int L = (int)min((int64_t)C, sg.hi - t0);
-    const int buf = cc & 1;
+    const int L = rows_of(cc), buf = cc & 1;
+    const int64_t t0 = first + (int64_t)cc * STEP;
     const bf16_t *const sX = rows_at(buf), *const sZ = sX + F::nX / 2, *const sW = sZ + F::nZ / 2;
     const float *const tab = tab_at(buf);
-    const bool anchored = MODE == 0 && p.ckpt && t0 + L < sg.e && (t0 + L - sg.a) % p.anchor == 0;
+    // an anchor: whole multiples of kLinearAnchor tokens into the sequence, before its end
+    const bool anchored = MODE == kDots && (((uint32_t)(t0 - sg.a) + L) % kLinearAnchor) == 0 && t0 + L < sg.e;
 
     f32x4_t y[NC];
     bf16x4_t uh[NC];
     f32x4_t uf[NC];
-    if constexpr (MODE == 0) {
+    if constexpr (MODE == kDots) {
       if (REV && anchored) {  // <h, dh> behind this chunk
-        const float *src = p.ckpt + ((t0 + L) / p.anchor) * fragH + frag;
+        const float *src = p.ckpt + ((t0 + L) / kLinearAnchor) * fragH + frag;
         float d = 0.f;
 #pragma unroll
         for (int t = 0; t < F::NT; ++t) {
@@ -303,16 +322,18 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
         for (int off = 32; off > 0; off >>= 1) d += __shfl_xor(d, off);
         if (lane == 0) sAnc[wave] = d;
       }
-      if (p.u) {  // the row dots' partners: four columns of a row a lane
-        const auto rs = tile_rsrc(uh0 + t0 * ldu, (uint32_t)(((L - 1) * ldu + ncol) * (int64_t)sizeof(T)));
+      // the row dots' partners: four columns of a row a lane
+      const auto rs = tile_rsrc(uc, (uint32_t)(((L - 1) * ldu + ncol) * SZ));
+      uc += du;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          if constexpr (sizeof(T) == 2)
-            uh[i] = __builtin_bit_cast(bf16x4_t, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)(gu + i * ru), 0, 0));
-          else
-            uf[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(gu + i * ru), 0, 0));
-        }
+      for (int i = 0; i < NC; ++i) {
+        if constexpr (SZ == 2)
+          uh[i] = __builtin_bit_cast(bf16x4_t, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)(gu + 16 * i * ldu * SZ), 0, 0));
+        else
+          uf[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(gu + 16 * i * ldu * SZ), 0, 0));
       }
+    }
+    if constexpr (MODE != kState) {
       // ---- scores of the causal blocks: lane has row l16 of x, four rows of z ----
 #pragma unroll
       for (int b0 = 0; b0 < NB; b0 += NW) {
@@ -320,15 +341,15 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
         if (blk < NB) {
           const int i = blk < 1 ? 0 : (blk < 3 ? 1 : (blk < 6 ? 2 : 3)), j = blk - i * (i + 1) / 2;
           const int ri = REV ? j : i, cj = REV ? i : j;
-          const bf16_t *xs = sX + 16 * ri * F::LDX + ax + 8 * grp, *zs = sZ + 16 * cj * F::LDX + ax + 8 * grp;
+          const bf16_t *xs = sX + 16 * ri * F::LDX + ax, *zs = sZ + 16 * cj * F::LDX + ax;
           f32x4_t acc = zero4();
 #pragma unroll
           for (int s = 0; s < F::PS; ++s) {
             bf16x8_t a[IN], bz[IN];
 #pragma unroll
             for (int pl = 0; pl < IN; ++pl) {
-              a[pl] = *reinterpret_cast<const bf16x8_t *>(xs + pl * F::XPL + 32 * s);
-              bz[pl] = *reinterpret_cast<const bf16x8_t *>(zs + pl * F::XPL + 32 * s);
+              a[pl] = row_frag(xs + pl * F::XPL + 32 * s);
+              bz[pl] = row_frag(zs + pl * F::XPL + 32 * s);
             }
             acc = mma_parts(bz, a, acc);
           }
@@ -340,7 +361,7 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
           for (int e = 0; e < 4; ++e) {
             const float d = REV ? (hs[e] - hr) + (ls[e] - lr) : (hr - hs[e]) + (lr - ls[e]);
             const bool keep = i != j || (REV ? 4 * grp + e >= l16 : 4 * grp + e <= l16);
-            v[e] = keep ? acc[e] * fast_exp2(d) * wscale : 0.f;
+            v[e] = keep ? acc[e] * (fast_exp2(d) * p.scale) : 0.f;
           }
           bf16_t *dst = sP + 16 * ri * F::LDP + 16 * cj + ap;
 #pragma unroll
@@ -365,8 +386,7 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
           bf16x8_t a[IN];
 #pragma unroll
           for (int pl = 0; pl < IN; ++pl) {
-            const bf16_t *src = sX + pl * F::XPL + 16 * i * F::LDX + ax + 32 * s + 4 * grp;
-            a[pl] = join8(*reinterpret_cast<const bf16x4_t *>(src), *reinterpret_cast<const bf16x4_t *>(src + 16));
+            a[pl] = row_frag(sX + pl * F::XPL + 16 * i * F::LDX + ax + 32 * s);
           }
           y[i] = mma_parts(sb, a, y[i]);
         }
@@ -374,11 +394,11 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) y[i] *= tab[128 + 16 * i + l16];
       __syncthreads();
-      if (REV && anchored && tid == 0) {
+      if (MODE == kDots && REV && anchored && tid == 0) {
         float d = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) d += sAnc[w];
-        p.anchor_dot[(((t0 + L) / p.anchor) * p.H + h) * ncb + cb] = d;
+        p.anchor_dot[(((t0 + L) / kLinearAnchor) * p.H + h) * ncb + cb] = d;
       }
     }
 
@@ -403,10 +423,10 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
       split8<3>(x, wc[s]);
     }
 
-    if constexpr (MODE == 0) {
+    if constexpr (MODE != kState) {
       // ---- y += scores w, out ----
-      const auto rs = tile_rsrc(reinterpret_cast<char *>(p.y) + ((t0 * p.H + h) * Q + col0) * ysz,
-                                (uint32_t)(((L - 1) * ldy + ncol) * ysz));
+      const auto rs = tile_rsrc(yc, (uint32_t)(((L - 1) * ldy + ncol) * ysz));
+      yc += dy;
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
 #pragma unroll
@@ -414,17 +434,14 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
           bf16x8_t a[OPL];
 #pragma unroll
           for (int pl = 0; pl < OPL; ++pl) {
-            const bf16_t *src = sP + pl * F::PPL + 16 * i * F::LDP + ap + 32 * s;
-            a[pl] = join8(*reinterpret_cast<const bf16x4_t *>(src), *reinterpret_cast<const bf16x4_t *>(src + 16));
+            a[pl] = row_frag(sP + pl * F::PPL + 16 * i * F::LDP + ap + 32 * s);
           }
           y[i] = mma_parts(wf[s], a, y[i]);
         }
-        y[i] *= yscale;
-        if (y32)
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y[i]), rs, (int)(gy + i * ry), 0, 0);
-        else
-          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, to_bf16x4(y[i])), rs, (int)(gy + i * ry), 0, 0);
-        if (p.u) {  // this wave's columns of the row's dot
+        const int off = (int)(gy + 16 * i * ldy * ysz);
+        if (ysz == 4) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y[i]), rs, off, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, to_bf16x4(y[i])), rs, off, 0, 0);
+        if constexpr (MODE == kDots) {  // this wave's columns of the row's dot
           const f32x4_t u = sizeof(T) == 2 ? to_f32x4(uh[i]) : uf[i];
           float d = (y[i][0] * u[0] + y[i][1] * u[1]) + (y[i][2] * u[2] + y[i][3] * u[3]);
           d += __shfl_xor(d, 16);
@@ -447,8 +464,8 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
         S[t] = mma_parts(a, wc[s], S[t]);
       }
     }
-    if (MODE == 0 && !REV && anchored) {
-      float *dst = p.ckpt + ((t0 + L) / p.anchor) * fragH + frag;
+    if (MODE == kDots && !REV && anchored) {
+      float *dst = p.ckpt + ((t0 + L) / kLinearAnchor) * fragH + frag;
 #pragma unroll
       for (int t = 0; t < F::NT; ++t) *reinterpret_cast<f32x4_t *>(dst + t * 256) = S[t];
     }
@@ -461,7 +478,7 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
       if (cc + 2 < nch) fetch(cc + 2);
     }
     __syncthreads();
-    if (MODE == 0 && p.u && tid < L) {  // behind the barrier: every wave's part is there
+    if (MODE == kDots && tid < L) {  // behind the barrier: every wave's part is there
       float d = 0.f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) d += sRed[w * 64 + tid];
@@ -469,7 +486,7 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
     }
   }
 
-  if constexpr (MODE == 1) {
+  if constexpr (MODE == kState) {
     float *dst = p.seg_state + sg.out * fragH + frag;
 #pragma unroll
     for (int t = 0; t < F::NT; ++t) *reinterpret_cast<f32x4_t *>(dst + t * 256) = S[t];
@@ -484,7 +501,7 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
           if (r < P && q < Q) p.sT[sbase + r * p.sp + q * p.sq] = S[t][e];
         }
     }
-    if (p.end_dot) {
+    if (MODE == kDots && p.end_dot) {
       float d = 0.f;
 #pragma unroll
       for (int t = 0; t < F::NT; ++t)
@@ -525,30 +542,30 @@ hipError_t launch_one(const LinearWalk &p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename T, int PT, int NW, bool REV, int OPL>
+template <typename T, int PT, int NW, bool REV, int OPL, int MODE>
 hipError_t launch_modes(const LinearWalk &p, hipStream_t st) {
   if (p.seg) {
-    hipError_t e = launch_one<T, PT, NW, REV, 1, 1>(p, st);
+    hipError_t e = launch_one<T, PT, NW, REV, 1, kState>(p, st);
     if (e != hipSuccess) return e;
     const int ncb = (p.Q + 16 * NW - 1) / (16 * NW);
     if ((e = launch_linear_chain(p, REV, (int64_t)ncb * PT * 16 * NW, st)) != hipSuccess) return e;
   }
-  return launch_one<T, PT, NW, REV, OPL, 0>(p, st);
+  return launch_one<T, PT, NW, REV, OPL, MODE>(p, st);
 }
 
-template <typename T, int PT, bool REV, int OPL>
+template <typename T, int PT, bool REV, int OPL, int MODE>
 hipError_t launch_cols(const LinearWalk &p, hipStream_t st) {
   int ncb;
-  if (linear_cols(p.Q, &ncb) == 64) return launch_modes<T, PT, 4, REV, OPL>(p, st);
-  return launch_modes<T, PT, 8, REV, OPL>(p, st);
+  if (linear_cols(p.Q, &ncb) == 64) return launch_modes<T, PT, 4, REV, OPL, MODE>(p, st);
+  return launch_modes<T, PT, 8, REV, OPL, MODE>(p, st);
 }
 
-template <typename T, bool REV, int OPL>
+template <typename T, bool REV, int OPL, int MODE>
 hipError_t launch_width(const LinearWalk &p, hipStream_t st) {
   switch (linear_tile(p.P)) {
-    case 64: return launch_cols<T, 64, REV, OPL>(p, st);
-    case 128: return launch_cols<T, 128, REV, OPL>(p, st);
-    default: return launch_cols<T, 256, REV, OPL>(p, st);
+    case 64: return launch_cols<T, 64, REV, OPL, MODE>(p, st);
+    case 128: return launch_cols<T, 128, REV, OPL, MODE>(p, st);
+    default: return launch_cols<T, 256, REV, OPL, MODE>(p, st);
   }
 }
 

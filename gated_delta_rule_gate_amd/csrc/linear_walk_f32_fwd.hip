@@ -1,13 +1,11 @@
-// The chunk walk of linear attention, fp32 inputs, in token order.
+// The chunk walk of linear attention, fp32 inputs, in token order. Three
+// bf16 parts hold every fp32 operand.
 #include "linear_walk.h"
 
 namespace kda {
 
 hipError_t launch_linear_walk_f32_fwd(const LinearWalk &p, hipStream_t st) {
-  switch (p.OPL) {
-    case 3: return launch_width<float, false, 3>(p, st);
-  }
-  return hipErrorInvalidValue;
+  return p.u ? launch_width<float, false, 3, kDots>(p, st) : launch_width<float, false, 3, kOut>(p, st);
 }
 
 }  // namespace kda
