@@ -79,19 +79,20 @@ struct WalkCfg {
   static constexpr int PT = PT_, NW = NW_, OPL = OPL_, MODE = MODE_;
   static constexpr int IN = F32 ? 3 : 1;  // bf16 parts of an input
   static constexpr int C = (F32 || PT == 256) ? 32 : 64;
-  static constexpr int NC = C / 16, KS = C / 32, PS = PT / 32, NT = PT / 16, QT = 16 * NW, THREADS = 64 * NW;
-  // row strides: 16 bytes past a multiple of 128, so the 16 rows of an operand read start in 16 bank groups
-  static constexpr int LDX = PT + 8, LDW = QT + 8, LDP = C + 8;
+  static constexpr int NC = C / 16, KS = C / 32, PS = PT / 32, NT = PT / 16, QT = 16 * NW;
+  static constexpr int HELPERS = 4, THREADS = 64 * (NW + HELPERS), HT = 64 * HELPERS;
+  // row strides: 16 bytes past a multiple of 128 (of scores: 8 bytes), so that the 8-byte operand reads
+  // of 16 rows by two lane groups fall into 64 different banks
+  static constexpr int LDX = PT + 8, LDW = QT + 8, LDP = C + 4;
   static constexpr int XPL = C * LDX, WPL = C * LDW, PPL = C * LDP;  // elements of one part
   static constexpr unsigned nX = MODE != kState ? 2u * IN * XPL : 0u, nZ = 2u * IN * XPL, nW = 2u * IN * WPL;
   static constexpr unsigned rows = nX + nZ + nW;  // one chunk's rows
   static constexpr unsigned nP = MODE != kState ? 2u * OPL * PPL : 0u;
   static constexpr unsigned tab = 4u * (4 * 64 + 4);  // hi, lo, a, c of every row, and the chunk's decay
-  static constexpr unsigned red = 4u * NW * 64 + 64;  // row dots of every wave, and its part of <h, dh>
-  static constexpr unsigned fixed = nP + 2 * tab + red;
-  // two chunks' rows where they fit: the next chunk is written while this one is read
-  static constexpr int NBUF = 2 * rows + fixed <= 160 * 1024 ? 2 : 1;
-  static constexpr unsigned oP = NBUF * rows, oTab = oP + nP, oRed = oTab + 2 * tab, total = oRed + red;
+  static constexpr unsigned red = MODE == kDots ? 4u * NW * 64 + 64 : 64u;  // row dots of every wave; <h, dh>
+  // two chunks' rows and scores where they fit
+  static constexpr int NBUF = 2 * (rows + nP + tab) + red <= 160 * 1024 ? 2 : 1;
+  static constexpr unsigned oP = NBUF * rows, oTab = oP + NBUF * nP, oRed = oTab + 2 * tab, total = oRed + red;
   static_assert(total <= 160 * 1024, "LDS");
 };
 
@@ -136,20 +137,24 @@ struct RowsMove {
   }
 };
 
-// Per chunk, two periods between barriers. In the first, the waves share out
-// the causal 16 x 16 blocks of the scores, write them decayed to LDS, and each
-// multiplies every row with its own columns of the state. In the second each
-// adds scores times its columns of w, stores its columns of y, updates its
-// columns of the state, and writes its share of the next chunk's rows (loaded a
-// whole chunk earlier) to the other LDS buffer; one wave forms the next chunk's
-// decays. Products that give y are taken transposed, so that a lane holds four
-// neighbouring columns of one row: scores and y leave in 8-byte pieces.
+// NW state waves each keep 16 columns of the state; four helper waves, one a
+// SIMD beside two state waves, bring rows to LDS, form decays and the scores.
+// With two LDS buffers a chunk takes two periods between barriers:
+//   state waves   y = a (x S) of chunk c        | w decayed, y += scores w, y out, S updated
+//   helper waves  rows of c + 1 (loaded a chunk | scores of c + 1
+//                 ago) to LDS, its decays, the
+//                 loads of c + 2
+// so the state's chain holds no load, no decay and no score. With one buffer
+// (fp32 rows from 128 wide) the scores are those of c, beside a (x S), and the
+// next rows go to LDS in a period of their own. Products that give y and scores
+// are taken transposed, so that a lane holds four neighbouring columns of one
+// row and both leave in 8-byte pieces.
 template <typename T, int PT, int NW, bool REV, int OPL, int MODE>
-__global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
+__global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p) {
   using F = WalkCfg<T, PT, NW, OPL, MODE>;
   constexpr int C = F::C, NC = F::NC, KS = F::KS, IN = F::IN, QT = F::QT, NB = NC * (NC + 1) / 2;
-  using MX = RowsMove<T, F::THREADS, C, PT>;
-  using MW = RowsMove<T, F::THREADS, C, QT>;
+  using MX = RowsMove<T, F::HT, C, PT>;
+  using MW = RowsMove<T, F::HT, C, QT>;
   extern __shared__ __align__(16) char smem[];
 
   // Workgroups that read the same q/k rows (a group's heads, a head's column
@@ -171,173 +176,99 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
   const int grp = lane >> 4, l16 = lane & 15;
   const int P = p.P, Q = p.Q, col0 = cb * QT, ncol = min(QT, Q - col0);
   const int64_t rows = (int64_t)p.B * p.T;
-  const int q = col0 + 16 * wave + l16;  // this lane's state column
-  const int64_t frag = ((int64_t)h * ncb + cb) * (PT * QT) + ((int64_t)wave * F::NT * 64 + lane) * 4;
-  const int64_t fragH = (int64_t)p.H * ncb * (PT * QT);  // elements of one boundary
 
-  // ---- the state at the segment's start: rows 16t + 4 grp + e of column q ----
-  f32x4_t S[F::NT];
   const int64_t sbase = ((int64_t)sg.n * p.H + h) * P * Q;
-  if (MODE != kState && sg.in >= 0) {
-    const float *src = p.seg_state + sg.in * fragH + frag;
-#pragma unroll
-    for (int t = 0; t < F::NT; ++t) S[t] = *reinterpret_cast<const f32x4_t *>(src + t * 256);
-  } else if (MODE != kState && p.seg_first && sg.out >= 0) {
-    const float *src = p.seg_first + sg.n * fragH + frag;
-#pragma unroll
-    for (int t = 0; t < F::NT; ++t) S[t] = *reinterpret_cast<const f32x4_t *>(src + t * 256);
-  } else {
-    const bool from = p.s0 && sg.in < 0;
-#pragma unroll
-    for (int t = 0; t < F::NT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 16 * t + 4 * grp + e;
-        S[t][e] = (from && r < P && q < Q) ? p.s0[sbase + r * p.sp + q * p.sq] : 0.f;
-      }
-    if (MODE == kState && sg.in < 0 && p.seg_first) {
-      float *dst = p.seg_first + sg.n * fragH + frag;
-#pragma unroll
-      for (int t = 0; t < F::NT; ++t) *reinterpret_cast<f32x4_t *>(dst + t * 256) = S[t];
-    }
-  }
 
-  // ---- fixed offsets of this thread, and what moves from chunk to chunk ----
   constexpr int SZ = sizeof(T);
-  const int ldx = p.Hx * P, ldw = p.Hw * Q, ldu = p.Hu * Q, ldy = p.H * Q;  // row strides, elements
-  const int ysz = SZ == 4 || p.y_f32 ? 4 : 2;
-  const uint32_t gx = MX::lane_offset(tid, ldx, P), gw = MW::lane_offset(tid, ldw, ncol);
-  const uint32_t rx = (uint32_t)(MX::RPI * ldx * SZ), rw = (uint32_t)(MW::RPI * ldw * SZ);
-  const int px = MX::lds_offset(tid, F::LDX), pw = MW::lds_offset(tid, F::LDW);
-  const int ax = l16 * F::LDX + 4 * grp;  // a row of x or z as an operand
-  const int tz = cfrag_lane_off(F::LDX), tw = cfrag_lane_off(F::LDW) + 16 * wave;
-  const int ap = l16 * F::LDP + 4 * grp;  // a row of the scores
-  // y and its partner u: four neighbouring columns of row l16 of each 16
-  const bool yin = 16 * wave + 4 * grp < ncol;
-  const uint32_t gu = yin ? (uint32_t)((l16 * ldu + 16 * wave + 4 * grp) * SZ) : kOffNone;
-  const uint32_t gy = yin ? (uint32_t)((l16 * ldy + 16 * wave + 4 * grp) * ysz) : kOffNone;
-  bf16_t *const sP = reinterpret_cast<bf16_t *>(smem + F::oP);
-  auto rows_at = [&](int buf) { return reinterpret_cast<bf16_t *>(smem + (F::NBUF == 2 && buf ? F::rows : 0u)); };
-  auto tab_at = [&](int buf) { return reinterpret_cast<float *>(smem + F::oTab + (buf ? F::tab : 0u)); };
-  float *const sRed = reinterpret_cast<float *>(smem + F::oRed), *const sAnc = sRed + NW * 64;
-
   const int nch = (int)((sg.hi - sg.lo + C - 1) / C);
   const int tail = (int)(sg.hi - sg.lo) - (nch - 1) * C;  // rows of the last chunk in token order
   const int64_t first = sg.lo + (REV ? (int64_t)(nch - 1) * C : 0);
   constexpr int STEP = REV ? -C : C;
-  const T *xf = reinterpret_cast<const T *>(p.x) + (first * p.Hx + h / (p.H / p.Hx)) * P;
-  const T *zf = reinterpret_cast<const T *>(p.z) + (first * p.Hx + h / (p.H / p.Hx)) * P;
-  const T *wf0 = reinterpret_cast<const T *>(p.w) + (first * p.Hw + h / (p.H / p.Hw)) * Q + col0;
-  const float *gf = p.g + (p.g_head ? h : first * p.H + h);
-  const T *uc = reinterpret_cast<const T *>(p.u) + (first * p.Hu + h / (p.H / p.Hu)) * Q + col0;
-  char *yc = reinterpret_cast<char *>(p.y) + ((first * p.H + h) * Q + col0) * ysz;
-  const int64_t dx = (int64_t)STEP * ldx, dw = (int64_t)STEP * ldw, du = (int64_t)STEP * ldu;
-  const int64_t dy = (int64_t)STEP * ldy * ysz, dgs = p.g_head ? 0 : (int64_t)STEP * p.H;
   auto rows_of = [&](int cc) { return (REV ? cc == 0 : cc == nch - 1) ? tail : C; };
-
-  u32x4_t fx[MODE != kState ? MX::IT : 1], fz[MX::IT], fw[MW::IT];
-  float fg = 0.f;
-  double total = 0.0;  // log2 decay of the whole segment (the decays' wave)
-  constexpr int DW = 3;  // the wave that forms the decays: one with a single block of the scores
-  auto fetch = [&](int cc) {  // chunk cc in the walk's order, one after the other
-    const int L = rows_of(cc);
-    if constexpr (MODE != kState) MX::load(fx, xf, ldx, L, P, gx, rx);
-    MX::load(fz, zf, ldx, L, P, gx, rx);
-    MW::load(fw, wf0, ldw, L, ncol, gw, rw);
-    if (wave == DW) {
-      const auto rs = tile_rsrc(gf, (uint32_t)(p.g_head ? 4 : ((L - 1) * p.H + 1) * 4));
-      fg = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-          rs, lane < L ? (p.g_head ? 0 : lane * p.H * 4) : (int)kOffNone, 0, 0));
-    }
-    xf += dx;
-    zf += dx;
-    wf0 += dw;
-    gf += dgs;
+  auto rows_at = [&](int cc) { return reinterpret_cast<bf16_t *>(smem + (F::NBUF == 2 && (cc & 1) ? F::rows : 0u)); };
+  auto scores_at = [&](int cc) {
+    return reinterpret_cast<bf16_t *>(smem + F::oP + (F::NBUF == 2 && (cc & 1) ? F::nP : 0u));
   };
-  auto put = [&](int buf) {
-    bf16_t *s = rows_at(buf);
-    if constexpr (MODE != kState) MX::put(fx, s + px, F::LDX, F::XPL);
-    MX::put(fz, s + F::nX / 2 + px, F::LDX, F::XPL);
-    MW::put(fw, s + (F::nX + F::nZ) / 2 + pw, F::LDW, F::WPL);
-  };
-  // The chunk's decays: b summed in fp64, as an integer and a fraction; a is the
-  // factor of x S, c that of z in the state. The scale goes with y, in reverse
-  // with z. A decay below 2^-160 is none at all and counts as 2^-32768:
-  // differences across it give zero, those beyond it stay exact.
-  auto decays = [&](int buf) {
-    if (wave != DW) return;
-    double b = (double)fg * 1.4426950408889634073599;
-    if (b <= -160.0) b = -32768.0;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const double up = __shfl_up(b, off);
-      if (lane >= off) b += up;
-    }
-    const double bl = __shfl(b, 63);
-    const double hi = rint(b);
-    const float from = fast_exp2((float)b), rest = fast_exp2((float)(bl - b));
-    float *t = tab_at(buf);
-    t[lane] = (float)hi;
-    t[64 + lane] = (float)(b - hi);
-    t[128 + lane] = REV ? rest : from * p.scale;
-    t[192 + lane] = REV ? from * p.scale : rest;
-    if (lane == 0) t[256] = fast_exp2((float)bl);
-    total += bl;
+  auto tab_at = [&](int cc) { return reinterpret_cast<float *>(smem + F::oTab + ((cc & 1) ? F::tab : 0u)); };
+  float *const sRed = reinterpret_cast<float *>(smem + F::oRed), *const sAnc = sRed + (MODE == kDots ? NW * 64 : 0);
+  // whole multiples of kLinearAnchor tokens into the sequence, before its end
+  auto anchored = [&](int64_t t0, int L) {
+    return MODE == kDots && (((uint32_t)(t0 - sg.a) + L) % kLinearAnchor) == 0 && t0 + L < sg.e;
   };
 
-  if (nch > 0) {
-    fetch(0);
-    put(0);
-    decays(0);
-    if (nch > 1) fetch(1);
-  }
-  if constexpr (MODE != kState) {
-    // the blocks of the scores beyond the triangle stay zero
-    for (int i = tid; i < OPL * F::PPL / 2; i += F::THREADS) reinterpret_cast<unsigned *>(sP)[i] = 0u;
-  }
-  __syncthreads();
-
-  for (int cc = 0; cc < nch; ++cc) {
-    const int L = rows_of(cc), buf = cc & 1;
-    const int64_t t0 = first + (int64_t)cc * STEP;
-    const bf16_t *const sX = rows_at(buf), *const sZ = sX + F::nX / 2, *const sW = sZ + F::nZ / 2;
-    const float *const tab = tab_at(buf);
-    // an anchor: whole multiples of kLinearAnchor tokens into the sequence, before its end
-    const bool anchored = MODE == kDots && (((uint32_t)(t0 - sg.a) + L) % kLinearAnchor) == 0 && t0 + L < sg.e;
-
-    f32x4_t y[NC];
-    bf16x4_t uh[NC];
-    f32x4_t uf[NC];
-    if constexpr (MODE == kDots) {
-      if (REV && anchored) {  // <h, dh> behind this chunk
-        const float *src = p.ckpt + ((t0 + L) / kLinearAnchor) * fragH + frag;
-        float d = 0.f;
-#pragma unroll
-        for (int t = 0; t < F::NT; ++t) {
-          const f32x4_t x = *reinterpret_cast<const f32x4_t *>(src + t * 256);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) d += x[e] * S[t][e];
-        }
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) d += __shfl_xor(d, off);
-        if (lane == 0) sAnc[wave] = d;
+  if (wave >= NW) {
+    // =================================== helper waves ===================================
+    const int hw = wave - NW, ht = tid - 64 * NW;
+    const int ldx = p.Hx * P, ldw = p.Hw * Q;  // row strides, elements
+    const uint32_t gx = MX::lane_offset(ht, ldx, P), gw = MW::lane_offset(ht, ldw, ncol);
+    const uint32_t rx = (uint32_t)(MX::RPI * ldx * SZ), rw = (uint32_t)(MW::RPI * ldw * SZ);
+    const int px = MX::lds_offset(ht, F::LDX), pw = MW::lds_offset(ht, F::LDW);
+    const int ax = l16 * F::LDX + 4 * grp;  // a row of x or z as an operand
+    const T *xf = reinterpret_cast<const T *>(p.x) + (first * p.Hx + h / (p.H / p.Hx)) * P;
+    const T *zf = reinterpret_cast<const T *>(p.z) + (first * p.Hx + h / (p.H / p.Hx)) * P;
+    const T *wf = reinterpret_cast<const T *>(p.w) + (first * p.Hw + h / (p.H / p.Hw)) * Q + col0;
+    const float *gf = p.g + (p.g_head ? h : first * p.H + h);
+    const int64_t dx = (int64_t)STEP * ldx, dw = (int64_t)STEP * ldw, dg = p.g_head ? 0 : (int64_t)STEP * p.H;
+    u32x4_t fx[MODE != kState ? MX::IT : 1], fz[MX::IT], fw[MW::IT];
+    float fg = 0.f;
+    double total = 0.0;  // log2 decay of the whole segment (the decays' wave)
+    constexpr int DW = 3;  // the helper that forms the decays: one with fewer blocks of the scores
+    auto fetch = [&](int cc) {  // chunk after chunk in the walk's order
+      const int L = rows_of(cc);
+      if constexpr (MODE != kState) MX::load(fx, xf, ldx, L, P, gx, rx);
+      MX::load(fz, zf, ldx, L, P, gx, rx);
+      MW::load(fw, wf, ldw, L, ncol, gw, rw);
+      if (hw == DW) {
+        const auto rs = tile_rsrc(gf, (uint32_t)(p.g_head ? 4 : ((L - 1) * p.H + 1) * 4));
+        fg = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+            rs, lane < L ? (p.g_head ? 0 : lane * p.H * 4) : (int)kOffNone, 0, 0));
       }
-      // the row dots' partners: four columns of a row a lane
-      const auto rs = tile_rsrc(uc, (uint32_t)(((L - 1) * ldu + ncol) * SZ));
-      uc += du;
+      xf += dx;
+      zf += dx;
+      wf += dw;
+      gf += dg;
+    };
+    // The chunk's decays: b summed in fp64, as an integer and a fraction; a is
+    // the factor of x S, c that of z in the state. The scale goes with y, in
+    // reverse with z. A decay below 2^-160 is none at all and counts as
+    // 2^-32768: differences across it give zero, those beyond it stay exact.
+    auto decays = [&](int cc) {
+      if (hw != DW) return;
+      double b = (double)fg * 1.4426950408889634073599;
+      if (b <= -160.0) b = -32768.0;
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        if constexpr (SZ == 2)
-          uh[i] = __builtin_bit_cast(bf16x4_t, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)(gu + 16 * i * ldu * SZ), 0, 0));
-        else
-          uf[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(gu + 16 * i * ldu * SZ), 0, 0));
+      for (int off = 1; off < 64; off <<= 1) {
+        const double up = __shfl_up(b, off);
+        if (lane >= off) b += up;
       }
-    }
-    if constexpr (MODE != kState) {
-      // ---- scores of the causal blocks: lane has row l16 of x, four rows of z ----
+      const double bl = __shfl(b, 63);
+      const double hi = rint(b);
+      const float from = fast_exp2((float)b), rest = fast_exp2((float)(bl - b));
+      float *t = tab_at(cc);
+      t[lane] = (float)hi;
+      t[64 + lane] = (float)(b - hi);
+      t[128 + lane] = REV ? rest : from * p.scale;
+      t[192 + lane] = REV ? from * p.scale : rest;
+      if (lane == 0) t[256] = fast_exp2((float)bl);
+      total += bl;
+    };
+    auto bring = [&](int cc) {  // rows and decays of cc to LDS, loads of the chunk after it
+      bf16_t *s = rows_at(cc);
+      if constexpr (MODE != kState) MX::put(fx, s + px, F::LDX, F::XPL);
+      MX::put(fz, s + F::nX / 2 + px, F::LDX, F::XPL);
+      MW::put(fw, s + (F::nX + F::nZ) / 2 + pw, F::LDW, F::WPL);
+      decays(cc);
+      if (cc + 1 < nch) fetch(cc + 1);
+    };
+    // scores of the causal 16 x 16 blocks, decayed and scaled, a wave taking
+    // every fourth: lane has row l16 of x, four rows of z
+    auto scores = [&](int cc) {
+      const bf16_t *const sX = rows_at(cc), *const sZ = sX + F::nX / 2;
+      const float *const tab = tab_at(cc);
+      bf16_t *const sP = scores_at(cc);
 #pragma unroll
-      for (int b0 = 0; b0 < NB; b0 += NW) {
-        const int blk = b0 + wave;
+      for (int b0 = 0; b0 < NB; b0 += F::HELPERS) {
+        const int blk = b0 + hw;
         if (blk < NB) {
           const int i = blk < 1 ? 0 : (blk < 3 ? 1 : (blk < 6 ? 2 : 3)), j = blk - i * (i + 1) / 2;
           const int ri = REV ? j : i, cj = REV ? i : j;
@@ -363,7 +294,7 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
             const bool keep = i != j || (REV ? 4 * grp + e >= l16 : 4 * grp + e <= l16);
             v[e] = keep ? acc[e] * (fast_exp2(d) * p.scale) : 0.f;
           }
-          bf16_t *dst = sP + 16 * ri * F::LDP + 16 * cj + ap;
+          bf16_t *dst = sP + (16 * ri + l16) * F::LDP + 16 * cj + 4 * grp;
 #pragma unroll
           for (int pl = 0; pl < OPL; ++pl) {
             const bf16x4_t part = to_bf16x4(v);
@@ -372,34 +303,175 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
           }
         }
       }
-      // ---- y = a (x S) ----
+    };
+    auto dots = [&](int cc) {  // the row dots of chunk cc: every state wave's part
+      const int L = rows_of(cc);
+      if (ht < L) {
+        float d = 0.f;
 #pragma unroll
-      for (int i = 0; i < NC; ++i) y[i] = zero4();
-#pragma unroll
-      for (int s = 0; s < F::PS; ++s) {
-        bf16x8_t sb[OPL];
-        const float sv[8] = {S[2 * s][0], S[2 * s][1], S[2 * s][2], S[2 * s][3],
-                             S[2 * s + 1][0], S[2 * s + 1][1], S[2 * s + 1][2], S[2 * s + 1][3]};
-        split8<OPL>(sv, sb);
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          bf16x8_t a[IN];
-#pragma unroll
-          for (int pl = 0; pl < IN; ++pl) {
-            a[pl] = row_frag(sX + pl * F::XPL + 16 * i * F::LDX + ax + 32 * s);
-          }
-          y[i] = mma_parts(sb, a, y[i]);
-        }
+        for (int w = 0; w < NW; ++w) d += sRed[w * 64 + ht];
+        p.dot[((int64_t)cb * p.H + h) * rows + first + (int64_t)cc * STEP + ht] = d;
       }
-#pragma unroll
-      for (int i = 0; i < NC; ++i) y[i] *= tab[128 + 16 * i + l16];
-      __syncthreads();
-      if (MODE == kDots && REV && anchored && tid == 0) {
+    };
+    auto anchor = [&](int cc) {  // <h, dh> behind chunk cc
+      const int L = rows_of(cc);
+      const int64_t t0 = first + (int64_t)cc * STEP;
+      if (anchored(t0, L) && ht == 0) {
         float d = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) d += sAnc[w];
         p.anchor_dot[(((t0 + L) / kLinearAnchor) * p.H + h) * ncb + cb] = d;
       }
+    };
+
+    if (nch > 0) fetch(0);
+    if constexpr (MODE != kState) {
+      // the blocks of the scores beyond the triangle stay zero
+      for (int i = ht; i < (int)(F::NBUF * F::nP / 4); i += F::HT) reinterpret_cast<unsigned *>(smem + F::oP)[i] = 0u;
+    }
+    if (nch > 0) bring(0);
+    __syncthreads();
+    if constexpr (F::NBUF == 2 && MODE != kState) {
+      if (nch > 0) scores(0);
+      __syncthreads();
+      for (int cc = 0; cc < nch; ++cc) {
+        if (MODE == kDots && cc > 0) dots(cc - 1);
+        if (cc + 1 < nch) bring(cc + 1);
+        __syncthreads();
+        if (MODE == kDots && REV) anchor(cc);
+        if (cc + 1 < nch) scores(cc + 1);
+        __syncthreads();
+      }
+    } else {
+      for (int cc = 0; cc < nch; ++cc) {
+        if constexpr (MODE != kState) {
+          scores(cc);
+          __syncthreads();
+          if (MODE == kDots && REV) anchor(cc);
+        }
+        if constexpr (F::NBUF == 1) __syncthreads();
+        if constexpr (MODE == kDots) dots(cc);
+        if (cc + 1 < nch) bring(cc + 1);
+        __syncthreads();
+      }
+    }
+    if (MODE == kDots && F::NBUF == 2 && nch > 0) dots(nch - 1);
+    if (MODE == kState && hw == DW && lane == 0 && cb == 0) p.seg_decay[sg.out * p.H + h] = total;
+    if (MODE == kDots && p.end_dot && sg.out < 0) {
+      __syncthreads();
+      if (ht == 0) {
+        float d = 0.f;
+        for (int w = 0; w < NW; ++w) d += sAnc[w];
+        p.end_dot[((int64_t)sg.n * p.H + h) * ncb + cb] = d;
+      }
+    }
+    return;
+  }
+
+  // ==================================== state waves ====================================
+  const int q = col0 + 16 * wave + l16;  // this lane's state column
+  const int64_t frag = ((int64_t)h * ncb + cb) * (PT * QT) + ((int64_t)wave * F::NT * 64 + lane) * 4;
+  const int64_t fragH = (int64_t)p.H * ncb * (PT * QT);  // elements of one boundary
+
+  // ---- the state at the segment's start: rows 16t + 4 grp + e of column q ----
+  f32x4_t S[F::NT];
+  if (MODE != kState && sg.in >= 0) {
+    const float *src = p.seg_state + sg.in * fragH + frag;
+#pragma unroll
+    for (int t = 0; t < F::NT; ++t) S[t] = *reinterpret_cast<const f32x4_t *>(src + t * 256);
+  } else if (MODE != kState && p.seg_first && sg.out >= 0) {
+    const float *src = p.seg_first + sg.n * fragH + frag;
+#pragma unroll
+    for (int t = 0; t < F::NT; ++t) S[t] = *reinterpret_cast<const f32x4_t *>(src + t * 256);
+  } else {
+    const bool from = p.s0 && sg.in < 0;
+#pragma unroll
+    for (int t = 0; t < F::NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 16 * t + 4 * grp + e;
+        S[t][e] = (from && r < P && q < Q) ? p.s0[sbase + r * p.sp + q * p.sq] : 0.f;
+      }
+    if (MODE == kState && sg.in < 0 && p.seg_first) {
+      float *dst = p.seg_first + sg.n * fragH + frag;
+#pragma unroll
+      for (int t = 0; t < F::NT; ++t) *reinterpret_cast<f32x4_t *>(dst + t * 256) = S[t];
+    }
+  }
+
+  const int ax = l16 * F::LDX + 4 * grp;  // a row of x as an operand
+  const int tz = cfrag_lane_off(F::LDX), tw = cfrag_lane_off(F::LDW) + 16 * wave;
+  const int ap = l16 * F::LDP + 4 * grp;  // a row of the scores
+  // y and its partner u: four neighbouring columns of row l16 of each 16
+  const int ldu = p.Hu * Q, ldy = p.H * Q, ysz = SZ == 4 || p.y_f32 ? 4 : 2;
+  const bool yin = 16 * wave + 4 * grp < ncol;
+  const uint32_t gu = yin ? (uint32_t)((l16 * ldu + 16 * wave + 4 * grp) * SZ) : kOffNone;
+  const uint32_t gy = yin ? (uint32_t)((l16 * ldy + 16 * wave + 4 * grp) * ysz) : kOffNone;
+  const T *uc = reinterpret_cast<const T *>(p.u) + (first * p.Hu + h / (p.H / p.Hu)) * Q + col0;
+  char *yc = reinterpret_cast<char *>(p.y) + ((first * p.H + h) * Q + col0) * ysz;
+  const int64_t du = (int64_t)STEP * ldu, dy = (int64_t)STEP * ldy * ysz;
+
+  f32x4_t y[NC];
+  bf16x4_t uh[NC];
+  f32x4_t uf[NC];
+  auto times_state = [&](int cc) {  // y = a (x S)
+    const bf16_t *const sX = rows_at(cc);
+    const float *const tab = tab_at(cc);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) y[i] = zero4();
+#pragma unroll
+    for (int s = 0; s < F::PS; ++s) {
+      bf16x8_t sb[OPL];
+      const float sv[8] = {S[2 * s][0], S[2 * s][1], S[2 * s][2], S[2 * s][3],
+                           S[2 * s + 1][0], S[2 * s + 1][1], S[2 * s + 1][2], S[2 * s + 1][3]};
+      split8<OPL>(sv, sb);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        bf16x8_t a[IN];
+#pragma unroll
+        for (int pl = 0; pl < IN; ++pl) a[pl] = row_frag(sX + pl * F::XPL + 16 * i * F::LDX + ax + 32 * s);
+        y[i] = mma_parts(sb, a, y[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NC; ++i) y[i] *= tab[128 + 16 * i + l16];
+  };
+
+  __syncthreads();
+  if constexpr (F::NBUF == 2 && MODE != kState) __syncthreads();
+  for (int cc = 0; cc < nch; ++cc) {
+    const int L = rows_of(cc);
+    const int64_t t0 = first + (int64_t)cc * STEP;
+    const bf16_t *const sZ = rows_at(cc) + F::nX / 2, *const sW = sZ + F::nZ / 2;
+    const float *const tab = tab_at(cc);
+
+    if constexpr (MODE != kState) {
+      if constexpr (MODE == kDots) {
+        if (REV && anchored(t0, L)) {  // <h, dh> behind this chunk
+          const float *src = p.ckpt + ((t0 + L) / kLinearAnchor) * fragH + frag;
+          float d = 0.f;
+#pragma unroll
+          for (int t = 0; t < F::NT; ++t) {
+            const f32x4_t x = *reinterpret_cast<const f32x4_t *>(src + t * 256);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d += x[e] * S[t][e];
+          }
+#pragma unroll
+          for (int off = 32; off > 0; off >>= 1) d += __shfl_xor(d, off);
+          if (lane == 0) sAnc[wave] = d;
+        }
+        // the row dots' partners: four columns of a row a lane
+        const auto rs = tile_rsrc(uc, (uint32_t)(((L - 1) * ldu + ncol) * SZ));
+        uc += du;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int off = (int)(gu + 16 * i * ldu * SZ);
+          if constexpr (SZ == 2) uh[i] = __builtin_bit_cast(bf16x4_t, __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0));
+          else uf[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+        }
+      }
+      times_state(cc);
+      __syncthreads();
     }
 
     // ---- w as an operand, and decayed to the chunk's end in three parts ----
@@ -425,6 +497,7 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
 
     if constexpr (MODE != kState) {
       // ---- y += scores w, out ----
+      const bf16_t *const sP = scores_at(cc);
       const auto rs = tile_rsrc(yc, (uint32_t)(((L - 1) * ldy + ncol) * ysz));
       yc += dy;
 #pragma unroll
@@ -433,20 +506,18 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
         for (int s = REV ? i / 2 : 0; s <= (REV ? KS - 1 : i / 2); ++s) {
           bf16x8_t a[OPL];
 #pragma unroll
-          for (int pl = 0; pl < OPL; ++pl) {
-            a[pl] = row_frag(sP + pl * F::PPL + 16 * i * F::LDP + ap + 32 * s);
-          }
+          for (int pl = 0; pl < OPL; ++pl) a[pl] = row_frag(sP + pl * F::PPL + 16 * i * F::LDP + ap + 32 * s);
           y[i] = mma_parts(wf[s], a, y[i]);
         }
         const int off = (int)(gy + 16 * i * ldy * ysz);
         if (ysz == 4) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y[i]), rs, off, 0, 0);
         else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, to_bf16x4(y[i])), rs, off, 0, 0);
-        if constexpr (MODE == kDots) {  // this wave's columns of the row's dot
-          const f32x4_t u = sizeof(T) == 2 ? to_f32x4(uh[i]) : uf[i];
+        if constexpr (MODE == kDots) {  // this wave's columns of the row's dot; u is zero past the width
+          const f32x4_t u = SZ == 2 ? to_f32x4(uh[i]) : uf[i];
           float d = (y[i][0] * u[0] + y[i][1] * u[1]) + (y[i][2] * u[2] + y[i][3] * u[3]);
           d += __shfl_xor(d, 16);
           d += __shfl_xor(d, 32);
-          if (grp == 0) sRed[wave * 64 + 16 * i + l16] = d;  // columns past the width read u as zero
+          if (grp == 0) sRed[wave * 64 + 16 * i + l16] = d;
         }
       }
     }
@@ -464,33 +535,19 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
         S[t] = mma_parts(a, wc[s], S[t]);
       }
     }
-    if (MODE == kDots && !REV && anchored) {
+    if (!REV && anchored(t0, L)) {
       float *dst = p.ckpt + ((t0 + L) / kLinearAnchor) * fragH + frag;
 #pragma unroll
       for (int t = 0; t < F::NT; ++t) *reinterpret_cast<f32x4_t *>(dst + t * 256) = S[t];
     }
-
-    // ---- the next chunk's rows ----
     if constexpr (F::NBUF == 1) __syncthreads();
-    if (cc + 1 < nch) {
-      put(buf ^ 1);
-      decays(buf ^ 1);
-      if (cc + 2 < nch) fetch(cc + 2);
-    }
     __syncthreads();
-    if (MODE == kDots && tid < L) {  // behind the barrier: every wave's part is there
-      float d = 0.f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) d += sRed[w * 64 + tid];
-      p.dot[((int64_t)cb * p.H + h) * rows + t0 + tid] = d;
-    }
   }
 
   if constexpr (MODE == kState) {
     float *dst = p.seg_state + sg.out * fragH + frag;
 #pragma unroll
     for (int t = 0; t < F::NT; ++t) *reinterpret_cast<f32x4_t *>(dst + t * 256) = S[t];
-    if (wave == DW && lane == 0 && cb == 0) p.seg_decay[sg.out * p.H + h] = total;
   } else if (sg.out < 0) {
     if (p.sT && !(nch == 0 && p.sT == p.s0)) {
 #pragma unroll
@@ -512,14 +569,8 @@ __global__ __launch_bounds__(64 * NW) void linear_walk_kernel(LinearWalk p) {
         }
 #pragma unroll
       for (int off = 32; off > 0; off >>= 1) d += __shfl_xor(d, off);
+      if (lane == 0) sAnc[wave] = d;
       __syncthreads();
-      if (lane == 0) sRed[wave] = d;
-      __syncthreads();
-      if (tid == 0) {
-        float s = 0.f;
-        for (int w = 0; w < NW; ++w) s += sRed[w];
-        p.end_dot[((int64_t)sg.n * p.H + h) * ncb + cb] = s;
-      }
     }
   }
 }
