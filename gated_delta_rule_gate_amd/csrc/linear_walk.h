@@ -47,12 +47,14 @@ __device__ __forceinline__ bf16x8_t join8(const bf16x4_t &lo, const bf16x4_t &hi
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// The operand of a 32-deep step from a row-major row at src (the lane's row and
-// 4 grp): slots 0..3 hold elements 4 grp.., slots 4..7 those 16 further on, the
-// order in which the state's accumulators lie.
-__device__ __forceinline__ bf16x8_t row_frag(const bf16_t *src) {
-  return join8(*reinterpret_cast<const bf16x4_t *>(src), *reinterpret_cast<const bf16x4_t *>(src + 16));
-}
+// Slots of a 32-deep step. An operand read from a row holds elements 8 grp..
+// 8 grp + 7 of 32 in slots 0..7 (one 16-byte read). A state tile pair is laid out
+// to match, so that its accumulators are the other operand as they stand: row
+// 4 grp + e of tile t is channel 32 (t / 2) + 8 grp + 4 (t % 2) + e. Tokens keep
+// the order of Mma<bf16_t>::kidx (16 rows to a transposing read), and the scores
+// are stored in it.
+__device__ __forceinline__ int state_channel(int t, int grp) { return 32 * (t >> 1) + 8 * grp + 4 * (t & 1); }
+__device__ __forceinline__ bf16x8_t row_frag(const bf16_t *src) { return *reinterpret_cast<const bf16x8_t *>(src); }
 
 // acc += A B over the parts of both that matter: with three parts on either
 // side, products of parts i and j with i + j <= 2.
@@ -72,6 +74,21 @@ __device__ __forceinline__ f32x4_t mma_parts(const bf16x8_t (&a)[NA], const bf16
 // boundary behind the segment (kState).
 enum WalkMode : int { kOut = 0, kState = 1, kDots = 2 };
 
+// y[i] += S^T x_i over the parts of both that matter, part by part: products
+// into one accumulator lie NC apart.
+template <int NC, int NA, int NB_>
+__device__ __forceinline__ void mma_rows(const bf16x8_t (&s)[NA], const bf16x8_t (&x)[NC][NB_], f32x4_t (&y)[NC]) {
+  constexpr int M = NA > NB_ ? NA : NB_;
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = NB_ - 1; j >= 0; --j)
+      if (i + j < M) {
+#pragma unroll
+        for (int r = 0; r < NC; ++r) y[r] = Mma<bf16_t>::mma(s[i], x[r][j], y[r]);
+      }
+}
+
 // Geometry of one walk.
 template <typename T, int PT_, int NW_, int OPL_, int MODE_>
 struct WalkCfg {
@@ -81,18 +98,21 @@ struct WalkCfg {
   static constexpr int C = (F32 || PT == 256) ? 32 : 64;
   static constexpr int NC = C / 16, KS = C / 32, PS = PT / 32, NT = PT / 16, QT = 16 * NW;
   static constexpr int HELPERS = 4, THREADS = 64 * (NW + HELPERS), HT = 64 * HELPERS;
-  // row strides: 16 bytes past a multiple of 128 (of scores: 8 bytes), so that the 8-byte operand reads
-  // of 16 rows by two lane groups fall into 64 different banks
-  static constexpr int LDX = PT + 8, LDW = QT + 8, LDP = C + 4;
+  // Row strides are 32 bytes past a multiple of 128. LDS instructions measured
+  // on MI355X at this stride, in cycles a wave with eight waves reading: 16 rows
+  // by 16-byte reads 4.5 (8.0 at 16 bytes past), transposing reads at 8-byte
+  // steps 3.2, at 16-byte steps 4.2 (8.0); two 8-byte reads in one instruction 32.
+  static constexpr int LDX = PT + 16, LDW = QT + 16, LDP = C + 16;
   static constexpr int XPL = C * LDX, WPL = C * LDW, PPL = C * LDP;  // elements of one part
   static constexpr unsigned nX = MODE != kState ? 2u * IN * XPL : 0u, nZ = 2u * IN * XPL, nW = 2u * IN * WPL;
   static constexpr unsigned rows = nX + nZ + nW;  // one chunk's rows
   static constexpr unsigned nP = MODE != kState ? 2u * OPL * PPL : 0u;
   static constexpr unsigned tab = 4u * (4 * 64 + 4);  // hi, lo, a, c of every row, and the chunk's decay
   static constexpr unsigned red = MODE == kDots ? 4u * NW * 64 + 64 : 64u;  // row dots of every wave; <h, dh>
-  // two chunks' rows and scores where they fit
-  static constexpr int NBUF = 2 * (rows + nP + tab) + red <= 160 * 1024 ? 2 : 1;
-  static constexpr unsigned oP = NBUF * rows, oTab = oP + NBUF * nP, oRed = oTab + 2 * tab, total = oRed + red;
+  // two chunks' rows, and two chunks' scores, where they fit
+  static constexpr int NBUF = 2 * rows + nP + 2 * tab + red <= 160 * 1024 ? 2 : 1;
+  static constexpr int PBUF = NBUF == 2 && 2 * (rows + nP + tab) + red <= 160 * 1024 ? 2 : 1;
+  static constexpr unsigned oP = NBUF * rows, oTab = oP + PBUF * nP, oRed = oTab + 2 * tab, total = oRed + red;
   static_assert(total <= 160 * 1024, "LDS");
 };
 
@@ -139,18 +159,21 @@ struct RowsMove {
 
 // NW state waves each keep 16 columns of the state; four helper waves, one a
 // SIMD beside two state waves, bring rows to LDS, form decays and the scores.
-// With two LDS buffers a chunk takes two periods between barriers:
-//   state waves   y = a (x S) of chunk c        | w decayed, y += scores w, y out, S updated
+// A chunk takes two periods between barriers:
+//   state waves   y = a (x S) of chunk c        | y += scores w, y out, S updated and
+//                 w decayed                     | split for the next x S
 //   helper waves  rows of c + 1 (loaded a chunk | scores of c + 1
 //                 ago) to LDS, its decays, the
 //                 loads of c + 2
-// so the state's chain holds no load, no decay and no score. With one buffer
-// (fp32 rows from 128 wide) the scores are those of c, beside a (x S), and the
-// next rows go to LDS in a period of their own. Products that give y and scores
-// are taken transposed, so that a lane holds four neighbouring columns of one
-// row and both leave in 8-byte pieces.
+// so the state's chain holds no load, no decay and no score. Where LDS holds one
+// chunk's scores the helpers form those of c beside a (x S) and bring c + 1
+// afterwards; where it holds one chunk's rows (fp32 from 128 wide), those go to
+// LDS in a period of their own. Products that give y and scores are taken
+// transposed, so that a lane holds four neighbouring columns of one row and both
+// leave in 8-byte pieces.
 template <typename T, int PT, int NW, bool REV, int OPL, int MODE>
-__global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p) {
+__global__ __launch_bounds__(64 * (NW + 4)) __attribute__((amdgpu_waves_per_eu((NW + 4) / 4, (NW + 4) / 4)))
+void linear_walk_kernel(LinearWalk p) {
   using F = WalkCfg<T, PT, NW, OPL, MODE>;
   constexpr int C = F::C, NC = F::NC, KS = F::KS, IN = F::IN, QT = F::QT, NB = NC * (NC + 1) / 2;
   using MX = RowsMove<T, F::HT, C, PT>;
@@ -187,7 +210,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
   auto rows_of = [&](int cc) { return (REV ? cc == 0 : cc == nch - 1) ? tail : C; };
   auto rows_at = [&](int cc) { return reinterpret_cast<bf16_t *>(smem + (F::NBUF == 2 && (cc & 1) ? F::rows : 0u)); };
   auto scores_at = [&](int cc) {
-    return reinterpret_cast<bf16_t *>(smem + F::oP + (F::NBUF == 2 && (cc & 1) ? F::nP : 0u));
+    return reinterpret_cast<bf16_t *>(smem + F::oP + (F::PBUF == 2 && (cc & 1) ? F::nP : 0u));
   };
   auto tab_at = [&](int cc) { return reinterpret_cast<float *>(smem + F::oTab + ((cc & 1) ? F::tab : 0u)); };
   float *const sRed = reinterpret_cast<float *>(smem + F::oRed), *const sAnc = sRed + (MODE == kDots ? NW * 64 : 0);
@@ -203,7 +226,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
     const uint32_t gx = MX::lane_offset(ht, ldx, P), gw = MW::lane_offset(ht, ldw, ncol);
     const uint32_t rx = (uint32_t)(MX::RPI * ldx * SZ), rw = (uint32_t)(MW::RPI * ldw * SZ);
     const int px = MX::lds_offset(ht, F::LDX), pw = MW::lds_offset(ht, F::LDW);
-    const int ax = l16 * F::LDX + 4 * grp;  // a row of x or z as an operand
+    const int ax = l16 * F::LDX + 8 * grp;  // a row of x or z as an operand
     const T *xf = reinterpret_cast<const T *>(p.x) + (first * p.Hx + h / (p.H / p.Hx)) * P;
     const T *zf = reinterpret_cast<const T *>(p.z) + (first * p.Hx + h / (p.H / p.Hx)) * P;
     const T *wf = reinterpret_cast<const T *>(p.w) + (first * p.Hw + h / (p.H / p.Hw)) * Q + col0;
@@ -294,7 +317,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
             const bool keep = i != j || (REV ? 4 * grp + e >= l16 : 4 * grp + e <= l16);
             v[e] = keep ? acc[e] * (fast_exp2(d) * p.scale) : 0.f;
           }
-          bf16_t *dst = sP + (16 * ri + l16) * F::LDP + 16 * cj + 4 * grp;
+          bf16_t *dst = sP + (16 * ri + l16) * F::LDP + 32 * (cj >> 1) + 8 * grp + 4 * (cj & 1);
 #pragma unroll
           for (int pl = 0; pl < OPL; ++pl) {
             const bf16x4_t part = to_bf16x4(v);
@@ -327,11 +350,11 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
     if (nch > 0) fetch(0);
     if constexpr (MODE != kState) {
       // the blocks of the scores beyond the triangle stay zero
-      for (int i = ht; i < (int)(F::NBUF * F::nP / 4); i += F::HT) reinterpret_cast<unsigned *>(smem + F::oP)[i] = 0u;
+      for (int i = ht; i < (int)(F::PBUF * F::nP / 4); i += F::HT) reinterpret_cast<unsigned *>(smem + F::oP)[i] = 0u;
     }
     if (nch > 0) bring(0);
     __syncthreads();
-    if constexpr (F::NBUF == 2 && MODE != kState) {
+    if constexpr (F::PBUF == 2 && MODE != kState) {
       if (nch > 0) scores(0);
       __syncthreads();
       for (int cc = 0; cc < nch; ++cc) {
@@ -345,17 +368,17 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
     } else {
       for (int cc = 0; cc < nch; ++cc) {
         if constexpr (MODE != kState) {
+          if (MODE == kDots && cc > 0) dots(cc - 1);
           scores(cc);
           __syncthreads();
           if (MODE == kDots && REV) anchor(cc);
         }
         if constexpr (F::NBUF == 1) __syncthreads();
-        if constexpr (MODE == kDots) dots(cc);
         if (cc + 1 < nch) bring(cc + 1);
         __syncthreads();
       }
     }
-    if (MODE == kDots && F::NBUF == 2 && nch > 0) dots(nch - 1);
+    if (MODE == kDots && nch > 0) dots(nch - 1);
     if (MODE == kState && hw == DW && lane == 0 && cb == 0) p.seg_decay[sg.out * p.H + h] = total;
     if (MODE == kDots && p.end_dot && sg.out < 0) {
       __syncthreads();
@@ -373,7 +396,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
   const int64_t frag = ((int64_t)h * ncb + cb) * (PT * QT) + ((int64_t)wave * F::NT * 64 + lane) * 4;
   const int64_t fragH = (int64_t)p.H * ncb * (PT * QT);  // elements of one boundary
 
-  // ---- the state at the segment's start: rows 16t + 4 grp + e of column q ----
+  // ---- the state at the segment's start: channels state_channel(t, grp) + e of column q ----
   f32x4_t S[F::NT];
   if (MODE != kState && sg.in >= 0) {
     const float *src = p.seg_state + sg.in * fragH + frag;
@@ -389,7 +412,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
     for (int t = 0; t < F::NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int r = 16 * t + 4 * grp + e;
+        const int r = state_channel(t, grp) + e;
         S[t][e] = (from && r < P && q < Q) ? p.s0[sbase + r * p.sp + q * p.sq] : 0.f;
       }
     if (MODE == kState && sg.in < 0 && p.seg_first) {
@@ -399,9 +422,9 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
     }
   }
 
-  const int ax = l16 * F::LDX + 4 * grp;  // a row of x as an operand
-  const int tz = cfrag_lane_off(F::LDX), tw = cfrag_lane_off(F::LDW) + 16 * wave;
-  const int ap = l16 * F::LDP + 4 * grp;  // a row of the scores
+  const int ax = l16 * F::LDX + 8 * grp;  // a row of x as an operand
+  const int tz = (4 * grp + (l16 >> 2)) * F::LDX + 8 * (l16 & 3), tw = cfrag_lane_off(F::LDW) + 16 * wave;
+  const int ap = l16 * F::LDP + 8 * grp;  // a row of the scores
   // y and its partner u: four neighbouring columns of row l16 of each 16
   const int ldu = p.Hu * Q, ldy = p.H * Q, ysz = SZ == 4 || p.y_f32 ? 4 : 2;
   const bool yin = 16 * wave + 4 * grp < ncol;
@@ -414,35 +437,48 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
   f32x4_t y[NC];
   bf16x4_t uh[NC];
   f32x4_t uf[NC];
-  auto times_state = [&](int cc) {  // y = a (x S)
-    const bf16_t *const sX = rows_at(cc);
+  // The state as an operand of x S: split beside the matrix products that update
+  // it, so that x S starts with products; split there where 256 rows of state
+  // leave no registers to hold it.
+  constexpr bool KEEP = MODE != kState && PT <= 128;
+  bf16x8_t sb[KEEP ? F::PS : 1][OPL];
+  auto split_state = [&](int s) {
+    const float sv[8] = {S[2 * s][0], S[2 * s][1], S[2 * s][2], S[2 * s][3],
+                         S[2 * s + 1][0], S[2 * s + 1][1], S[2 * s + 1][2], S[2 * s + 1][3]};
+    split8<OPL>(sv, sb[KEEP ? s : 0]);
+  };
+  if constexpr (KEEP) {
+#pragma unroll
+    for (int s = 0; s < F::PS; ++s) split_state(s);
+  }
+  // w as an operand, and decayed to the chunk's end in three parts
+  bf16x8_t wf[KS][IN], wc[KS][3];
+  auto decay_w = [&](int cc, int s) {
+    const bf16_t *const sW = rows_at(cc) + (F::nX + F::nZ) / 2;
     const float *const tab = tab_at(cc);
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < NC; ++i) y[i] = zero4();
+    for (int pl = IN - 1; pl >= 0; --pl) {
+      wf[s][pl] = load_frag32_at(sW + pl * F::WPL + 32 * s * F::LDW, F::LDW, tw);
 #pragma unroll
-    for (int s = 0; s < F::PS; ++s) {
-      bf16x8_t sb[OPL];
-      const float sv[8] = {S[2 * s][0], S[2 * s][1], S[2 * s][2], S[2 * s][3],
-                           S[2 * s + 1][0], S[2 * s + 1][1], S[2 * s + 1][2], S[2 * s + 1][3]};
-      split8<OPL>(sv, sb);
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        bf16x8_t a[IN];
-#pragma unroll
-        for (int pl = 0; pl < IN; ++pl) a[pl] = row_frag(sX + pl * F::XPL + 16 * i * F::LDX + ax + 32 * s);
-        y[i] = mma_parts(sb, a, y[i]);
-      }
+      for (int e = 0; e < 8; ++e) x[e] += static_cast<float>(wf[s][pl][e]);
     }
+    const f32x4_t c0 = *reinterpret_cast<const f32x4_t *>(tab + 192 + 32 * s + 4 * grp);
+    const f32x4_t c1 = *reinterpret_cast<const f32x4_t *>(tab + 192 + 32 * s + 16 + 4 * grp);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) y[i] *= tab[128 + 16 * i + l16];
+    for (int e = 0; e < 4; ++e) {
+      x[e] *= c0[e];
+      x[e + 4] *= c1[e];
+    }
+    split8<3>(x, wc[s]);
   };
 
   __syncthreads();
-  if constexpr (F::NBUF == 2 && MODE != kState) __syncthreads();
+  if constexpr (F::PBUF == 2 && MODE != kState) __syncthreads();
   for (int cc = 0; cc < nch; ++cc) {
     const int L = rows_of(cc);
     const int64_t t0 = first + (int64_t)cc * STEP;
-    const bf16_t *const sZ = rows_at(cc) + F::nX / 2, *const sW = sZ + F::nZ / 2;
+    const bf16_t *const sX = rows_at(cc), *const sZ = sX + F::nX / 2;
     const float *const tab = tab_at(cc);
 
     if constexpr (MODE != kState) {
@@ -470,29 +506,26 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
           else uf[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
         }
       }
-      times_state(cc);
+      // ---- y = a (x S), and w's parts beside the products ----
+#pragma unroll
+      for (int i = 0; i < NC; ++i) y[i] = zero4();
+#pragma unroll
+      for (int s = 0; s < F::PS; ++s) {
+        bf16x8_t a[NC][IN];
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+          for (int pl = 0; pl < IN; ++pl) a[i][pl] = row_frag(sX + pl * F::XPL + 16 * i * F::LDX + ax + 32 * s);
+        if (s < KS) decay_w(cc, s);
+        if constexpr (!KEEP) split_state(s);
+        mma_rows<NC>(sb[KEEP ? s : 0], a, y);
+      }
+#pragma unroll
+      for (int i = 0; i < NC; ++i) y[i] *= tab[128 + 16 * i + l16];
       __syncthreads();
-    }
-
-    // ---- w as an operand, and decayed to the chunk's end in three parts ----
-    bf16x8_t wf[KS][IN], wc[KS][3];
+    } else {
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int pl = IN - 1; pl >= 0; --pl) {
-        wf[s][pl] = load_frag32_at(sW + pl * F::WPL + 32 * s * F::LDW, F::LDW, tw);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] += static_cast<float>(wf[s][pl][e]);
-      }
-      const f32x4_t c0 = *reinterpret_cast<const f32x4_t *>(tab + 192 + 32 * s + 4 * grp);
-      const f32x4_t c1 = *reinterpret_cast<const f32x4_t *>(tab + 192 + 32 * s + 16 + 4 * grp);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] *= c0[e];
-        x[e + 4] *= c1[e];
-      }
-      split8<3>(x, wc[s]);
+      for (int s = 0; s < KS; ++s) decay_w(cc, s);
     }
 
     if constexpr (MODE != kState) {
@@ -500,19 +533,32 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
       const bf16_t *const sP = scores_at(cc);
       const auto rs = tile_rsrc(yc, (uint32_t)(((L - 1) * ldy + ncol) * ysz));
       yc += dy;
+      // every operand first, so that their reads are in flight together
+      bf16x8_t a[NC][KS][OPL];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
+      for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int s = REV ? i / 2 : 0; s <= (REV ? KS - 1 : i / 2); ++s) {
-          bf16x8_t a[OPL];
+        for (int s = REV ? i / 2 : 0; s <= (REV ? KS - 1 : i / 2); ++s)
 #pragma unroll
-          for (int pl = 0; pl < OPL; ++pl) a[pl] = row_frag(sP + pl * F::PPL + 16 * i * F::LDP + ap + 32 * s);
-          y[i] = mma_parts(wf[s], a, y[i]);
-        }
-        const int off = (int)(gy + 16 * i * ldy * ysz);
-        if (ysz == 4) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y[i]), rs, off, 0, 0);
-        else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, to_bf16x4(y[i])), rs, off, 0, 0);
-        if constexpr (MODE == kDots) {  // this wave's columns of the row's dot; u is zero past the width
+          for (int pl = 0; pl < OPL; ++pl) a[i][s][pl] = row_frag(sP + pl * F::PPL + 16 * i * F::LDP + ap + 32 * s);
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          if (REV ? s >= i / 2 : s <= i / 2) y[i] = mma_parts(wf[s], a[i][s], y[i]);
+      if (ysz == 4) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y[i]), rs, (int)(gy + 16 * i * ldy * ysz), 0, 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, to_bf16x4(y[i])), rs,
+                                                (int)(gy + 16 * i * ldy * ysz), 0, 0);
+      }
+      if constexpr (MODE == kDots) {  // this wave's columns of the rows' dots; u is zero past the width
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
           const f32x4_t u = SZ == 2 ? to_f32x4(uh[i]) : uf[i];
           float d = (y[i][0] * u[0] + y[i][1] * u[1]) + (y[i][2] * u[2] + y[i][3] * u[3]);
           d += __shfl_xor(d, 16);
@@ -531,9 +577,10 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
       for (int s = 0; s < KS; ++s) {
         bf16x8_t a[IN];
 #pragma unroll
-        for (int pl = 0; pl < IN; ++pl) a[pl] = load_frag32_at(sZ + pl * F::XPL + 32 * s * F::LDX + 16 * t, F::LDX, tz);
+        for (int pl = 0; pl < IN; ++pl) a[pl] = load_frag32_at(sZ + pl * F::XPL + 32 * s * F::LDX + state_channel(t, 0), F::LDX, tz);
         S[t] = mma_parts(a, wc[s], S[t]);
       }
+      if (KEEP && (t & 1)) split_state(t / 2);
     }
     if (!REV && anchored(t0, L)) {
       float *dst = p.ckpt + ((t0 + L) / kLinearAnchor) * fragH + frag;
@@ -554,7 +601,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
       for (int t = 0; t < F::NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int r = 16 * t + 4 * grp + e;
+          const int r = state_channel(t, grp) + e;
           if (r < P && q < Q) p.sT[sbase + r * p.sp + q * p.sq] = S[t][e];
         }
     }
@@ -564,7 +611,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) void linear_walk_kernel(LinearWalk p
       for (int t = 0; t < F::NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int r = 16 * t + 4 * grp + e;
+          const int r = state_channel(t, grp) + e;
           if (r < P && q < Q) d += S[t][e] * p.s_dot[sbase + r * p.sp + q * p.sq];
         }
 #pragma unroll
