@@ -89,6 +89,31 @@ __device__ __forceinline__ void mma_rows(const bf16x8_t (&s)[NA], const bf16x8_t
       }
 }
 
+// Inclusive sum over the wave's 64 lanes in fp64: within rows of 16 by row
+// shifts, across them by the broadcasts of a row's and a half's last lane, all
+// on the VALU (lane shuffles through the LDS unit took four times as long).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_or_zero(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_scan(double x) {
+  x += dpp_or_zero<0x111, 0xf>(x);  // row_shr:1, 2, 4, 8
+  x += dpp_or_zero<0x112, 0xf>(x);
+  x += dpp_or_zero<0x114, 0xf>(x);
+  x += dpp_or_zero<0x118, 0xf>(x);
+  x += dpp_or_zero<0x142, 0xa>(x);  // row_bcast:15 into rows 1 and 3
+  x += dpp_or_zero<0x143, 0xc>(x);  // row_bcast:31 into rows 2 and 3
+  return x;
+}
+__device__ __forceinline__ double last_lane(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
 // Geometry of one walk.
 template <typename T, int PT_, int NW_, int OPL_, int MODE_>
 struct WalkCfg {
@@ -112,6 +137,10 @@ struct WalkCfg {
   // two chunks' rows, and two chunks' scores, where they fit
   static constexpr int NBUF = 2 * rows + nP + 2 * tab + red <= 160 * 1024 ? 2 : 1;
   static constexpr int PBUF = NBUF == 2 && 2 * (rows + nP + tab) + red <= 160 * 1024 ? 2 : 1;
+  // y leaves through x's place in LDS, which its chunk no longer needs, so that
+  // the helpers store whole rows (a state wave's 32-byte pieces of 16 rows cost
+  // four times the address work)
+  static constexpr bool STAGE = !F32 && MODE != kState && NBUF == 2 && QT <= PT;
   static constexpr unsigned oP = NBUF * rows, oTab = oP + PBUF * nP, oRed = oTab + 2 * tab, total = oRed + red;
   static_assert(total <= 160 * 1024, "LDS");
 };
@@ -259,12 +288,8 @@ void linear_walk_kernel(LinearWalk p) {
       if (hw != DW) return;
       double b = (double)fg * 1.4426950408889634073599;
       if (b <= -160.0) b = -32768.0;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const double up = __shfl_up(b, off);
-        if (lane >= off) b += up;
-      }
-      const double bl = __shfl(b, 63);
+      b = wave_scan(b);
+      const double bl = last_lane(b);
       const double hi = rint(b);
       const float from = fast_exp2((float)b), rest = fast_exp2((float)(bl - b));
       float *t = tab_at(cc);
@@ -292,7 +317,7 @@ void linear_walk_kernel(LinearWalk p) {
 #pragma unroll
       for (int b0 = 0; b0 < NB; b0 += F::HELPERS) {
         const int blk = b0 + hw;
-        if (blk < NB) {
+        if (b0 + F::HELPERS <= NB || blk < NB) {
           const int i = blk < 1 ? 0 : (blk < 3 ? 1 : (blk < 6 ? 2 : 3)), j = blk - i * (i + 1) / 2;
           const int ri = REV ? j : i, cj = REV ? i : j;
           const bf16_t *xs = sX + 16 * ri * F::LDX + ax, *zs = sZ + 16 * cj * F::LDX + ax;
@@ -327,6 +352,25 @@ void linear_walk_kernel(LinearWalk p) {
         }
       }
     };
+    // y of chunk cc, row by row, from where the state waves left it: a thread
+    // reads the places that its own rows of x go to next
+    const int ldy = p.H * Q;
+    const int yr = ht / MX::VPR, yq = (ht % MX::VPR) * MX::EPV;
+    const uint32_t gy = yq < ncol && yq < QT ? (uint32_t)((yr * ldy + yq) * 2) : kOffNone;
+    char *yc = reinterpret_cast<char *>(p.y) + ((first * p.H + h) * Q + col0) * 2;
+    const int64_t dy = (int64_t)STEP * ldy * 2;
+    auto store_rows = [&](int cc) {
+      if (p.y_f32) return;
+      const auto rs = tile_rsrc(yc, (uint32_t)(((rows_of(cc) - 1) * ldy + ncol) * 2));
+      yc += dy;
+      const bf16_t *s = rows_at(cc) + px;
+      u32x4_t v[MX::IT];
+#pragma unroll
+      for (int it = 0; it < MX::IT; ++it) v[it] = *reinterpret_cast<const u32x4_t *>(s + it * MX::RPI * F::LDX);
+#pragma unroll
+      for (int it = 0; it < MX::IT; ++it)
+        __builtin_amdgcn_raw_buffer_store_b128(v[it], rs, (int)(gy + it * MX::RPI * ldy * 2), 0, 0);
+    };
     auto dots = [&](int cc) {  // the row dots of chunk cc: every state wave's part
       const int L = rows_of(cc);
       if (ht < L) {
@@ -359,6 +403,7 @@ void linear_walk_kernel(LinearWalk p) {
       __syncthreads();
       for (int cc = 0; cc < nch; ++cc) {
         if (MODE == kDots && cc > 0) dots(cc - 1);
+        if (F::STAGE && cc > 0) store_rows(cc - 1);
         if (cc + 1 < nch) bring(cc + 1);
         __syncthreads();
         if (MODE == kDots && REV) anchor(cc);
@@ -369,6 +414,7 @@ void linear_walk_kernel(LinearWalk p) {
       for (int cc = 0; cc < nch; ++cc) {
         if constexpr (MODE != kState) {
           if (MODE == kDots && cc > 0) dots(cc - 1);
+          if (F::STAGE && cc > 0) store_rows(cc - 1);
           scores(cc);
           __syncthreads();
           if (MODE == kDots && REV) anchor(cc);
@@ -379,6 +425,7 @@ void linear_walk_kernel(LinearWalk p) {
       }
     }
     if (MODE == kDots && nch > 0) dots(nch - 1);
+    if (F::STAGE && nch > 0) store_rows(nch - 1);
     if (MODE == kState && hw == DW && lane == 0 && cb == 0) p.seg_decay[sg.out * p.H + h] = total;
     if (MODE == kDots && p.end_dot && sg.out < 0) {
       __syncthreads();
@@ -546,7 +593,11 @@ void linear_walk_kernel(LinearWalk p) {
 #pragma unroll
         for (int i = 0; i < NC; ++i)
           if (REV ? s >= i / 2 : s <= i / 2) y[i] = mma_parts(wf[s], a[i][s], y[i]);
-      if (ysz == 4) {
+      if (F::STAGE && ysz == 2) {
+        bf16_t *dst = rows_at(cc) + l16 * F::LDX + 16 * wave + 4 * grp;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) *reinterpret_cast<bf16x4_t *>(dst + 16 * i * F::LDX) = to_bf16x4(y[i]);
+      } else if (ysz == 4) {
 #pragma unroll
         for (int i = 0; i < NC; ++i)
           __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, y[i]), rs, (int)(gy + 16 * i * ldy * ysz), 0, 0);
