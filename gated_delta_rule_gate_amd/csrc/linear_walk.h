@@ -250,6 +250,8 @@ void linear_walk_kernel(LinearWalk p) {
 
   if (wave >= NW) {
     // =================================== helper waves ===================================
+    // what a helper holds up, eight state waves wait for (1.5 to 3.5% shorter walks)
+    __builtin_amdgcn_s_setprio(2);
     const int hw = wave - NW, ht = tid - 64 * NW;
     const int ldx = p.Hx * P, ldw = p.Hw * Q;  // row strides, elements
     const uint32_t gx = MX::lane_offset(ht, ldx, P), gw = MW::lane_offset(ht, ldw, ncol);
@@ -356,7 +358,6 @@ void linear_walk_kernel(LinearWalk p) {
     // reads the places that its own rows of x go to next
     const int ldy = p.H * Q;
     const int yr = ht / MX::VPR, yq = (ht % MX::VPR) * MX::EPV;
-    const uint32_t gy = yq < ncol && yq < QT ? (uint32_t)((yr * ldy + yq) * 2) : kOffNone;
     char *yc = reinterpret_cast<char *>(p.y) + ((first * p.H + h) * Q + col0) * 2;
     const int64_t dy = (int64_t)STEP * ldy * 2;
     auto store_rows = [&](int cc) {
@@ -369,7 +370,10 @@ void linear_walk_kernel(LinearWalk p) {
       for (int it = 0; it < MX::IT; ++it) v[it] = *reinterpret_cast<const u32x4_t *>(s + it * MX::RPI * F::LDX);
 #pragma unroll
       for (int it = 0; it < MX::IT; ++it)
-        __builtin_amdgcn_raw_buffer_store_b128(v[it], rs, (int)(gy + it * MX::RPI * ldy * 2), 0, 0);
+      {
+        const int r = yr + it * MX::RPI, c = yq ^ (((r >> 3) & 1) * 8);  // where the state waves put it
+        __builtin_amdgcn_raw_buffer_store_b128(v[it], rs, c < ncol && yq < QT ? (r * ldy + c) * 2 : (int)kOffNone, 0, 0);
+      }
     };
     auto dots = [&](int cc) {  // the row dots of chunk cc: every state wave's part
       const int L = rows_of(cc);
@@ -594,7 +598,8 @@ void linear_walk_kernel(LinearWalk p) {
         for (int i = 0; i < NC; ++i)
           if (REV ? s >= i / 2 : s <= i / 2) y[i] = mma_parts(wf[s], a[i][s], y[i]);
       if (F::STAGE && ysz == 2) {
-        bf16_t *dst = rows_at(cc) + l16 * F::LDX + 16 * wave + 4 * grp;
+        // rows 8..15 of 16 swap 16-byte neighbours: 16 rows then cover all banks
+        bf16_t *dst = rows_at(cc) + l16 * F::LDX + ((16 * wave + 4 * grp) ^ (l16 & 8));
 #pragma unroll
         for (int i = 0; i < NC; ++i) *reinterpret_cast<bf16x4_t *>(dst + 16 * i * F::LDX) = to_bf16x4(y[i]);
       } else if (ysz == 4) {
