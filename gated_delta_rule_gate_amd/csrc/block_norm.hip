@@ -13,9 +13,9 @@
 //
 // Bound by the bytes of the rows: each input is read once into registers, the
 // row sums are taken there, and each output is written once. A row of D values
-// is held by LPR lanes, NV vectors of eight values each (at most two: the
-// backward holds eight such sets): up to 1024 values by part of a wave or a
-// wave (no barrier), longer rows by a whole workgroup of 256 to 1024 threads. Parameter gradients stay in registers while a workgroup walks its
+// is held by LPR lanes of eight values each: up to 512 values by part of a wave
+// or a wave (no barrier), longer rows by a whole workgroup of 128 to 1024
+// threads, which past 8192 values take two vectors a lane (NV). Parameter gradients stay in registers while a workgroup walks its
 // rows; its sums go to the workspace and are added over workgroups in order.
 #include "kda_device.h"
 #include "linear_launch.h"
@@ -57,7 +57,7 @@ __device__ __forceinline__ void fill8(float (&x)[8], float v) {
 
 // Sums of a row's lanes: within the wave by shuffles, over a workgroup's waves
 // through LDS (two buffers in turn, so one barrier a sum is enough).
-constexpr int block_threads(int lpr) { return lpr > 256 ? lpr : 256; }
+constexpr int block_threads(int lpr) { return lpr >= 128 ? lpr : 256; }
 
 template <int LPR, int NS>
 __device__ __forceinline__ void row_sums(float (&s)[NS], float (*red)[2][16], int &turn) {
@@ -154,45 +154,115 @@ __global__ __launch_bounds__(block_threads(LPR)) void block_norm_fwd_kernel(Bloc
   }
 }
 
-template <typename Tx, typename Tr, int LPR, int NV>
+// Eight values as they lie in memory.
+template <typename T>
+struct Raw8 {
+  u32x4_t v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const void *p, int64_t at) {
+    const u32x4_t *src = reinterpret_cast<const u32x4_t *>(reinterpret_cast<const T *>(p) + at);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v[i] = src[i];
+  }
+  __device__ __forceinline__ void get(float (&x)[8], bool ok) const {  // zeros where !ok
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      unsigned u;
+      if constexpr (sizeof(T) == 2) u = e & 1 ? v[0][e / 2] & 0xffff0000u : v[0][e / 2] << 16;
+      else u = v[e / 4][e % 4];
+      x[e] = __uint_as_float(ok ? u : 0u);
+    }
+  }
+};
+
+// The next rows' loads are in flight while a workgroup computes on its rows:
+// with the registers this takes, few waves share a SIMD, and their number alone
+// does not cover the loads (262144 x 128 with a SiLU gate: 169 us without).
+template <typename Tx, typename Tr, int LPR, int NV, bool NEXT>
 __global__ __launch_bounds__(block_threads(LPR)) void block_norm_bwd_kernel(BlockNorm p) {
   constexpr int RPB = block_threads(LPR) / LPR;
   __shared__ float red[2][2][16];
   int turn = 0;
   const int lane = threadIdx.x % LPR;
   const float inv = p.l2 ? 1.0f : 1.0f / (float)p.D, inv2 = 1.0f / (float)p.D;
-  float aw[NV][8], as[NV][8], an[NV][8];  // sums over this lane's rows
+  const bool has_dy = p.dy, has_gate = p.gate, has_res = p.residual;
+  float aw[NV][8], as[NV][8], an[NEXT ? NV : 1][8];  // sums over this lane's rows
+  // 1024 threads leave 128 registers each: none for the next rows or for the
+  // weights, which then come from the cache for every row.
+  constexpr bool AHEAD = LPR < 1024;
+  float w[NV][8], sc[NV][8], w2[NEXT ? NV : 1][8];
+  auto weights = [&]() {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = min((v * LPR + lane) * 8, p.D - 8);
+      fill8(w[v], 1.f);
+      fill8(sc[v], p.scale);
+      if (p.weight) load8<float>(p.weight, c, w[v]);
+      if (p.scale_vec) load8<float>(p.scale_vec, c, sc[v]);
+      if constexpr (NEXT) {
+        fill8(w2[v], 1.f);
+        if (p.next_weight) load8<float>(p.next_weight, c, w2[v]);
+      }
+    }
+  };
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     fill8(aw[v], 0.f);
     fill8(as[v], 0.f);
-    fill8(an[v], 0.f);
+    if constexpr (NEXT) fill8(an[v], 0.f);
   }
-  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.rows; row0 += (int64_t)gridDim.x * RPB) {
-    const int64_t row = row0 + threadIdx.x / LPR;
-    const bool live = row < p.rows;
-    const int64_t base = row * p.D;
-    float x[NV][8], gt[NV][8], t[NV][8], y[NV][8], dz[NV][8];
+  if constexpr (AHEAD) weights();
+  Raw8<Tx> rx[NV], rg[NV], rz[NEXT ? NV : 1];
+  Raw8<Tr> rt[NV], rr[NEXT ? NV : 1];
+  auto fetch = [&](int64_t row0) {  // rows and columns past the end repeat the last
+    const int64_t base = min(row0 + threadIdx.x / LPR, p.rows - 1) * p.D;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = (v * LPR + lane) * 8;
-      fill8(x[v], 0.f);
-      fill8(gt[v], 0.f);
-      fill8(t[v], 0.f);
-      fill8(y[v], 0.f);
-      fill8(dz[v], 0.f);
-      if (live && c < p.D) {
-        load8<Tx>(p.x, base + c, x[v]);
-        if (p.gate) load8<Tx>(p.gate, base + c, gt[v]);
-        if (p.dy) load8<Tr>(p.dy, base + c, t[v]);
-        if (p.dz) {
-          load8<Tx>(p.dz, base + c, dz[v]);
-          if (p.residual) load8<Tr>(p.residual, base + c, y[v]);
-        }
+      const int64_t at = base + min((v * LPR + lane) * 8, p.D - 8);
+      rx[v].load(p.x, at);
+      if (has_gate) rg[v].load(p.gate, at);
+      if (has_dy) rt[v].load(p.dy, at);
+      if constexpr (NEXT) {
+        rz[v].load(p.dz, at);
+        if (has_res) rr[v].load(p.residual, at);
       }
     }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row0 = (int64_t)blockIdx.x * RPB;
+  if (AHEAD && row0 < p.rows) fetch(row0);
+  for (; row0 < p.rows; row0 += step) {
+    if constexpr (!AHEAD) {
+      fetch(row0);
+      weights();
+    }
+    const int64_t row = row0 + threadIdx.x / LPR;
+    const int64_t base = row * p.D;
+    float x[NV][8], gt[NV][8], t[NV][8], y[NEXT ? NV : 1][8], dz[NEXT ? NV : 1][8];
+    bool ok[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      ok[v] = row < p.rows && (v * LPR + lane) * 8 < p.D;
+      rx[v].get(x[v], ok[v]);
+      rg[v].get(gt[v], ok[v] && has_gate);
+      rt[v].get(t[v], ok[v] && has_dy);
+      if constexpr (NEXT) {
+        rz[v].get(dz[v], ok[v]);
+        rr[v].get(y[v], ok[v] && has_res);
+      }
+    }
+    if (AHEAD && row0 + step < p.rows) fetch(row0 + step);
+
+    float act[NV][8], dact[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float g = gt[v][e], sg = sigmoid_f32(g), ds = sg * (1.0f - sg);
+        act[v][e] = !has_gate ? 1.f : (p.silu ? g * sg : sg);
+        dact[v][e] = p.silu ? sg + g * ds : ds;
+      }
     float rho = 0.f;
-    if (p.dz) {
+    if constexpr (NEXT) {
       float s[1] = {0.f};
 #pragma unroll
       for (int v = 0; v < NV; ++v)
@@ -202,89 +272,52 @@ __global__ __launch_bounds__(block_threads(LPR)) void block_norm_bwd_kernel(Bloc
       rho = 1.0f / sqrtf(s[0] * inv + p.eps);
       float s2[2] = {0.f, 0.f};
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int c = (v * LPR + lane) * 8;
-        if (!live || c >= p.D) continue;
-        float w[8], sc[8], w2[8];
-        if (p.weight) load8<float>(p.weight, c, w);
-        else fill8(w, 1.f);
-        if (p.scale_vec) load8<float>(p.scale_vec, c, sc);
-        else fill8(sc, p.scale);
-        if (p.next_weight) load8<float>(p.next_weight, c, w2);
-        else fill8(w2, 1.f);
+      for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float n = x[v][e] * rho * w[e];
-          if (p.gate) n *= act_of(p.silu, gt[v][e]);
-          y[v][e] += n * sc[e];
+          y[v][e] += x[v][e] * rho * w[v][e] * act[v][e] * sc[v][e];
           s2[0] += y[v][e] * y[v][e];
-          s2[1] += y[v][e] * dz[v][e] * w2[e];
+          s2[1] += y[v][e] * dz[v][e] * w2[v][e];
         }
-      }
       row_sums<LPR, 2>(s2, red, turn);
       const float rho2 = 1.0f / sqrtf(s2[0] * inv2 + p.eps), m = s2[1] * inv2 * rho2 * rho2;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int c = (v * LPR + lane) * 8;
-        if (!live || c >= p.D) continue;
-        float w2[8];
-        if (p.next_weight) load8<float>(p.next_weight, c, w2);
-        else fill8(w2, 1.f);
+      for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           an[v][e] += dz[v][e] * y[v][e] * rho2;
-          t[v][e] += rho2 * (dz[v][e] * w2[e] - y[v][e] * m);
+          t[v][e] += rho2 * (dz[v][e] * w2[v][e] - y[v][e] * m);
         }
-      }
     }
-    // t is the whole gradient of y from here on; what follows turns it into dn
+    // t is the whole gradient of y from here on
     float s3[2] = {0.f, 0.f};
-    float dgv[NV][8];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = (v * LPR + lane) * 8;
-      if (!live || c >= p.D) continue;
-      if (p.dresidual) store8<Tr>(p.dresidual, base + c, t[v]);
-      float w[8], sc[8];
-      if (p.weight) load8<float>(p.weight, c, w);
-      else fill8(w, 1.f);
-      if (p.scale_vec) load8<float>(p.scale_vec, c, sc);
-      else fill8(sc, p.scale);
+      if (p.dresidual && ok[v]) store8<Tr>(p.dresidual, base + (v * LPR + lane) * 8, t[v]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        float act = 1.f, dact = 0.f;
-        if (p.gate) {
-          const float g = gt[v][e], sg = sigmoid_f32(g), ds = sg * (1.0f - sg);
-          act = p.silu ? g * sg : sg;
-          dact = p.silu ? sg + g * ds : ds;
-        }
-        const float xw = x[v][e] * w[e];  // n / rho
-        dgv[v][e] = t[v][e] * sc[e] * xw * dact;  // dgate / rho
-        y[v][e] = t[v][e] * xw * act;             // d scale / rho
-        t[v][e] *= sc[e] * act;                   // dn
         s3[0] += x[v][e] * x[v][e];
-        s3[1] += t[v][e] * xw;
+        s3[1] += t[v][e] * sc[v][e] * act[v][e] * x[v][e] * w[v][e];
       }
     }
     row_sums<LPR, 2>(s3, red, turn);
-    if (!p.dz) rho = 1.0f / sqrtf(s3[0] * inv + p.eps);
+    if constexpr (!NEXT) rho = 1.0f / sqrtf(s3[0] * inv + p.eps);
     const float m = s3[1] * inv * rho * rho;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = (v * LPR + lane) * 8;
-      if (!live || c >= p.D) continue;
-      float w[8];
-      if (p.weight) load8<float>(p.weight, c, w);
-      else fill8(w, 1.f);
+      float dg[8], dx[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        aw[v][e] += t[v][e] * x[v][e] * rho;
-        as[v][e] += y[v][e] * rho;
-        dgv[v][e] *= rho;
-        w[e] = rho * (t[v][e] * w[e] - x[v][e] * m);
+        const float xr = x[v][e] * rho, n = xr * w[v][e], dn = t[v][e] * sc[v][e] * act[v][e];
+        aw[v][e] += dn * xr;
+        as[v][e] += t[v][e] * n * act[v][e];
+        dg[e] = t[v][e] * sc[v][e] * n * dact[v][e];
+        dx[e] = rho * (dn * w[v][e] - x[v][e] * m);
       }
-      if (p.dgate) store8<Tx>(p.dgate, base + c, dgv[v]);
-      store8<Tx>(p.dx, base + c, w);
+      if (ok[v]) {
+        if (p.dgate) store8<Tx>(p.dgate, base + (v * LPR + lane) * 8, dg);
+        store8<Tx>(p.dx, base + (v * LPR + lane) * 8, dx);
+      }
     }
   }
 
@@ -293,11 +326,11 @@ __global__ __launch_bounds__(block_threads(LPR)) void block_norm_bwd_kernel(Bloc
   __shared__ float sums[RPB > 1 ? 256 : 1][8];
   float *const wanted[3] = {p.dweight, p.dscale_vec, p.dnext_weight};
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < (NEXT ? 3 : 2); ++i) {
     if (!wanted[i]) continue;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float(&a)[8] = i == 0 ? aw[v] : (i == 1 ? as[v] : an[v]);
+      float(&a)[8] = i == 0 ? aw[v] : (i == 1 ? as[v] : an[NEXT ? v : 0]);
       const int c = (v * LPR + lane) * 8;
       if constexpr (RPB > 1) {
         __syncthreads();
@@ -317,28 +350,37 @@ __global__ __launch_bounds__(block_threads(LPR)) void block_norm_bwd_kernel(Bloc
   }
 }
 
-// Sums over the workgroups' parts: 64 columns a workgroup, four waves each
-// taking every fourth part.
-__global__ __launch_bounds__(256) void block_norm_params_kernel(BlockNorm p, int blocks) {
-  __shared__ double red[4][64];
+// Sums over the workgroups' parts in a fixed order: 64 columns a workgroup,
+// sixteen waves each taking every sixteenth part, eight parts in flight (one
+// part at a time, a wave's loads alone took 60 us for 1024 parts).
+__global__ __launch_bounds__(1024) void block_norm_params_kernel(BlockNorm p, int blocks) {
+  __shared__ double red[16][64];
   float *const wanted[3] = {p.dweight, p.dscale_vec, p.dnext_weight};
   float *out = wanted[blockIdx.y];
   if (!out) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * 64 + lane;
+  const float *src = p.part + (int64_t)blockIdx.y * p.D + min(c, p.D - 1);
   double s = 0.0;
-  if (c < p.D)
-    for (int b = wave; b < blocks; b += 4) s += (double)p.part[((int64_t)b * 3 + blockIdx.y) * p.D + c];
+  for (int b = wave; b < blocks; b += 128) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = src[(int64_t)min(b + 16 * i, blocks - 1) * 3 * p.D];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += b + 16 * i < blocks ? (double)v[i] : 0.0;
+  }
   red[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && c < p.D) out[c] = (float)((red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]));
+  if (wave == 0 && c < p.D) {
+    for (int w = 1; w < 16; ++w) s += red[w][lane];
+    out[c] = (float)s;
+  }
 }
 
 // Lanes a row.
 int row_lanes(int D) {
-  if (D > 1024) return D <= 2048 ? 256 : (D <= 8192 ? 512 : 1024);
   int lpr = 1;
-  while (lpr < 64 && lpr * 8 < D) lpr *= 2;
+  while (lpr < 1024 && lpr * 8 < D) lpr *= 2;
   return lpr;
 }
 
@@ -347,7 +389,7 @@ int row_lanes(int D) {
 int bwd_blocks(int64_t rows, int D) {
   const int lpr = row_lanes(D), rpb = block_threads(lpr) / lpr;
   const int64_t need = (rows + rpb - 1) / rpb;
-  const int64_t most = (int64_t)device_cus() * (D > 2048 ? 2 : 4);
+  const int64_t most = (int64_t)device_cus() * (D > 2048 ? 2 : (D > 512 ? 1024 / lpr : 4));
   return (int)(need < most ? (need > 0 ? need : 1) : most);
 }
 
@@ -357,7 +399,10 @@ hipError_t launch_nv(const BlockNorm &p, bool bwd, hipStream_t st) {
   const int64_t need = (p.rows + RPB - 1) / RPB;
   if (bwd) {
     const int blocks = bwd_blocks(p.rows, p.D);
-    hipLaunchKernelGGL((block_norm_bwd_kernel<Tx, Tr, LPR, NV>), dim3(blocks), dim3(block_threads(LPR)), 0, st, p);
+    if (p.dz)
+      hipLaunchKernelGGL((block_norm_bwd_kernel<Tx, Tr, LPR, NV, true>), dim3(blocks), dim3(block_threads(LPR)), 0, st, p);
+    else
+      hipLaunchKernelGGL((block_norm_bwd_kernel<Tx, Tr, LPR, NV, false>), dim3(blocks), dim3(block_threads(LPR)), 0, st, p);
   } else {
     if (need == 0) return hipSuccess;
     const int64_t grid = need < 0x7fffffff ? need : 0x7fffffff;
@@ -375,10 +420,11 @@ hipError_t launch_rows(const BlockNorm &p, bool bwd, hipStream_t st) {
     case 8: return launch_nv<Tx, Tr, 8, 1>(p, bwd, st);
     case 16: return launch_nv<Tx, Tr, 16, 1>(p, bwd, st);
     case 32: return launch_nv<Tx, Tr, 32, 1>(p, bwd, st);
-    case 64: return p.D <= 512 ? launch_nv<Tx, Tr, 64, 1>(p, bwd, st) : launch_nv<Tx, Tr, 64, 2>(p, bwd, st);
+    case 64: return launch_nv<Tx, Tr, 64, 1>(p, bwd, st);
+    case 128: return launch_nv<Tx, Tr, 128, 1>(p, bwd, st);
     case 256: return launch_nv<Tx, Tr, 256, 1>(p, bwd, st);
-    case 512: return p.D <= 4096 ? launch_nv<Tx, Tr, 512, 1>(p, bwd, st) : launch_nv<Tx, Tr, 512, 2>(p, bwd, st);
-    default: return launch_nv<Tx, Tr, 1024, 2>(p, bwd, st);
+    case 512: return launch_nv<Tx, Tr, 512, 1>(p, bwd, st);
+    default: return p.D <= 8192 ? launch_nv<Tx, Tr, 1024, 1>(p, bwd, st) : launch_nv<Tx, Tr, 1024, 2>(p, bwd, st);
   }
 }
 
@@ -398,7 +444,7 @@ hipError_t launch_block_norm_fwd(const BlockNorm &p, hipStream_t st) { return la
 hipError_t launch_block_norm_bwd(const BlockNorm &p, hipStream_t st) {
   hipError_t e = launch_types(p, true, st);
   if (e != hipSuccess || !(p.dweight || p.dscale_vec || p.dnext_weight)) return e;
-  hipLaunchKernelGGL(block_norm_params_kernel, dim3((p.D + 63) / 64, 3), dim3(256), 0, st, p,
+  hipLaunchKernelGGL(block_norm_params_kernel, dim3((p.D + 63) / 64, 3), dim3(1024), 0, st, p,
                      bwd_blocks(p.rows, p.D));
   return hipGetLastError();
 }
