@@ -14,8 +14,8 @@
 // Bound by the bytes of the rows: each input is read once into registers, the
 // row sums are taken there, and each output is written once. A row of D values
 // is held by LPR lanes of eight values each: up to 512 values by part of a wave
-// or a wave (no barrier), longer rows by a whole workgroup of 128 to 1024
-// threads, which past 8192 values take two vectors a lane (NV). Parameter gradients stay in registers while a workgroup walks its
+// or a wave (no barrier), longer rows by a whole workgroup of 128 to 512
+// threads, which past 4096 values take two or four vectors a lane (NV). Parameter gradients stay in registers while a workgroup walks its
 // rows; its sums go to the workspace and are added over workgroups in order.
 #include "kda_device.h"
 #include "linear_launch.h"
@@ -163,6 +163,11 @@ struct Raw8 {
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v[i] = src[i];
   }
+  // hides the value's origin, so that its uses on either side are converted apart
+  __device__ __forceinline__ void renew() {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) asm volatile("" : "+v"(v[i]));
+  }
   __device__ __forceinline__ void get(float (&x)[8], bool ok) const {  // zeros where !ok
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -186,31 +191,34 @@ __global__ __launch_bounds__(block_threads(LPR)) void block_norm_bwd_kernel(Bloc
   const float inv = p.l2 ? 1.0f : 1.0f / (float)p.D, inv2 = 1.0f / (float)p.D;
   const bool has_dy = p.dy, has_gate = p.gate, has_res = p.residual;
   float aw[NV][8], as[NV][8], an[NEXT ? NV : 1][8];  // sums over this lane's rows
-  // 1024 threads leave 128 registers each: none for the next rows or for the
-  // weights, which then come from the cache for every row.
-  constexpr bool AHEAD = LPR < 1024;
-  float w[NV][8], sc[NV][8], w2[NEXT ? NV : 1][8];
-  auto weights = [&]() {
+  // One vector a lane leaves registers for the next rows and for the weights;
+  // with more, weights come from the cache for every use, and inputs stay as
+  // they lie in memory until used.
+  constexpr bool AHEAD = NV == 1;
+  float kw[AHEAD ? 3 : 1][8];
+  auto weight_of = [&](int i, int v, float(&o)[8]) {  // 0: weight, 1: scale, 2: next weight
+    const float *const src[3] = {p.weight, p.scale_vec, p.next_weight};
+    fill8(o, i == 1 ? p.scale : 1.f);
+    if (src[i]) load8<float>(src[i], min((v * LPR + lane) * 8, p.D - 8), o);
+  };
+  auto weight = [&](int i, int v, float(&o)[8]) {
+    if constexpr (AHEAD) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = min((v * LPR + lane) * 8, p.D - 8);
-      fill8(w[v], 1.f);
-      fill8(sc[v], p.scale);
-      if (p.weight) load8<float>(p.weight, c, w[v]);
-      if (p.scale_vec) load8<float>(p.scale_vec, c, sc[v]);
-      if constexpr (NEXT) {
-        fill8(w2[v], 1.f);
-        if (p.next_weight) load8<float>(p.next_weight, c, w2[v]);
-      }
+      for (int e = 0; e < 8; ++e) o[e] = kw[i][e];
+    } else {
+      weight_of(i, v, o);
     }
   };
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int i = 0; i < (NEXT ? 3 : 2); ++i) weight_of(i, 0, kw[i]);
+  }
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     fill8(aw[v], 0.f);
     fill8(as[v], 0.f);
     if constexpr (NEXT) fill8(an[v], 0.f);
   }
-  if constexpr (AHEAD) weights();
   Raw8<Tx> rx[NV], rg[NV], rz[NEXT ? NV : 1];
   Raw8<Tr> rt[NV], rr[NEXT ? NV : 1];
   auto fetch = [&](int64_t row0) {  // rows and columns past the end repeat the last
@@ -231,88 +239,127 @@ __global__ __launch_bounds__(block_threads(LPR)) void block_norm_bwd_kernel(Bloc
   int64_t row0 = (int64_t)blockIdx.x * RPB;
   if (AHEAD && row0 < p.rows) fetch(row0);
   for (; row0 < p.rows; row0 += step) {
-    if constexpr (!AHEAD) {
-      fetch(row0);
-      weights();
-    }
+    if constexpr (!AHEAD) fetch(row0);
     const int64_t row = row0 + threadIdx.x / LPR;
     const int64_t base = row * p.D;
-    float x[NV][8], gt[NV][8], t[NV][8], y[NEXT ? NV : 1][8], dz[NEXT ? NV : 1][8];
+    Raw8<Tx> cx[NV], cg[NV], cz[NEXT ? NV : 1];
+    float t[NV][8], y[NEXT ? NV : 1][8];
     bool ok[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       ok[v] = row < p.rows && (v * LPR + lane) * 8 < p.D;
-      rx[v].get(x[v], ok[v]);
-      rg[v].get(gt[v], ok[v] && has_gate);
+      cx[v] = rx[v];
+      cg[v] = rg[v];
       rt[v].get(t[v], ok[v] && has_dy);
       if constexpr (NEXT) {
-        rz[v].get(dz[v], ok[v]);
+        cz[v] = rz[v];
         rr[v].get(y[v], ok[v] && has_res);
       }
     }
     if (AHEAD && row0 + step < p.rows) fetch(row0 + step);
 
-    float act[NV][8], dact[NV][8];
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
+    // act(gate) and its derivative; no gate: 1 and 0
+    auto gate = [&](int v, float(&act)[8], float(&dact)[8]) {
+      cg[v].get(act, has_gate);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float g = gt[v][e], sg = sigmoid_f32(g), ds = sg * (1.0f - sg);
-        act[v][e] = !has_gate ? 1.f : (p.silu ? g * sg : sg);
-        dact[v][e] = p.silu ? sg + g * ds : ds;
+        const float g = act[e], sg = sigmoid_f32(g), ds = sg * (1.0f - sg);
+        act[e] = !has_gate ? 1.f : (p.silu ? g * sg : sg);
+        dact[e] = p.silu ? sg + g * ds : ds;
       }
+    };
+    // between the passes over a row, wide rows keep neither converted inputs nor
+    // weights: held, they spill (8192 x 8192: 850 us)
+    auto apart = [&]() {
+      if constexpr (AHEAD) return;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        cx[v].renew();
+        cg[v].renew();
+        if constexpr (NEXT) cz[v].renew();
+      }
+      asm volatile("" ::: "memory");
+    };
     float rho = 0.f;
     if constexpr (NEXT) {
       float s[1] = {0.f};
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+      for (int v = 0; v < NV; ++v) {
+        float x[8];
+        cx[v].get(x, ok[v]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[0] += x[v][e] * x[v][e];
+        for (int e = 0; e < 8; ++e) s[0] += x[e] * x[e];
+      }
       row_sums<LPR, 1>(s, red, turn);
       rho = 1.0f / sqrtf(s[0] * inv + p.eps);
+      apart();
       float s2[2] = {0.f, 0.f};
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+      for (int v = 0; v < NV; ++v) {
+        float x[8], w[8], sc[8], w2[8], act[8], dact[8], dz[8];
+        cx[v].get(x, ok[v]);
+        cz[v].get(dz, ok[v]);
+        weight(0, v, w);
+        weight(1, v, sc);
+        weight(2, v, w2);
+        gate(v, act, dact);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          y[v][e] += x[v][e] * rho * w[v][e] * act[v][e] * sc[v][e];
+          y[v][e] += x[e] * rho * w[e] * act[e] * sc[e];
           s2[0] += y[v][e] * y[v][e];
-          s2[1] += y[v][e] * dz[v][e] * w2[v][e];
+          s2[1] += y[v][e] * dz[e] * w2[e];
         }
+      }
       row_sums<LPR, 2>(s2, red, turn);
       const float rho2 = 1.0f / sqrtf(s2[0] * inv2 + p.eps), m = s2[1] * inv2 * rho2 * rho2;
+      apart();
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+      for (int v = 0; v < NV; ++v) {
+        float w2[8], dz[8];
+        cz[v].get(dz, ok[v]);
+        weight(2, v, w2);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          an[v][e] += dz[v][e] * y[v][e] * rho2;
-          t[v][e] += rho2 * (dz[v][e] * w2[v][e] - y[v][e] * m);
+          an[v][e] += dz[e] * y[v][e] * rho2;
+          t[v][e] += rho2 * (dz[e] * w2[e] - y[v][e] * m);
         }
+      }
     }
     // t is the whole gradient of y from here on
+    apart();
     float s3[2] = {0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      float x[8], w[8], sc[8], act[8], dact[8];
+      cx[v].get(x, ok[v]);
+      weight(0, v, w);
+      weight(1, v, sc);
+      gate(v, act, dact);
       if (p.dresidual && ok[v]) store8<Tr>(p.dresidual, base + (v * LPR + lane) * 8, t[v]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        s3[0] += x[v][e] * x[v][e];
-        s3[1] += t[v][e] * sc[v][e] * act[v][e] * x[v][e] * w[v][e];
+        s3[0] += x[e] * x[e];
+        s3[1] += t[v][e] * sc[e] * act[e] * x[e] * w[e];
       }
     }
     row_sums<LPR, 2>(s3, red, turn);
     if constexpr (!NEXT) rho = 1.0f / sqrtf(s3[0] * inv + p.eps);
     const float m = s3[1] * inv * rho * rho;
+    apart();
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float dg[8], dx[8];
+      float x[8], w[8], sc[8], act[8], dact[8], dg[8], dx[8];
+      cx[v].get(x, ok[v]);
+      weight(0, v, w);
+      weight(1, v, sc);
+      gate(v, act, dact);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float xr = x[v][e] * rho, n = xr * w[v][e], dn = t[v][e] * sc[v][e] * act[v][e];
+        const float xr = x[e] * rho, n = xr * w[e], dn = t[v][e] * sc[e] * act[e];
         aw[v][e] += dn * xr;
-        as[v][e] += t[v][e] * n * act[v][e];
-        dg[e] = t[v][e] * sc[v][e] * n * dact[v][e];
-        dx[e] = rho * (dn * w[v][e] - x[v][e] * m);
+        as[v][e] += t[v][e] * n * act[e];
+        dg[e] = t[v][e] * sc[e] * n * dact[e];
+        dx[e] = rho * (dn * w[e] - x[e] * m);
       }
       if (ok[v]) {
         if (p.dgate) store8<Tx>(p.dgate, base + (v * LPR + lane) * 8, dg);
@@ -380,7 +427,7 @@ __global__ __launch_bounds__(1024) void block_norm_params_kernel(BlockNorm p, in
 // Lanes a row.
 int row_lanes(int D) {
   int lpr = 1;
-  while (lpr < 1024 && lpr * 8 < D) lpr *= 2;
+  while (lpr < 512 && lpr * 8 < D) lpr *= 2;
   return lpr;
 }
 
@@ -389,7 +436,7 @@ int row_lanes(int D) {
 int bwd_blocks(int64_t rows, int D) {
   const int lpr = row_lanes(D), rpb = block_threads(lpr) / lpr;
   const int64_t need = (rows + rpb - 1) / rpb;
-  const int64_t most = (int64_t)device_cus() * (D > 2048 ? 2 : (D > 512 ? 1024 / lpr : 4));
+  const int64_t most = (int64_t)device_cus() * (D > 4096 ? 1 : (D > 512 ? 1024 / lpr : 4));
   return (int)(need < most ? (need > 0 ? need : 1) : most);
 }
 
@@ -423,8 +470,9 @@ hipError_t launch_rows(const BlockNorm &p, bool bwd, hipStream_t st) {
     case 64: return launch_nv<Tx, Tr, 64, 1>(p, bwd, st);
     case 128: return launch_nv<Tx, Tr, 128, 1>(p, bwd, st);
     case 256: return launch_nv<Tx, Tr, 256, 1>(p, bwd, st);
-    case 512: return launch_nv<Tx, Tr, 512, 1>(p, bwd, st);
-    default: return p.D <= 8192 ? launch_nv<Tx, Tr, 1024, 1>(p, bwd, st) : launch_nv<Tx, Tr, 1024, 2>(p, bwd, st);
+    default:
+      if (p.D <= 4096) return launch_nv<Tx, Tr, 512, 1>(p, bwd, st);
+      return p.D <= 8192 ? launch_nv<Tx, Tr, 512, 2>(p, bwd, st) : launch_nv<Tx, Tr, 512, 4>(p, bwd, st);
   }
 }
 
