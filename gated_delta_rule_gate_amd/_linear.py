@@ -52,29 +52,40 @@ def _lib():
     return _READY
 
 
+def _refuse(name, t, shape, dtype, device):
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError("%s must be %s %s, got %s %s" % (name, dtype, list(shape), t.dtype, list(t.shape)))
+    if not t.is_cuda or t.device != device:
+        raise ValueError("%s must be on %s" % (name, device if device.type == "cuda" else "a GPU"))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    raise RuntimeError("%s requires grad: this op does not track gradients; call its _bwd for them" % name)
+
+
 def _tensor(name, t, shape, dtype, device):
     """A tensor's pointer, after its checks; None for None."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError("%s must be %s %s, got %s %s" % (name, dtype, list(shape), t.dtype, list(t.shape)))
-    if not t.is_cuda or t.device != device:
-        raise ValueError("%s must be on %s" % (name, device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    if t.requires_grad:
-        raise RuntimeError("%s requires grad: this op does not track gradients; call its _bwd for them" % name)
+    if (t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_cuda or t.requires_grad
+            or not t.is_contiguous()):
+        _refuse(name, t, shape, dtype, device)
     return t.data_ptr()
 
 
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _launch(device, entry, *args):
-    """One entry point on the device's current stream."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        check(entry(*args, stream))
+    """One entry point on the device's current stream (its handle read without building a
+    Stream object, which costs as much as the launch of a single-token step)."""
+    i = device.index
+    if _current_device() == i:
+        status = entry(*args, _current_stream(i))
     else:
         with torch.cuda.device(device):
-            check(entry(*args, stream))
+            status = entry(*args, _current_stream(i))
+    if status:
+        check(status)
 
 
 def _attn_args(q, k, v, g, h0, cu_seqlens, scale):
