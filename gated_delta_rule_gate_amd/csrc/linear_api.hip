@@ -55,13 +55,11 @@ struct SegPlan {
   size_t total() const { return align_up(state) + align_up(decay) + align_up(first); }
 };
 
-SegPlan seg_plan(const kda_linear_args *a, bool packed, int P, int Q) {
+SegPlan seg_plan(const kda_linear_args *a, bool packed, int Q, bool dots) {
   SegPlan s;
-  s.seg = kda::linear_segment(a->T, a->N, a->H, Q, packed);
+  s.seg = kda::linear_segment(a->T, a->N, a->H, Q, packed, dots);
   if (!s.seg) return s;
-  int ncb;
-  const int qt = kda::linear_cols(Q, &ncb);
-  const size_t elems = (size_t)a->H * ncb * kda::linear_tile(P) * qt;
+  const size_t elems = (size_t)a->H * a->K * a->V;
   const size_t bounds = (size_t)((int64_t)a->B * a->T / s.seg + 1);
   s.state = 4 * bounds * elems;
   s.decay = 8 * bounds * a->H;
@@ -94,7 +92,7 @@ kda::LinearWalk walk_base(const kda_linear_args *a, const float *g, const int32_
 
 // The backward's workspace.
 struct BwdPlan {
-  SegPlan dq, dv, dk;
+  SegPlan seg;  // of all three walks: dk's starts from the boundary states of dv's
   size_t segs, ckpt, dots, adot, edot, heads, part;
   int ncb;
   int64_t anchors, items;
@@ -106,10 +104,8 @@ struct BwdPlan {
 
 BwdPlan bwd_plan(const kda_linear_args *a, bool packed) {
   BwdPlan b;
-  b.dq = seg_plan(a, packed, a->V, a->K);
-  b.dv = seg_plan(a, packed, a->K, a->V);
-  b.dk = b.dq;
-  b.segs = std::max(b.dq.total(), b.dv.total());
+  b.seg = seg_plan(a, packed, a->K, true);
+  b.segs = b.seg.total();
   const int qt = kda::linear_cols(a->K, &b.ncb);
   const int64_t rows = (int64_t)a->B * a->T;
   b.anchors = rows / kda::kLinearAnchor + 1;
@@ -133,8 +129,8 @@ bool maybe_packed(const kda_linear_args *a) { return a->B == 1; }
 extern "C" size_t kda_linear_chunk_workspace_bytes(const kda_linear_args *a) {
   if (check_sizes(a) != KDA_OK) return 0;
   size_t n = 0;
-  if (maybe_dense(a)) n = std::max(n, seg_plan(a, false, a->K, a->V).total());
-  if (maybe_packed(a)) n = std::max(n, seg_plan(a, true, a->K, a->V).total());
+  if (maybe_dense(a)) n = std::max(n, seg_plan(a, false, a->V, false).total());
+  if (maybe_packed(a)) n = std::max(n, seg_plan(a, true, a->V, false).total());
   return n;
 }
 
@@ -143,7 +139,7 @@ extern "C" kda_status kda_linear_chunk_fwd(const kda_linear_args *a, const void 
                                            void *workspace, size_t ws_bytes, void *stream) {
   const kda_status s = check_common(a, q, k, v, g, h0, cu, o, ht);
   if (s != KDA_OK) return s;
-  const SegPlan plan = seg_plan(a, cu != nullptr, a->K, a->V);
+  const SegPlan plan = seg_plan(a, cu != nullptr, a->V, false);
   if (plan.total() > 0 && (!workspace || ws_bytes < plan.total())) return KDA_ERR_WORKSPACE;
   if (plan.total() > 0 && !aligned256(workspace)) return KDA_ERR_ALIGN;
   kda::LinearWalk w = walk_base(a, g, cu);
@@ -220,28 +216,10 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   w.s_dot = dht;
   w.end_dot = dht ? edot : nullptr;
   w.ckpt = ckpt;
-  set_segments(w, b.dq, segs, false);
+  set_segments(w, b.seg, segs, false);
   hipError_t e = kda::launch_linear_walk(w, st);
   if (e == hipSuccess && shared)
     e = kda::launch_linear_group_sum(heads, dq, w.is_bf16, cu, a->N, rows, a->H, Hk, a->K, st);
-  if (e != hipSuccess) return kda::report_hip(e);
-
-  // dk: the reverse walk of dh^T, with <h, dh> at the anchors
-  w.reverse = true;
-  w.x = v;
-  w.z = d_o;
-  w.w = q;
-  w.u = k;
-  w.y = shared ? static_cast<void *>(heads) : dk;
-  w.dot = dot_k;
-  w.s0 = dht;
-  w.s_dot = nullptr;
-  w.end_dot = nullptr;
-  w.anchor_dot = adot;
-  set_segments(w, b.dk, segs, false);
-  e = kda::launch_linear_walk(w, st);
-  if (e == hipSuccess && shared)
-    e = kda::launch_linear_group_sum(heads, dk, w.is_bf16, cu, a->N, rows, a->H, Hk, a->K, st);
   if (e != hipSuccess) return kda::report_hip(e);
 
   // dv: the reverse walk of dh, which ends in dh0
@@ -259,8 +237,27 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   r.sT = dh0;
   r.sp = a->V;
   r.sq = 1;
-  set_segments(r, b.dv, segs, false);
+  set_segments(r, b.seg, segs, false);
   e = kda::launch_linear_walk(r, st);
+  if (e != hipSuccess) return kda::report_hip(e);
+
+  // dk: the reverse walk of dh^T, with <h, dh> at the anchors
+  w.reverse = true;
+  w.x = v;
+  w.z = d_o;
+  w.w = q;
+  w.u = k;
+  w.y = shared ? static_cast<void *>(heads) : dk;
+  w.dot = dot_k;
+  w.s0 = dht;
+  w.s_dot = nullptr;
+  w.end_dot = nullptr;
+  w.anchor_dot = adot;
+  set_segments(w, b.seg, segs, false);
+  w.seg_ready = true;  // dv's boundary states, read across
+  e = kda::launch_linear_walk(w, st);
+  if (e == hipSuccess && shared)
+    e = kda::launch_linear_group_sum(heads, dk, w.is_bf16, cu, a->N, rows, a->H, Hk, a->K, st);
   if (e != hipSuccess) return kda::report_hip(e);
 
   kda::LinearDg d{};

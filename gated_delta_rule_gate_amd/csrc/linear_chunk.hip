@@ -141,10 +141,11 @@ int linear_cols(int width, int *ncb) {
   return qt;
 }
 
-// Segments pay where whole sequences leave compute units idle: the state pass
-// reads two of the walk's three inputs once more (about 0.6 of a chunk's
-// time), and the two extra launches cost about as much as eight chunks.
-int linear_segment(int T, int slots, int H, int Q, bool packed) {
+// Segments pay where whole sequences leave compute units idle. Costs in chunks
+// of a walk that has the device to itself (3.3 us with y, 5 us with row dots at
+// 128 wide): a state pass's chunk 0.62 or 0.42 of that; chaining and the two
+// more launches 12 to 20 us.
+int linear_segment(int T, int slots, int H, int Q, bool packed, bool dots) {
   int ncb;
   const int qt = linear_cols(Q, &ncb);
   const int64_t room = (int64_t)device_cus() * (qt == 64 ? 2 : 1);
@@ -154,8 +155,9 @@ int linear_segment(int T, int slots, int H, int Q, bool packed) {
   double best = (double)((pairs + room - 1) / room) * chunks;
   int64_t take = 1;
   for (int64_t s = 2; s <= 64 && chunks / s >= 4; ++s) {
-    const double cost = (double)((pairs * s + room - 1) / room) * ((chunks + s - 1) / s) * 1.6 + 8;
-    if (cost < 0.95 * best) {
+    const double cost = (double)((pairs * s + room - 1) / room) * ((chunks + s - 1) / s) * (dots ? 1.42 : 1.62) +
+                        (dots ? 2.4 : 6.0);
+    if (cost < 0.97 * best) {
       best = cost;
       take = s;
     }
@@ -163,7 +165,8 @@ int linear_segment(int T, int slots, int H, int Q, bool packed) {
   return take == 1 ? 0 : (int)((chunks + take - 1) / take * 64);
 }
 
-hipError_t launch_linear_chain(const LinearWalk &p, bool rev, int64_t elems, hipStream_t st) {
+hipError_t launch_linear_chain(const LinearWalk &p, bool rev, hipStream_t st) {
+  const int64_t elems = (int64_t)p.P * p.Q;
   const int64_t grid = (elems / 4 + 255) / 256 * p.H * p.N;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
   hipLaunchKernelGGL(linear_chain_kernel, dim3((unsigned)grid), dim3(256), 0, st, p, rev, elems);

@@ -54,22 +54,22 @@ struct LinearWalk {
   // segment's own state change (and decay) at the boundary behind it, a second
   // chains them, and the walk of every segment starts from its boundary.
   int seg;
-  float *seg_state;       // [boundary, H, ncb, PT * QT] in operand order
+  bool seg_ready;         // the boundaries hold the states already (of the same walk, or of its transpose)
+  float *seg_state;       // [boundary, H, P x Q], strided as s0
   double *seg_decay;      // [boundary, H] log2
-  float *seg_first;       // copies of s0 where sT is s0 itself, [N, H, ncb, PT * QT], or null
+  float *seg_first;       // copies of s0 where sT is s0 itself, [N, H, P x Q], or null
 };
 
 int linear_tile(int width);              // padded P: 64, 128 or 256
 int linear_cols(int width, int *ncb);    // columns per workgroup (64 or 128) and column blocks
-// tokens per segment for one walk with Q columns, or 0 for none
-int linear_segment(int T, int slots, int H, int Q, bool packed);
+// tokens per segment for one walk with Q columns, or 0 for none; dots: a walk with row dots
+int linear_segment(int T, int slots, int H, int Q, bool packed, bool dots);
 hipError_t launch_linear_walk(const LinearWalk &p, hipStream_t st);
 hipError_t launch_linear_walk_bf16_fwd(const LinearWalk &p, hipStream_t st);
 hipError_t launch_linear_walk_bf16_rev(const LinearWalk &p, hipStream_t st);
 hipError_t launch_linear_walk_f32_fwd(const LinearWalk &p, hipStream_t st);
 hipError_t launch_linear_walk_f32_rev(const LinearWalk &p, hipStream_t st);
-// elems: floats of one (boundary, head)
-hipError_t launch_linear_chain(const LinearWalk &p, bool rev, int64_t elems, hipStream_t st);
+hipError_t launch_linear_chain(const LinearWalk &p, bool rev, hipStream_t st);
 
 // out[rows, Hk, D] = sum over the heads of a group of in[rows, H, D], in order
 hipError_t launch_linear_group_sum(const float *in, void *out, bool is_bf16, const int32_t *cu, int N, int64_t rows,

@@ -460,27 +460,28 @@ void linear_walk_kernel(LinearWalk p) {
 
   // ---- the state at the segment's start: channels state_channel(t, grp) + e of column q ----
   f32x4_t S[F::NT];
-  if (MODE != kState && sg.in >= 0) {
-    const float *src = p.seg_state + sg.in * fragH + frag;
-#pragma unroll
-    for (int t = 0; t < F::NT; ++t) S[t] = *reinterpret_cast<const f32x4_t *>(src + t * 256);
-  } else if (MODE != kState && p.seg_first && sg.out >= 0) {
-    const float *src = p.seg_first + sg.n * fragH + frag;
-#pragma unroll
-    for (int t = 0; t < F::NT; ++t) S[t] = *reinterpret_cast<const f32x4_t *>(src + t * 256);
-  } else {
-    const bool from = p.s0 && sg.in < 0;
+  {
+    // over a boundary, or the sequence's own start: h0 or its copy, made by the
+    // state pass where the final state goes over it
+    const float *src = sg.in >= 0 ? p.seg_state + ((int64_t)sg.in * p.H + h) * P * Q
+                       : MODE != kState && p.seg_first && sg.out >= 0 ? p.seg_first + sbase
+                       : p.s0 ? p.s0 + sbase : nullptr;
+    if (MODE == kState && sg.in >= 0) src = nullptr;  // its own change only
 #pragma unroll
     for (int t = 0; t < F::NT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = state_channel(t, grp) + e;
-        S[t][e] = (from && r < P && q < Q) ? p.s0[sbase + r * p.sp + q * p.sq] : 0.f;
+        S[t][e] = (src && r < P && q < Q) ? src[r * p.sp + q * p.sq] : 0.f;
       }
     if (MODE == kState && sg.in < 0 && p.seg_first) {
-      float *dst = p.seg_first + sg.n * fragH + frag;
 #pragma unroll
-      for (int t = 0; t < F::NT; ++t) *reinterpret_cast<f32x4_t *>(dst + t * 256) = S[t];
+      for (int t = 0; t < F::NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = state_channel(t, grp) + e;
+          if (r < P && q < Q) p.seg_first[sbase + r * p.sp + q * p.sq] = S[t][e];
+        }
     }
   }
 
@@ -584,6 +585,19 @@ void linear_walk_kernel(LinearWalk p) {
       }
 #pragma unroll
       for (int i = 0; i < NC; ++i) y[i] *= tab[128 + 16 * i + l16];
+      // w's parts are formed in this period, beside x S: left to itself the
+      // compiler moves them behind the barrier, before their use (with the dots'
+      // registers it has to: holding them spills)
+      if constexpr (MODE == kOut) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int pl = 0; pl < 3; ++pl) {
+            u32x4_t v = __builtin_bit_cast(u32x4_t, wc[s][pl]);
+            asm volatile("" : "+v"(v));
+            wc[s][pl] = __builtin_bit_cast(bf16x8_t, v);
+          }
+      }
       __syncthreads();
     } else {
 #pragma unroll
@@ -659,9 +673,14 @@ void linear_walk_kernel(LinearWalk p) {
   }
 
   if constexpr (MODE == kState) {
-    float *dst = p.seg_state + sg.out * fragH + frag;
+    float *dst = p.seg_state + ((int64_t)sg.out * p.H + h) * P * Q;
 #pragma unroll
-    for (int t = 0; t < F::NT; ++t) *reinterpret_cast<f32x4_t *>(dst + t * 256) = S[t];
+    for (int t = 0; t < F::NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = state_channel(t, grp) + e;
+        if (r < P && q < Q) dst[r * p.sp + q * p.sq] = S[t][e];
+      }
   } else if (sg.out < 0) {
     if (p.sT && !(nch == 0 && p.sT == p.s0)) {
 #pragma unroll
@@ -709,11 +728,10 @@ hipError_t launch_one(const LinearWalk &p, hipStream_t st) {
 
 template <typename T, int PT, int NW, bool REV, int OPL, int MODE>
 hipError_t launch_modes(const LinearWalk &p, hipStream_t st) {
-  if (p.seg) {
+  if (p.seg && !p.seg_ready) {
     hipError_t e = launch_one<T, PT, NW, REV, 1, kState>(p, st);
     if (e != hipSuccess) return e;
-    const int ncb = (p.Q + 16 * NW - 1) / (16 * NW);
-    if ((e = launch_linear_chain(p, REV, (int64_t)ncb * PT * 16 * NW, st)) != hipSuccess) return e;
+    if ((e = launch_linear_chain(p, REV, st)) != hipSuccess) return e;
   }
   return launch_one<T, PT, NW, REV, OPL, MODE>(p, st);
 }
