@@ -1,6 +1,9 @@
 // Linear attention with one decay per head: the passes round the chunk walk
 // (linear_walk.h) -- chaining segments, summing the gradients of shared q/k
 // heads, the decay's gradient -- and the choice of segments.
+#include <algorithm>
+#include <cmath>
+
 #include "chunk_fused_tiles.h"
 #include "linear_launch.h"
 #include "linear_segments.h"
@@ -141,22 +144,33 @@ int linear_cols(int width, int *ncb) {
   return qt;
 }
 
-// Segments pay where whole sequences leave compute units idle. Costs in chunks
-// of a walk that has the device to itself (3.3 us with y, 5 us with row dots at
-// 128 wide): a state pass's chunk 0.62 or 0.42 of that; chaining and the two
-// more launches 12 to 20 us.
+// Segments pay where whole sequences leave compute units idle (one workgroup
+// each, by LDS). Costs in chunks of a walk that has the device to itself (3.3 us
+// with y, 5 us with row dots at 128 wide): a state pass's chunk 0.62 or 0.42 of
+// that; chaining and two more launches 12 to 20 us.
+// Dense: rounds of equal segments. Packed, lengths unknown: the work shared out
+// evenly plus half a segment behind the last, or one segment if that is longer,
+// and 7 chunks for each segment's start and end, of which every slot adds about
+// 0.6; whole slots are taken to be as long as 2.5 average ones at most. (32
+// heads, 10 slots, 15872 tokens, segments of 512, 1024, 1536, 1984: 259, 236,
+// 223, 249 us; gradient, 16 heads, 7 slots, 4999 tokens, of 320, 512, 768: 192,
+// 175, 217 us.)
 int linear_segment(int T, int slots, int H, int Q, bool packed, bool dots) {
   int ncb;
-  const int qt = linear_cols(Q, &ncb);
-  const int64_t room = (int64_t)device_cus() * (qt == 64 ? 2 : 1);
-  const int64_t pairs = (int64_t)(packed ? 1 : slots) * H * ncb;
+  linear_cols(Q, &ncb);
+  const double room = device_cus();
+  const int64_t pairs = (int64_t)H * ncb;
   const int64_t chunks = (T + 63) / 64;
-  if (pairs < 1 || chunks < 8) return 0;
-  double best = (double)((pairs + room - 1) / room) * chunks;
+  if (slots < 1 || chunks < 8) return 0;
+  const double rate = dots ? 1.42 : 1.62, join = dots ? 2.4 : 6.0;
+  const double share = pairs * chunks / room;
+  double best = packed ? std::max(chunks * std::min(1.0, 2.5 / slots), share)
+                       : std::ceil(pairs * slots / room) * chunks;
   int64_t take = 1;
   for (int64_t s = 2; s <= 64 && chunks / s >= 4; ++s) {
-    const double cost = (double)((pairs * s + room - 1) / room) * ((chunks + s - 1) / s) * (dots ? 1.42 : 1.62) +
-                        (dots ? 2.4 : 6.0);
+    const double len = (double)((chunks + s - 1) / s);
+    const double cost = packed ? std::max(len, share + len / 2) * rate + 7 * pairs * (s + 0.6 * slots) / room + join
+                               : std::ceil(pairs * slots * s / room) * len * rate + join;
     if (cost < 0.97 * best) {
       best = cost;
       take = s;
