@@ -151,9 +151,9 @@ int linear_cols(int width, int *ncb) {
 // Dense: rounds of equal segments. Packed, lengths unknown: the work shared out
 // evenly plus half a segment behind the last, or one segment if that is longer,
 // and 7 chunks for each segment's start and end, of which every slot adds about
-// 0.6; whole slots are taken to be as long as 2.5 average ones at most. (32
-// heads, 10 slots, 15872 tokens, segments of 512, 1024, 1536, 1984: 259, 236,
-// 223, 249 us; gradient, 16 heads, 7 slots, 4999 tokens, of 320, 512, 768: 192,
+// 0.6; the longest slot is taken to be as long as four average ones. (32
+// heads, 10 slots, 15872 tokens, segments of 512, 1024, 1536, 1984, none: 259,
+// 236, 223, 249, 300 us; gradient, 16 heads, 7 slots, 4999 tokens, of 320, 512, 768: 192,
 // 175, 217 us.)
 int linear_segment(int T, int slots, int H, int Q, bool packed, bool dots) {
   int ncb;
@@ -164,14 +164,14 @@ int linear_segment(int T, int slots, int H, int Q, bool packed, bool dots) {
   if (slots < 1 || chunks < 8) return 0;
   const double rate = dots ? 1.42 : 1.62, join = dots ? 2.4 : 6.0;
   const double share = pairs * chunks / room;
-  double best = packed ? std::max(chunks * std::min(1.0, 2.5 / slots), share)
-                       : std::ceil(pairs * slots / room) * chunks;
+  double best = 0.97 * (packed ? std::max(chunks * std::min(1.0, 4.0 / slots), share)
+                               : std::ceil(pairs * slots / room) * chunks);
   int64_t take = 1;
   for (int64_t s = 2; s <= 64 && chunks / s >= 4; ++s) {
     const double len = (double)((chunks + s - 1) / s);
     const double cost = packed ? std::max(len, share + len / 2) * rate + 7 * pairs * (s + 0.6 * slots) / room + join
                                : std::ceil(pairs * slots * s / room) * len * rate + join;
-    if (cost < 0.97 * best) {
+    if (cost < best) {
       best = cost;
       take = s;
     }
