@@ -97,7 +97,7 @@ struct BwdPlan {
   int ncb;
   int64_t anchors, items;
   size_t total() const {
-    return align_up(segs) + align_up(ckpt) + 2 * align_up(dots) + align_up(adot) + align_up(edot) + align_up(heads) +
+    return align_up(segs) + align_up(ckpt) + 4 * align_up(dots) + align_up(adot) + align_up(edot) + align_up(heads) +
            align_up(part);
   }
 };
@@ -189,6 +189,7 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   char *segs = take(b.segs);
   float *ckpt = reinterpret_cast<float *>(take(b.ckpt));
   float *dot_q = reinterpret_cast<float *>(take(b.dots)), *dot_k = reinterpret_cast<float *>(take(b.dots));
+  float *far_q = reinterpret_cast<float *>(take(b.dots)), *far_k = reinterpret_cast<float *>(take(b.dots));
   float *adot = reinterpret_cast<float *>(take(b.adot)), *edot = reinterpret_cast<float *>(take(b.edot));
   float *heads = reinterpret_cast<float *>(take(b.heads));
   double *part = reinterpret_cast<double *>(take(b.part));
@@ -206,6 +207,7 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   w.y = shared ? static_cast<void *>(heads) : dq;
   w.y_f32 = shared;
   w.dot = dot_q;
+  w.dot_far = far_q;
   w.Hx = a->H;
   w.Hw = w.Hu = Hk;
   w.P = a->V;
@@ -249,6 +251,7 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   w.u = k;
   w.y = shared ? static_cast<void *>(heads) : dk;
   w.dot = dot_k;
+  w.dot_far = far_k;
   w.s0 = dht;
   w.s_dot = nullptr;
   w.end_dot = nullptr;
@@ -263,6 +266,9 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   kda::LinearDg d{};
   d.a = dot_q;
   d.b = dot_k;
+  d.a_far = far_q;
+  d.b_far = far_k;
+  d.chunk = kda::linear_chunk_rows(a->V, a->dtype == KDA_BF16);
   d.anchor_dot = adot;
   d.end_dot = dht ? edot : nullptr;
   d.cu = cu;

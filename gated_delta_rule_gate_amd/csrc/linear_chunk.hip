@@ -56,11 +56,10 @@ __global__ __launch_bounds__(256) void linear_group_sum_kernel(const float *in, 
   else *reinterpret_cast<f32x4_t *>(dst) = s;
 }
 
-// dg over one anchored stretch of one (sequence, head): a decay at token t
-// scales every later use of everything before it, which is the sum of
-// q.dq - k.dk from t on; from the stretch's end that sum is <h, dh> there. A
-// wave takes the stretch, a lane kDgPer neighbouring tokens; sums in fp64.
+// dg over one anchored stretch of one (sequence, head): a wave takes the
+// stretch, a lane kDgPer neighbouring tokens, all of one chunk; sums in fp64.
 constexpr int kDgPer = kLinearAnchor / 64;
+static_assert(32 % kDgPer == 0, "a lane's tokens lie in one chunk");
 __global__ __launch_bounds__(256) void linear_dg_kernel(LinearDg p) {
   const int h = (int)(blockIdx.x % ((p.H + 3) / 4)) * 4 + (threadIdx.x >> 6);
   const int64_t item = blockIdx.x / ((p.H + 3) / 4);
@@ -77,13 +76,12 @@ __global__ __launch_bounds__(256) void linear_dg_kernel(LinearDg p) {
   double sum = 0.0;
   if (ok) {
     const int64_t rows = (int64_t)p.B * p.T;
-    double carry = 0.0;
+    double carry = 0.0;  // <h, dh> behind the stretch
     for (int cb = 0; cb < p.ncb; ++cb) {
       if (sg.out >= 0) carry += p.anchor_dot[(sg.out * p.H + h) * p.ncb + cb];
       else if (p.end_dot) carry += p.end_dot[((int64_t)sg.n * p.H + h) * p.ncb + cb];
     }
-    double x[kDgPer];
-    double own = 0.0;
+    double x[kDgPer], own = 0.0, far = 0.0;
 #pragma unroll
     for (int i = 0; i < kDgPer; ++i) {
       const int64_t t = sg.lo + lane * kDgPer + i;
@@ -92,16 +90,25 @@ __global__ __launch_bounds__(256) void linear_dg_kernel(LinearDg p) {
         for (int cb = 0; cb < p.ncb; ++cb) {
           const int64_t at = ((int64_t)cb * p.H + h) * rows + t;
           x[i] += (double)p.a[at] - (double)p.b[at];
+          far += (double)p.a_far[at] - (double)p.b_far[at];
         }
       own += x[i];
     }
-    double after = own;  // of this lane's tokens and all later ones
+    const int lanes = p.chunk / kDgPer, place = lane % lanes;
+    double run = 0.0;  // a - b of the chunk's later lanes
+    for (int off = 1; off < lanes; ++off) {
+      const double v = __shfl_down(own, off);
+      if (place + off < lanes) run += v;
+    }
+    double after = far;  // of this lane's tokens and all later ones
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-      const double dn = __shfl_down(after, off);
-      if (lane + off < 64) after += dn;
+      const double v = __shfl_down(after, off);
+      if (lane + off < 64) after += v;
     }
-    double run = after - own + carry;
+    const int next = lane - place + lanes;  // the next chunk's first lane
+    const double later = __shfl(after, next & 63);
+    run += carry + (next < 64 ? later : 0.0);
 #pragma unroll
     for (int i = kDgPer - 1; i >= 0; --i) {
       run += x[i];
@@ -206,6 +213,8 @@ hipError_t launch_linear_group_sum(const float *in, void *out, bool is_bf16, con
                        reinterpret_cast<float *>(out), cu, N, rows, H, Hk, D);
   return hipGetLastError();
 }
+
+int linear_chunk_rows(int P, bool is_bf16) { return !is_bf16 || linear_tile(P) == 256 ? 32 : 64; }
 
 int64_t linear_dg_items(int B, int T, int N) { return N + ((int64_t)B * T) / kLinearAnchor; }
 

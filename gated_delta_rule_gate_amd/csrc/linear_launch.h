@@ -32,7 +32,8 @@ struct LinearWalk {
   const void *x, *z, *w;  // [rows, Hx, P], [rows, Hx, P], [rows, Hw, Q]
   const void *u;          // [rows, Hu, Q] or null: partner of the row dots
   void *y;                // [rows, H, Q]
-  float *dot;             // [ncb][H][rows]: y_r . u_r in fp32, before y is rounded (with u)
+  float *dot, *dot_far;   // [ncb][H][rows]: y_r . u_r in fp32, before y is rounded, and the part
+                          // of it that comes through the state (with u)
   int Hx, Hw, Hu;
   bool y_f32;             // y is fp32 whatever the type (a head's part, summed over heads later)
   const float *g;
@@ -75,17 +76,23 @@ hipError_t launch_linear_chain(const LinearWalk &p, bool rev, hipStream_t st);
 hipError_t launch_linear_group_sum(const float *in, void *out, bool is_bf16, const int32_t *cu, int N, int64_t rows,
                                    int H, int Hk, int D, hipStream_t st);
 
-// dg from the row dots a = q.dq and b = k.dk: their difference summed from each
-// token to the end of its sequence, anchored at every kLinearAnchor tokens.
+// dg from the row dots a = q.dq and b = k.dk. What a decay at token t scales is
+// the sum of a - b from t to the end of the sequence. Most of it cancels, and so
+// that the cancelled terms' roundings do not add up, that sum runs to the end of
+// t's chunk only; there it is <h, dh>, which is carried over chunks by the dots'
+// parts through the states alone (a chunk's own pairs sum to zero) from every
+// kLinearAnchor-th token, where the states themselves are at hand.
 struct LinearDg {
-  const float *a, *b;  // [ncb][H][rows]
+  const float *a, *b, *a_far, *b_far;  // [ncb][H][rows]
   const float *anchor_dot, *end_dot;  // end_dot null: zero
   const int32_t *cu;
   float *dg;
   double *part;        // head decays: [items][H] sums
   bool g_head;
+  int chunk;           // rows of the walks' chunks
   int B, T, H, N, ncb;
 };
+int linear_chunk_rows(int P, bool is_bf16);
 int64_t linear_dg_items(int B, int T, int N);
 hipError_t launch_linear_dg(const LinearDg &p, hipStream_t st);
 

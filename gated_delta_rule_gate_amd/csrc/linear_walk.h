@@ -114,6 +114,14 @@ __device__ __forceinline__ double last_lane(double x) {
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
+// Sum over the wave's four rows of 16 lanes, in every row (two VALU swaps).
+__device__ __forceinline__ float rows4_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  const unsigned h = __float_as_uint(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+  const auto t = __builtin_amdgcn_permlane32_swap(h, h, false, false);
+  return __uint_as_float(t[0]) + __uint_as_float(t[1]);
+}
+
 // Geometry of one walk.
 template <typename T, int PT_, int NW_, int OPL_, int MODE_>
 struct WalkCfg {
@@ -133,7 +141,7 @@ struct WalkCfg {
   static constexpr unsigned rows = nX + nZ + nW;  // one chunk's rows
   static constexpr unsigned nP = MODE != kState ? 2u * OPL * PPL : 0u;
   static constexpr unsigned tab = 4u * (4 * 64 + 4);  // hi, lo, a, c of every row, and the chunk's decay
-  static constexpr unsigned red = MODE == kDots ? 4u * NW * 64 + 64 : 64u;  // row dots of every wave; <h, dh>
+  static constexpr unsigned red = MODE == kDots ? 2 * 4u * NW * 64 + 64 : 64u;  // row dots of every wave; <h, dh>
   // two chunks' rows, and two chunks' scores, where they fit
   static constexpr int NBUF = 2 * rows + nP + 2 * tab + red <= 160 * 1024 ? 2 : 1;
   static constexpr int PBUF = NBUF == 2 && 2 * (rows + nP + tab) + red <= 160 * 1024 ? 2 : 1;
@@ -242,7 +250,7 @@ void linear_walk_kernel(LinearWalk p) {
     return reinterpret_cast<bf16_t *>(smem + F::oP + (F::PBUF == 2 && (cc & 1) ? F::nP : 0u));
   };
   auto tab_at = [&](int cc) { return reinterpret_cast<float *>(smem + F::oTab + ((cc & 1) ? F::tab : 0u)); };
-  float *const sRed = reinterpret_cast<float *>(smem + F::oRed), *const sAnc = sRed + (MODE == kDots ? NW * 64 : 0);
+  float *const sRed = reinterpret_cast<float *>(smem + F::oRed), *const sAnc = sRed + (MODE == kDots ? 2 * NW * 64 : 0);
   // whole multiples of kLinearAnchor tokens into the sequence, before its end
   auto anchored = [&](int64_t t0, int L) {
     return MODE == kDots && (((uint32_t)(t0 - sg.a) + L) % kLinearAnchor) == 0 && t0 + L < sg.e;
@@ -381,13 +389,14 @@ void linear_walk_kernel(LinearWalk p) {
         __builtin_amdgcn_raw_buffer_store_b128(v[it], rs, c < ncol && yq < QT ? (r * ldy + c) * 2 : (int)kOffNone, 0, 0);
       }
     };
-    auto dots = [&](int cc) {  // the row dots of chunk cc: every state wave's part
-      const int L = rows_of(cc);
-      if (ht < L) {
+    auto dots = [&](int cc) {  // the row dots of chunk cc, whole and of a (x S): every state wave's part
+      const int L = rows_of(cc), r = ht & 63, which = ht >> 6;
+      if (which < 2 && r < L) {
         float d = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) d += sRed[w * 64 + ht];
-        p.dot[((int64_t)cb * p.H + h) * rows + first + (int64_t)cc * STEP + ht] = d;
+        for (int w = 0; w < NW; ++w) d += sRed[(which * NW + w) * 64 + r];
+        float *dst = which ? p.dot_far : p.dot;
+        dst[((int64_t)cb * p.H + h) * rows + first + (int64_t)cc * STEP + r] = d;
       }
     };
     auto anchor = [&](int cc) {  // <h, dh> behind chunk cc
@@ -502,8 +511,8 @@ void linear_walk_kernel(LinearWalk p) {
   f32x4_t uf[NC];
   // The state as an operand of x S: split beside the matrix products that update
   // it, so that x S starts with products; split there where 256 rows of state
-  // leave no registers to hold it.
-  constexpr bool KEEP = MODE != kState && PT <= 128;
+  // or the dots leave no registers to hold it.
+  constexpr bool KEEP = MODE == kOut && PT <= 128;
   bf16x8_t sb[KEEP ? F::PS : 1][OPL];
   auto split_state = [&](int s) {
     const float sv[8] = {S[2 * s][0], S[2 * s][1], S[2 * s][2], S[2 * s][3],
@@ -609,19 +618,36 @@ void linear_walk_kernel(LinearWalk p) {
       const bf16_t *const sP = scores_at(cc);
       const auto rs = tile_rsrc(yc, (uint32_t)(((L - 1) * ldy + ncol) * ysz));
       yc += dy;
-      // every operand first, so that their reads are in flight together
-      bf16x8_t a[NC][KS][OPL];
+      auto row_dots = [&](int which) {  // this wave's columns of the rows' dots; u is zero past the width
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
+        for (int i = 0; i < NC; ++i) {
+          const f32x4_t u = SZ == 2 ? to_f32x4(uh[i]) : uf[i];
+          float d = (y[i][0] * u[0] + y[i][1] * u[1]) + (y[i][2] * u[2] + y[i][3] * u[3]);
+          d = rows4_sum(d);
+          if (grp == 0) sRed[(which * NW + wave) * 64 + 16 * i + l16] = d;
+        }
+      };
+      if constexpr (MODE == kDots) row_dots(1);
+      // every operand first, so that their reads are in flight together (of three
+      // parts, those of half the tokens: registers)
+      constexpr int GROUP = OPL == 3 ? 1 : KS;
 #pragma unroll
-        for (int s = REV ? i / 2 : 0; s <= (REV ? KS - 1 : i / 2); ++s)
-#pragma unroll
-          for (int pl = 0; pl < OPL; ++pl) a[i][s][pl] = row_frag(sP + pl * F::PPL + 16 * i * F::LDP + ap + 32 * s);
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
+      for (int s0 = 0; s0 < KS; s0 += GROUP) {
+        bf16x8_t a[NC][GROUP][OPL];
 #pragma unroll
         for (int i = 0; i < NC; ++i)
-          if (REV ? s >= i / 2 : s <= i / 2) y[i] = mma_parts(wf[s], a[i][s], y[i]);
+#pragma unroll
+          for (int s = s0; s < s0 + GROUP; ++s)
+            if (REV ? s >= i / 2 : s <= i / 2) {
+#pragma unroll
+              for (int pl = 0; pl < OPL; ++pl) a[i][s - s0][pl] = row_frag(sP + pl * F::PPL + 16 * i * F::LDP + ap + 32 * s);
+            }
+#pragma unroll
+        for (int s = s0; s < s0 + GROUP; ++s)
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+            if (REV ? s >= i / 2 : s <= i / 2) y[i] = mma_parts(wf[s], a[i][s - s0], y[i]);
+      }
       if (F::STAGE && ysz == 2) {
         // rows 8..15 of 16 swap 16-byte neighbours: 16 rows then cover all banks
         bf16_t *dst = rows_at(cc) + l16 * F::LDX + ((16 * wave + 4 * grp) ^ (l16 & 8));
@@ -637,16 +663,7 @@ void linear_walk_kernel(LinearWalk p) {
           __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, to_bf16x4(y[i])), rs,
                                                 (int)(gy + 16 * i * ldy * ysz), 0, 0);
       }
-      if constexpr (MODE == kDots) {  // this wave's columns of the rows' dots; u is zero past the width
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          const f32x4_t u = SZ == 2 ? to_f32x4(uh[i]) : uf[i];
-          float d = (y[i][0] * u[0] + y[i][1] * u[1]) + (y[i][2] * u[2] + y[i][3] * u[3]);
-          d += __shfl_xor(d, 16);
-          d += __shfl_xor(d, 32);
-          if (grp == 0) sRed[wave * 64 + 16 * i + l16] = d;
-        }
-      }
+      if constexpr (MODE == kDots) row_dots(0);
     }
 
     // ---- the state ----
