@@ -3,6 +3,7 @@ per head, and the norms round an attention block. Argument checks and marshallin
 everything runs in libkda.so, on the tensors' device and its current stream.
 """
 import ctypes
+import functools
 
 import torch
 
@@ -75,15 +76,24 @@ def _tensor(name, t, shape, dtype, device):
 _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
+def _on_device(f):
+    """Runs f with its first tensor's device current: workspace sizes and launches go by it."""
+
+    @functools.wraps(f)
+    def g(x, *args, **kw):
+        i = x.device.index
+        if i is None or i == _current_device():
+            return f(x, *args, **kw)
+        with torch.cuda.device(i):
+            return f(x, *args, **kw)
+
+    return g
+
+
 def _launch(device, entry, *args):
     """One entry point on the device's current stream (its handle read without building a
     Stream object, which costs as much as the launch of a single-token step)."""
-    i = device.index
-    if _current_device() == i:
-        status = entry(*args, _current_stream(i))
-    else:
-        with torch.cuda.device(device):
-            status = entry(*args, _current_stream(i))
+    status = entry(*args, _current_stream(device.index))
     if status:
         check(status)
 
@@ -132,6 +142,7 @@ def _outputs(q, v, N, out, final_state, want_state):
             _tensor("final_state", ht, shape, torch.float32, q.device))
 
 
+@_on_device
 def chunk_linear_attn(q, k, v, g, initial_state=None, *, cu_seqlens=None, output_final_state=False, scale=None,
                       final_state=None, out=None, workspace=None):
     """Chunked linear attention with one decay per head. Returns (o, ht); ht is None unless requested.
@@ -142,8 +153,9 @@ def chunk_linear_attn(q, k, v, g, initial_state=None, *, cu_seqlens=None, output
     state. ``initial_state`` is fp32 [N, H, K, V]; ``final_state`` may preallocate the final
     state, including ``initial_state`` itself for an update in place. Packed batches pass
     ``cu_seqlens`` (int32 [N+1]); rows outside it are left as they are in ``out``.
-    ``workspace`` may pass a uint8 tensor of ``linear_workspace_bytes``, reused from call to call
-    (calls that share one must not overlap); otherwise each call allocates what it needs.
+    ``out`` must not overlap an input. ``workspace`` may pass a uint8 tensor of
+    ``linear_workspace_bytes``, reused from call to call (calls or captured graphs that share one
+    must not run at once); otherwise each call allocates what it needs.
     """
     a, N, (pq, pk, pv, pg, ph, pc) = _attn_args(q, k, v, g, initial_state, cu_seqlens, scale)
     o, ht, po, pt = _outputs(q, v, N, out, final_state, output_final_state)
@@ -153,6 +165,7 @@ def chunk_linear_attn(q, k, v, g, initial_state=None, *, cu_seqlens=None, output
     return o, ht
 
 
+@_on_device
 def recurrent_linear_attn(q, k, v, g, initial_state=None, *, cu_seqlens=None, output_final_state=False, scale=None,
                           final_state=None, out=None):
     """``chunk_linear_attn`` token by token, for decoding: one kernel that holds the state in
@@ -163,6 +176,7 @@ def recurrent_linear_attn(q, k, v, g, initial_state=None, *, cu_seqlens=None, ou
     return o, ht
 
 
+@_on_device
 def chunk_linear_attn_bwd(q, k, v, g, do, initial_state=None, *, dht=None, cu_seqlens=None, scale=None,
                           workspace=None):
     """Gradients of sum(do * o) + sum(dht * ht) for ``chunk_linear_attn``.
@@ -185,6 +199,7 @@ def chunk_linear_attn_bwd(q, k, v, g, do, initial_state=None, *, dht=None, cu_se
     return got
 
 
+@_on_device
 def linear_workspace_bytes(q, k, v, g, *, slots=None, backward=False):
     """Workspace bytes of ``chunk_linear_attn`` (or of its backward) for tensors like these;
     ``slots`` is the number of packed sequences (default: the batch, unpacked)."""
@@ -220,6 +235,7 @@ def _norm_args(x, weight, gate, gate_act, residual, scale, next_weight, eps, nor
     return a, ptrs, res, vec
 
 
+@_on_device
 def block_norm(x, weight=None, *, gate=None, gate_act="sigmoid", residual=None, scale=None, next_weight=None,
                next_norm=None, eps=1e-6, norm="rms", out=None, next_out=None):
     """The norm after a block with its gate, residual branch and the norm before the next block.
@@ -246,6 +262,7 @@ def block_norm(x, weight=None, *, gate=None, gate_act="sigmoid", residual=None, 
     return (y, z) if nxt else y
 
 
+@_on_device
 def block_norm_bwd(x, dy, weight=None, *, dz=None, gate=None, gate_act="sigmoid", residual=None, scale=None,
                    next_weight=None, eps=1e-6, norm="rms", workspace=None):
     """Gradients of sum(dy * y) + sum(dz * z) for ``block_norm``; dy may be None beside dz.

@@ -25,6 +25,8 @@
  *     the bf16 matrix cores with every fp32 operand taken as a sum of bf16
  *     parts, so fp32 results (states, dg, and every output of fp32 calls)
  *     carry fp32 rounding, not bf16's.
+ *   - Outputs must not overlap inputs, other than ht on h0 itself.
+ *   - fp32 inputs above 3.38e38 (bf16's largest value) count as infinite.
  *   - A NaN or infinity in q, k, v or g makes the outputs of its (sequence,
  *     head) non-finite from the start of the 64-token chunk that holds it (the
  *     backward: throughout the sequence), and no other sequence's or head's.

@@ -65,6 +65,7 @@ SHAPES = [
     (1, 300, 2, 1, 128, 128, [0, 64, 1, 0, 130, 0]),
     (1, 400, 2, 2, 72, 40, [33, 300]),
     (1, 1500, 2, 2, 64, 64, None),
+    (2, 1090, 2, 1, 40, 136, None),
     (1, 1700, 2, 1, 128, 136, [3, 1100, 0, 520, 60]),
 ]
 
@@ -362,6 +363,34 @@ def test_graph_replays(T):
         torch.cuda.synchronize()
         for x, y in zip(held, want):
             assert torch.equal(x, y)
+
+
+def test_two_graphs_and_an_eager_call():
+    """Graphs captured from the same inputs, each with its own workspace, replayed one after the other and
+    between eager calls."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import chunk_linear_attn, chunk_linear_attn_bwd
+
+    g = dev(make(1, 1300, 2, 2, 64, 128, torch.bfloat16, "head", seed=30))
+    fwd = lambda: list(chunk_linear_attn(g["q"], g["k"], g["v"], g["g"], g["h0"], output_final_state=True))  # noqa: E731
+    bwd = lambda: list(chunk_linear_attn_bwd(g["q"], g["k"], g["v"], g["g"], g["do"], g["h0"],  # noqa: E731
+                                             dht=g["dht"]).values())
+    fwd(), bwd()
+    torch.cuda.synchronize()
+    graphs = []
+    for f in (fwd, bwd):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = f()
+        graphs.append((graph, held, f))
+    for _ in range(3):
+        g["k"].mul_(1.25)
+        for graph, held, f in graphs + graphs[::-1]:
+            want = f()
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(held, want))
 
 
 def test_two_streams_with_workspaces_of_their_own():
