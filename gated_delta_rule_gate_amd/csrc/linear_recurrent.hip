@@ -26,8 +26,10 @@ __device__ __forceinline__ void store_once(float *p, f32x4_t v) {
   __builtin_nontemporal_store(v, reinterpret_cast<f32x4_t *>(p));
 }
 
-// FULL: K == KP and V a multiple of BV: no masks.
-template <typename T, int KP, int BV, bool FULL>
+// FULL: K == KP and V a multiple of BV: no masks. ONE: every sequence has one
+// token (a dense decode step): no loop and nothing prefetched, so fewer
+// registers and more workgroups a compute unit.
+template <typename T, int KP, int BV, bool FULL, bool ONE>
 __global__ __launch_bounds__(256) void linear_recurrent_kernel(LinearRecurrent p) {
   constexpr int CG = BV / 4, RG = 256 / CG, RPT = KP / RG;
   static_assert(256 % CG == 0 && KP % RG == 0 && CG <= 64, "tile");
@@ -39,7 +41,7 @@ __global__ __launch_bounds__(256) void linear_recurrent_kernel(LinearRecurrent p
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int cg = tid % CG, rg = tid / CG, row0 = rg * RPT, col0 = vb * BV + cg * 4;
   const bool col_ok = FULL || col0 < p.V;
-  const SlotRange sr = slot_range(p.cu, n, p.T);
+  SlotRange sr = slot_range(ONE ? nullptr : p.cu, n, ONE ? 1 : p.T);
   const int64_t sbase = (int64_t)(n * (int64_t)p.H + h) * K * p.V;
 
   const T *qp = reinterpret_cast<const T *>(p.q), *kp = reinterpret_cast<const T *>(p.k);
@@ -74,7 +76,7 @@ __global__ __launch_bounds__(256) void linear_recurrent_kernel(LinearRecurrent p
     }
     if (tid < BV) s_v[buf][tid] = nv;
     const float a = fast_exp2(ng * kLog2e);
-    if (i + 1 < sr.len) fetch(i + 1);
+    if (!ONE && i + 1 < sr.len) fetch(i + 1);
     __syncthreads();
     const f32x4_t v4 = *reinterpret_cast<const f32x4_t *>(&s_v[buf][cg * 4]);
     f32x4_t o4 = {0.f, 0.f, 0.f, 0.f};
@@ -106,10 +108,10 @@ hipError_t launch_rec(const LinearRecurrent &p, hipStream_t st) {
   const int64_t grid = (int64_t)p.N * p.H * ((p.V + BV - 1) / BV);
   if (grid == 0) return hipSuccess;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  if (p.K == KP && p.V % BV == 0)
-    hipLaunchKernelGGL((linear_recurrent_kernel<T, KP, BV, true>), dim3((unsigned)grid), dim3(256), 0, st, p);
-  else
-    hipLaunchKernelGGL((linear_recurrent_kernel<T, KP, BV, false>), dim3((unsigned)grid), dim3(256), 0, st, p);
+  const bool full = p.K == KP && p.V % BV == 0, one = !p.cu && p.T == 1;
+  auto kern = full ? (one ? linear_recurrent_kernel<T, KP, BV, true, true> : linear_recurrent_kernel<T, KP, BV, true, false>)
+                   : (one ? linear_recurrent_kernel<T, KP, BV, false, true> : linear_recurrent_kernel<T, KP, BV, false, false>);
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), 0, st, p);
   return hipGetLastError();
 }
 
