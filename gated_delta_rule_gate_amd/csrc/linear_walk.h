@@ -553,20 +553,17 @@ void linear_walk_kernel(LinearWalk p) {
     const bf16_t *const sX = rows_at(cc), *const sZ = sX + F::nX / 2;
     const float *const tab = tab_at(cc);
 
+    // Half of the state behind an anchored chunk loads beside a (x S), the other
+    // half afterwards: all of it there spills more and is no faster, none of it
+    // there left 7% of the walk waiting.
+    constexpr int CK = MODE == kDots && REV ? F::NT / 2 : 1;
+    const float *const ck_src = p.ckpt + ((t0 + L) / kLinearAnchor) * fragH + frag;
+    f32x4_t ck[CK];
     if constexpr (MODE != kState) {
       if constexpr (MODE == kDots) {
-        if (REV && anchored(t0, L)) {  // <h, dh> behind this chunk
-          const float *src = p.ckpt + ((t0 + L) / kLinearAnchor) * fragH + frag;
-          float d = 0.f;
+        if (REV && anchored(t0, L)) {  // h behind this chunk, on its way beside a (x S)
 #pragma unroll
-          for (int t = 0; t < F::NT; ++t) {
-            const f32x4_t x = *reinterpret_cast<const f32x4_t *>(src + t * 256);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d += x[e] * S[t][e];
-          }
-#pragma unroll
-          for (int off = 32; off > 0; off >>= 1) d += __shfl_xor(d, off);
-          if (lane == 0) sAnc[wave] = d;
+          for (int t = 0; t < CK; ++t) ck[t] = *reinterpret_cast<const f32x4_t *>(ck_src + t * 256);
         }
         // the row dots' partners: four columns of a row a lane
         const auto rs = tile_rsrc(uc, (uint32_t)(((L - 1) * ldu + ncol) * SZ));
@@ -594,6 +591,22 @@ void linear_walk_kernel(LinearWalk p) {
       }
 #pragma unroll
       for (int i = 0; i < NC; ++i) y[i] *= tab[128 + 16 * i + l16];
+      if (MODE == kDots && REV && anchored(t0, L)) {  // <h, dh> behind this chunk
+        float d = 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int t = 0; t < CK; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d += ck[t][e] * S[half * CK + t < F::NT ? half * CK + t : 0][e];
+          if (half == 0)
+#pragma unroll
+            for (int t = 0; t < CK; ++t) ck[t] = *reinterpret_cast<const f32x4_t *>(ck_src + (CK + t) * 256);
+        }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) d += __shfl_xor(d, off);
+        if (lane == 0) sAnc[wave] = d;
+      }
       // w's parts are formed in this period, beside x S: left to itself the
       // compiler moves them behind the barrier, before their use (with the dots'
       // registers it has to: holding them spills)
