@@ -56,18 +56,18 @@ def _lib():
 def _refuse(name, t, shape, dtype, device):
     if t.shape != shape or t.dtype != dtype:
         raise ValueError("%s must be %s %s, got %s %s" % (name, dtype, list(shape), t.dtype, list(t.shape)))
-    if not t.is_cuda or t.device != device:
-        raise ValueError("%s must be on %s" % (name, device if device.type == "cuda" else "a GPU"))
+    if device < 0 or t.get_device() != device:
+        raise ValueError("%s must be on %s" % (name, "a GPU" if device < 0 else "cuda:%d" % device))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     raise RuntimeError("%s requires grad: this op does not track gradients; call its _bwd for them" % name)
 
 
 def _tensor(name, t, shape, dtype, device):
-    """A tensor's pointer, after its checks; None for None."""
+    """A tensor's pointer, after its checks; None for None. device: the GPU's index, -1 for none."""
     if t is None:
         return None
-    if (t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_cuda or t.requires_grad
+    if (t.shape != shape or t.dtype is not dtype or device < 0 or t.get_device() != device or t.requires_grad
             or not t.is_contiguous()):
         _refuse(name, t, shape, dtype, device)
     return t.data_ptr()
@@ -81,8 +81,8 @@ def _on_device(f):
 
     @functools.wraps(f)
     def g(x, *args, **kw):
-        i = x.device.index
-        if i is None or i == _current_device():
+        i = x.get_device()
+        if i < 0 or i == _current_device():
             return f(x, *args, **kw)
         with torch.cuda.device(i):
             return f(x, *args, **kw)
@@ -93,7 +93,7 @@ def _on_device(f):
 def _launch(device, entry, *args):
     """One entry point on the device's current stream (its handle read without building a
     Stream object, which costs as much as the launch of a single-token step)."""
-    status = entry(*args, _current_stream(device.index))
+    status = entry(*args, _current_stream(device))
     if status:
         check(status)
 
@@ -107,7 +107,7 @@ def _attn_args(q, k, v, g, h0, cu_seqlens, scale):
     _require(v.shape[:2] == q.shape[:2] and Hk > 0 and H % Hk == 0,
              "v must be [B, T, H, V] with H a multiple of q's heads Hk")
     _require(q.dtype in (torch.bfloat16, torch.float32), "q, k, v must share dtype bf16 or fp32")
-    dev, N = q.device, B
+    dev, N = q.get_device(), B
     if cu_seqlens is not None:
         _require(B == 1, "packed inputs (cu_seqlens) need batch 1")
         _require(cu_seqlens.dim() == 1 and cu_seqlens.numel() > 0, "cu_seqlens must be int32 [N+1]")
@@ -119,7 +119,7 @@ def _attn_args(q, k, v, g, h0, cu_seqlens, scale):
             _tensor("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev))
     a = LinearArgs(B, T, H, K, V, N, 0 if Hk == H else Hk, KDA_BF16 if q.dtype == torch.bfloat16 else KDA_F32,
                    DECAY_HEAD if head else DECAY_TOKEN, 0.0 if scale is None else float(scale))
-    return a, N, ptrs
+    return a, N, dev, ptrs
 
 
 def _workspace(workspace, need, device):
@@ -127,19 +127,18 @@ def _workspace(workspace, need, device):
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+        workspace = torch.empty((need,), dtype=torch.uint8, device="cuda:%d" % device)
     _require(workspace.dtype == torch.uint8 and workspace.dim() == 1 and workspace.numel() >= need,
              "workspace must be a 1-D uint8 tensor of at least %d bytes" % need)
     return _tensor("workspace", workspace, workspace.shape, torch.uint8, device), workspace.numel(), workspace
 
 
-def _outputs(q, v, N, out, final_state, want_state):
+def _outputs(q, v, N, dev, out, final_state, want_state):
     o = torch.empty_like(v) if out is None else out
     B, T, H, V = v.shape
     shape = (N, H, q.shape[3], V)
     ht = torch.empty(shape, dtype=torch.float32, device=q.device) if final_state is None and want_state else final_state
-    return (o, ht, _tensor("out", o, v.shape, q.dtype, q.device),
-            _tensor("final_state", ht, shape, torch.float32, q.device))
+    return o, ht, _tensor("out", o, v.shape, q.dtype, dev), _tensor("final_state", ht, shape, torch.float32, dev)
 
 
 @_on_device
@@ -157,11 +156,11 @@ def chunk_linear_attn(q, k, v, g, initial_state=None, *, cu_seqlens=None, output
     ``linear_workspace_bytes``, reused from call to call (calls or captured graphs that share one
     must not run at once); otherwise each call allocates what it needs.
     """
-    a, N, (pq, pk, pv, pg, ph, pc) = _attn_args(q, k, v, g, initial_state, cu_seqlens, scale)
-    o, ht, po, pt = _outputs(q, v, N, out, final_state, output_final_state)
+    a, N, dev, (pq, pk, pv, pg, ph, pc) = _attn_args(q, k, v, g, initial_state, cu_seqlens, scale)
+    o, ht, po, pt = _outputs(q, v, N, dev, out, final_state, output_final_state)
     L = _lib()
-    pw, nw, _keep = _workspace(workspace, int(L.kda_linear_chunk_workspace_bytes(ctypes.byref(a))), q.device)
-    _launch(q.device, L.kda_linear_chunk_fwd, ctypes.byref(a), pq, pk, pv, pg, ph, pc, po, pt, pw, nw)
+    pw, nw, _keep = _workspace(workspace, int(L.kda_linear_chunk_workspace_bytes(ctypes.byref(a))), dev)
+    _launch(dev, L.kda_linear_chunk_fwd, ctypes.byref(a), pq, pk, pv, pg, ph, pc, po, pt, pw, nw)
     return o, ht
 
 
@@ -170,9 +169,9 @@ def recurrent_linear_attn(q, k, v, g, initial_state=None, *, cu_seqlens=None, ou
                           final_state=None, out=None):
     """``chunk_linear_attn`` token by token, for decoding: one kernel that holds the state in
     registers. ``final_state=initial_state`` updates the state in place. Returns (o, ht)."""
-    a, N, (pq, pk, pv, pg, ph, pc) = _attn_args(q, k, v, g, initial_state, cu_seqlens, scale)
-    o, ht, po, pt = _outputs(q, v, N, out, final_state, output_final_state)
-    _launch(q.device, _lib().kda_linear_recurrent_fwd, ctypes.byref(a), pq, pk, pv, pg, ph, pc, po, pt)
+    a, N, dev, (pq, pk, pv, pg, ph, pc) = _attn_args(q, k, v, g, initial_state, cu_seqlens, scale)
+    o, ht, po, pt = _outputs(q, v, N, dev, out, final_state, output_final_state)
+    _launch(dev, _lib().kda_linear_recurrent_fwd, ctypes.byref(a), pq, pk, pv, pg, ph, pc, po, pt)
     return o, ht
 
 
@@ -185,15 +184,14 @@ def chunk_linear_attn_bwd(q, k, v, g, do, initial_state=None, *, dht=None, cu_se
     (fp32, shaped as g) and dh0 (fp32 [N, H, K, V]). Nothing of the forward needs to be kept.
     Packed: gradients of rows outside cu_seqlens are not written.
     """
-    a, N, (pq, pk, pv, pg, ph, pc) = _attn_args(q, k, v, g, initial_state, cu_seqlens, scale)
-    dev = q.device
+    a, N, dev, (pq, pk, pv, pg, ph, pc) = _attn_args(q, k, v, g, initial_state, cu_seqlens, scale)
     state = (N, v.shape[2], q.shape[3], v.shape[3])
     pdo = _tensor("do", do, v.shape, q.dtype, dev)
     pdht = _tensor("dht", dht, state, torch.float32, dev)
     L = _lib()
     pw, nw, _keep = _workspace(workspace, int(L.kda_linear_chunk_bwd_workspace_bytes(ctypes.byref(a))), dev)
     got = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v), dg=torch.empty_like(g),
-               dh0=torch.empty(state, dtype=torch.float32, device=dev))
+               dh0=torch.empty(state, dtype=torch.float32, device=q.device))
     _launch(dev, L.kda_linear_chunk_bwd, ctypes.byref(a), pq, pk, pv, pg, ph, pc, pdo, pdht, got["dq"].data_ptr(),
             got["dk"].data_ptr(), got["dv"].data_ptr(), got["dg"].data_ptr(), got["dh0"].data_ptr(), pw, nw)
     return got
@@ -218,7 +216,7 @@ def _norm_args(x, weight, gate, gate_act, residual, scale, next_weight, eps, nor
     _require(x.dtype in (torch.bfloat16, torch.float32), "x must be bf16 or fp32")
     _require(norm in NORMS, "norm must be one of %s" % sorted(NORMS))
     _require(gate_act in GATE_ACTS, "gate_act must be one of %s" % sorted(GATE_ACTS))
-    D, dev = x.shape[-1], x.device
+    D, dev = x.shape[-1], x.get_device()
     bf16 = x.dtype == torch.bfloat16
     res = x.dtype
     if residual is not None:
@@ -253,12 +251,13 @@ def block_norm(x, weight=None, *, gate=None, gate_act="sigmoid", residual=None, 
     _require(nxt or next_weight is None, "next_weight needs the next norm")
     a, (px, pw, pg, pr, ps, pn), res, _ = _norm_args(x, weight, gate, gate_act, residual, scale, next_weight, eps, norm)
     y = torch.empty_like(x, dtype=res) if out is None else out
-    py = _tensor("out", y, x.shape, res, x.device)
+    dev = x.get_device()
+    py = _tensor("out", y, x.shape, res, dev)
     z = pz = None
     if nxt:
         z = torch.empty_like(x) if next_out is None else next_out
-        pz = _tensor("next_out", z, x.shape, x.dtype, x.device)
-    _launch(x.device, _lib().kda_block_norm_fwd, ctypes.byref(a), px, pw, pg, pr, ps, pn, py, pz)
+        pz = _tensor("next_out", z, x.shape, x.dtype, dev)
+    _launch(dev, _lib().kda_block_norm_fwd, ctypes.byref(a), px, pw, pg, pr, ps, pn, py, pz)
     return (y, z) if nxt else y
 
 
@@ -274,7 +273,7 @@ def block_norm_bwd(x, dy, weight=None, *, dz=None, gate=None, gate_act="sigmoid"
     _require(next_weight is None or dz is not None, "next_weight needs dz")
     a, (px, pw, pg, pr, ps, pn), res, vec = _norm_args(x, weight, gate, gate_act, residual, scale, next_weight, eps,
                                                       norm)
-    dev = x.device
+    dev = x.get_device()
     pdy, pdz = _tensor("dy", dy, x.shape, res, dev), _tensor("dz", dz, x.shape, x.dtype, dev)
     L = _lib()
     params = weight is not None or vec or next_weight is not None

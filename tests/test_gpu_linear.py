@@ -243,11 +243,11 @@ def test_rows_outside_the_offsets():
     within(o[:, 20:190], want[0], size[0], torch.bfloat16, ref.roundings(64, 64, 300), "o", PARTS[torch.bfloat16])
     assert (o[:, :20] == 7.0).all() and (o[:, 190:] == 7.0).all()
     # the C entry, with gradients that hold a mark
-    a, _, (pq, pk, pv, pg, ph, pc) = _linear._attn_args(g["q"], g["k"], g["v"], g["g"], g["h0"], g["cu"], None)
+    a, _, i, (pq, pk, pv, pg, ph, pc) = _linear._attn_args(g["q"], g["k"], g["v"], g["g"], g["h0"], g["cu"], None)
     marks = [torch.full_like(g[x], 7.0) for x in ("q", "k", "v", "g")]
     need = lib().kda_linear_chunk_bwd_workspace_bytes(a)
     ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")  # NaN everywhere
-    _linear._launch(g["q"].device, lib().kda_linear_chunk_bwd, a, pq, pk, pv, pg, ph, pc, g["do"].data_ptr(),
+    _linear._launch(i, lib().kda_linear_chunk_bwd, a, pq, pk, pv, pg, ph, pc, g["do"].data_ptr(),
                     g["dht"].data_ptr(), *[m.data_ptr() for m in marks], None, ws.data_ptr(), need)
     for m in marks:
         assert (m[:, :20] == 7.0).all() and (m[:, 190:] == 7.0).all()
