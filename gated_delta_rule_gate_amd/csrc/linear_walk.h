@@ -271,23 +271,20 @@ void linear_walk_kernel(LinearWalk p) {
     const T *wf = reinterpret_cast<const T *>(p.w) + (first * p.Hw + h / (p.H / p.Hw)) * Q + col0;
     const float *gf = p.g + (p.g_head ? h : first * p.H + h);
     const int64_t dx = (int64_t)STEP * ldx, dw = (int64_t)STEP * ldw, dg = p.g_head ? 0 : (int64_t)STEP * p.H;
-    // Loads run a chunk ahead; where a chunk takes 2 us only (the state alone),
-    // two, in two sets of registers. With y a second set does not fit: it
-    // spilled, and walks took 14% longer.
-    constexpr int DEPTH = MODE == kState ? 2 : 1;
-    u32x4_t fx[DEPTH][MODE != kState ? MX::IT : 1], fz[DEPTH][MX::IT], fw[DEPTH][MW::IT];
-    float fg[DEPTH];
+    // loads run a chunk ahead (two ahead changed nothing where only the state is
+    // walked, and spilled otherwise)
+    u32x4_t fx[MODE != kState ? MX::IT : 1], fz[MX::IT], fw[MW::IT];
+    float fg = 0.f;
     double total = 0.0;  // log2 decay of the whole segment (the decays' wave)
     constexpr int DW = 3;  // the helper that forms the decays: one with fewer blocks of the scores
-    auto fetch = [&](int cc, auto set) {  // chunk after chunk in the walk's order
-      constexpr int I = decltype(set)::value;
+    auto fetch = [&](int cc) {  // chunk after chunk in the walk's order
       const int L = rows_of(cc);
-      if constexpr (MODE != kState) MX::load(fx[I], xf, ldx, L, P, gx, rx);
-      MX::load(fz[I], zf, ldx, L, P, gx, rx);
-      MW::load(fw[I], wf, ldw, L, ncol, gw, rw);
+      if constexpr (MODE != kState) MX::load(fx, xf, ldx, L, P, gx, rx);
+      MX::load(fz, zf, ldx, L, P, gx, rx);
+      MW::load(fw, wf, ldw, L, ncol, gw, rw);
       if (hw == DW) {
         const auto rs = tile_rsrc(gf, (uint32_t)(p.g_head ? 4 : ((L - 1) * p.H + 1) * 4));
-        fg[I] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        fg = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
             rs, lane < L ? (p.g_head ? 0 : lane * p.H * 4) : (int)kOffNone, 0, 0));
       }
       xf += dx;
@@ -299,9 +296,9 @@ void linear_walk_kernel(LinearWalk p) {
     // the factor of x S, c that of z in the state. The scale goes with y, in
     // reverse with z. A decay below 2^-160 is none at all and counts as
     // 2^-32768: differences across it give zero, those beyond it stay exact.
-    auto decays = [&](int cc, float g) {
+    auto decays = [&](int cc) {
       if (hw != DW) return;
-      double b = (double)g * 1.4426950408889634073599;
+      double b = (double)fg * 1.4426950408889634073599;
       if (b <= -160.0) b = -32768.0;
       b = wave_scan(b);
       const double bl = last_lane(b);
@@ -315,14 +312,13 @@ void linear_walk_kernel(LinearWalk p) {
       if (lane == 0) t[256] = fast_exp2((float)bl);
       total += bl;
     };
-    auto bring = [&](int cc, auto set) {  // rows and decays of cc to LDS, the loads of cc + DEPTH
-      constexpr int I = decltype(set)::value;
+    auto bring = [&](int cc) {  // rows and decays of cc to LDS, the loads of the chunk after it
       bf16_t *s = rows_at(cc);
-      if constexpr (MODE != kState) MX::put(fx[I], s + px, F::LDX, F::XPL);
-      MX::put(fz[I], s + F::nX / 2 + px, F::LDX, F::XPL);
-      MW::put(fw[I], s + (F::nX + F::nZ) / 2 + pw, F::LDW, F::WPL);
-      decays(cc, fg[I]);
-      if (cc + DEPTH < nch) fetch(cc + DEPTH, set);
+      if constexpr (MODE != kState) MX::put(fx, s + px, F::LDX, F::XPL);
+      MX::put(fz, s + F::nX / 2 + px, F::LDX, F::XPL);
+      MW::put(fw, s + (F::nX + F::nZ) / 2 + pw, F::LDW, F::WPL);
+      decays(cc);
+      if (cc + 1 < nch) fetch(cc + 1);
     };
     // scores of the causal 16 x 16 blocks, decayed and scaled, a wave taking
     // every fourth: lane has row l16 of x, four rows of z
@@ -410,25 +406,22 @@ void linear_walk_kernel(LinearWalk p) {
       }
     };
 
-    using Set0 = std::integral_constant<int, 0>;
-    using Set1 = std::integral_constant<int, DEPTH - 1>;
-    if (nch > 0) fetch(0, Set0{});
-    if (DEPTH > 1 && nch > 1) fetch(1, Set1{});
+    if (nch > 0) fetch(0);
     if constexpr (MODE != kState) {
       // the blocks of the scores beyond the triangle stay zero
       for (int i = ht; i < (int)(F::PBUF * F::nP / 4); i += F::HT) reinterpret_cast<unsigned *>(smem + F::oP)[i] = 0u;
     }
-    if (nch > 0) bring(0, Set0{});
+    if (nch > 0) bring(0);
     __syncthreads();
     if constexpr (F::PBUF == 2 && MODE != kState) {
       if (nch > 0) scores(0);
       __syncthreads();
     }
-    auto chunk = [&](int cc, auto next) {  // beside chunk cc of the state waves; next: the set of cc + 1
+    for (int cc = 0; cc < nch; ++cc) {  // beside chunk cc of the state waves
       if (MODE == kDots && cc > 0) dots(cc - 1);
       if (F::STAGE && cc > 0) store_rows(cc - 1);
       if constexpr (F::PBUF == 2 && MODE != kState) {
-        if (cc + 1 < nch) bring(cc + 1, next);
+        if (cc + 1 < nch) bring(cc + 1);
         __syncthreads();
         if (MODE == kDots && REV) anchor(cc);
         if (cc + 1 < nch) scores(cc + 1);
@@ -440,13 +433,9 @@ void linear_walk_kernel(LinearWalk p) {
           if (MODE == kDots && REV) anchor(cc);
         }
         if constexpr (F::NBUF == 1) __syncthreads();
-        if (cc + 1 < nch) bring(cc + 1, next);
+        if (cc + 1 < nch) bring(cc + 1);
         __syncthreads();
       }
-    };
-    for (int cc = 0; cc < nch; cc += DEPTH) {
-      chunk(cc, Set1{});
-      if (DEPTH > 1 && cc + 1 < nch) chunk(cc + 1, Set0{});
     }
     if (MODE == kDots && nch > 0) dots(nch - 1);
     if (F::STAGE && nch > 0) store_rows(nch - 1);
