@@ -55,9 +55,9 @@ struct SegPlan {
   size_t total() const { return align_up(state) + align_up(decay) + align_up(first); }
 };
 
-SegPlan seg_plan(const kda_linear_args *a, bool packed, int Q, bool dots) {
+SegPlan seg_plan(const kda_linear_args *a, bool packed, int P, int Q, bool dots) {
   SegPlan s;
-  s.seg = kda::linear_segment(a->T, a->N, a->H, Q, packed, dots);
+  s.seg = kda::linear_segment(a->T, a->N, a->H, P, Q, a->dtype == KDA_BF16, packed, dots);
   if (!s.seg) return s;
   const size_t elems = (size_t)a->H * a->K * a->V;
   const size_t bounds = (size_t)((int64_t)a->B * a->T / s.seg + 1);
@@ -104,9 +104,9 @@ struct BwdPlan {
 
 BwdPlan bwd_plan(const kda_linear_args *a, bool packed) {
   BwdPlan b;
-  b.seg = seg_plan(a, packed, a->K, true);
+  b.seg = seg_plan(a, packed, a->V, a->K, true);
   b.segs = b.seg.total();
-  const int qt = kda::linear_cols(a->K, &b.ncb);
+  const int qt = kda::linear_cols(a->V, a->K, a->dtype == KDA_BF16, (int64_t)a->N * a->H, &b.ncb);
   const int64_t rows = (int64_t)a->B * a->T;
   b.anchors = rows / kda::kLinearAnchor + 1;
   b.ckpt = 4 * (size_t)b.anchors * a->H * b.ncb * kda::linear_tile(a->V) * qt;
@@ -129,8 +129,8 @@ bool maybe_packed(const kda_linear_args *a) { return a->B == 1; }
 extern "C" size_t kda_linear_chunk_workspace_bytes(const kda_linear_args *a) {
   if (check_sizes(a) != KDA_OK) return 0;
   size_t n = 0;
-  if (maybe_dense(a)) n = std::max(n, seg_plan(a, false, a->V, false).total());
-  if (maybe_packed(a)) n = std::max(n, seg_plan(a, true, a->V, false).total());
+  if (maybe_dense(a)) n = std::max(n, seg_plan(a, false, a->K, a->V, false).total());
+  if (maybe_packed(a)) n = std::max(n, seg_plan(a, true, a->K, a->V, false).total());
   return n;
 }
 
@@ -139,7 +139,7 @@ extern "C" kda_status kda_linear_chunk_fwd(const kda_linear_args *a, const void 
                                            void *workspace, size_t ws_bytes, void *stream) {
   const kda_status s = check_common(a, q, k, v, g, h0, cu, o, ht);
   if (s != KDA_OK) return s;
-  const SegPlan plan = seg_plan(a, cu != nullptr, a->V, false);
+  const SegPlan plan = seg_plan(a, cu != nullptr, a->K, a->V, false);
   if (plan.total() > 0 && (!workspace || ws_bytes < plan.total())) return KDA_ERR_WORKSPACE;
   if (plan.total() > 0 && !aligned256(workspace)) return KDA_ERR_ALIGN;
   kda::LinearWalk w = walk_base(a, g, cu);

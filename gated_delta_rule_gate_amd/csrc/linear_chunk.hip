@@ -145,8 +145,14 @@ __global__ __launch_bounds__(256) void linear_dg_head_kernel(const double *part,
 
 int linear_tile(int width) { return width <= 64 ? 64 : (width <= 128 ? 128 : 256); }
 
-int linear_cols(int width, int *ncb) {
-  const int qt = width <= 64 ? 64 : 128;
+// By 128 columns x and z are read once where by 64 they are read twice. fp32
+// takes 64 where 256 rows of state would spill by 128 (4 x 2048 tokens, 16
+// heads, 256 x 128: 333 us against 561), and for few (sequence, head) pairs,
+// where the smaller rows fit LDS twice and more workgroups help more than the
+// second read costs (128 x 128, by 64 and by 128: 32 pairs of 2048 tokens 78 and
+// 105 us, 64 of 4096 237 and 212, 256 of 2048 348 and 319).
+int linear_cols(int P, int width, bool is_bf16, int64_t pairs, int *ncb) {
+  const int qt = width <= 64 || (!is_bf16 && (P > 128 || 8 * pairs <= device_cus())) ? 64 : 128;
   *ncb = (width + qt - 1) / qt;
   return qt;
 }
@@ -162,9 +168,9 @@ int linear_cols(int width, int *ncb) {
 // heads, 10 slots, 15872 tokens, segments of 512, 1024, 1536, 1984, none: 259,
 // 236, 223, 249, 300 us; gradient, 16 heads, 7 slots, 4999 tokens, of 320, 512, 768: 192,
 // 175, 217 us.)
-int linear_segment(int T, int slots, int H, int Q, bool packed, bool dots) {
+int linear_segment(int T, int slots, int H, int P, int Q, bool is_bf16, bool packed, bool dots) {
   int ncb;
-  linear_cols(Q, &ncb);
+  linear_cols(P, Q, is_bf16, (int64_t)slots * H, &ncb);
   const double room = device_cus();
   const int64_t pairs = (int64_t)H * ncb;
   const int64_t chunks = (T + 63) / 64;

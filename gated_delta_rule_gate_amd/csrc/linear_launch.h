@@ -62,9 +62,10 @@ struct LinearWalk {
 };
 
 int linear_tile(int width);              // padded P: 64, 128 or 256
-int linear_cols(int width, int *ncb);    // columns per workgroup (64 or 128) and column blocks
+// columns per workgroup (64 or 128) and column blocks, for `pairs` (sequence, head) pairs
+int linear_cols(int P, int width, bool is_bf16, int64_t pairs, int *ncb);
 // tokens per segment for one walk with Q columns, or 0 for none; dots: a walk with row dots
-int linear_segment(int T, int slots, int H, int Q, bool packed, bool dots);
+int linear_segment(int T, int slots, int H, int P, int Q, bool is_bf16, bool packed, bool dots);
 hipError_t launch_linear_walk(const LinearWalk &p, hipStream_t st);
 hipError_t launch_linear_walk_bf16_fwd(const LinearWalk &p, hipStream_t st);
 hipError_t launch_linear_walk_bf16_rev(const LinearWalk &p, hipStream_t st);

@@ -764,8 +764,11 @@ hipError_t launch_modes(const LinearWalk &p, hipStream_t st) {
 template <typename T, int PT, bool REV, int OPL, int MODE>
 hipError_t launch_cols(const LinearWalk &p, hipStream_t st) {
   int ncb;
-  if (linear_cols(p.Q, &ncb) == 64) return launch_modes<T, PT, 4, REV, OPL, MODE>(p, st);
-  return launch_modes<T, PT, 8, REV, OPL, MODE>(p, st);
+  if constexpr (sizeof(T) == 2 || PT <= 128) {
+    if (linear_cols(p.P, p.Q, p.is_bf16, (int64_t)p.N * p.H, &ncb) == 128)
+      return launch_modes<T, PT, 8, REV, OPL, MODE>(p, st);
+  }
+  return launch_modes<T, PT, 4, REV, OPL, MODE>(p, st);
 }
 
 template <typename T, bool REV, int OPL, int MODE>
