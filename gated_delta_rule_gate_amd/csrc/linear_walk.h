@@ -17,6 +17,12 @@
 // and k stay exact. Within a chunk b is summed in fp64 and kept as an integer
 // and a fraction: differences of far larger sums stay exact to fp32, and the
 // exponent of every pair is formed on its own, so no decay is too strong.
+//
+// Bound by the bytes of its rows at the device's copy rate (234 us for 4 x 4096
+// tokens of 64 heads, 128 x 128 bf16); measured 274 us, 4.05 TB/s. In between
+// stand its vector instructions (46% of cycles, half of them the splitting of
+// the state and of w into parts) and its matrix instructions (38%), on three
+// waves a SIMD: with loads and stores left out it takes 206 us.
 #pragma once
 
 #include "chunk_fused_tiles.h"
