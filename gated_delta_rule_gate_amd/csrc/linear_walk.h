@@ -4,9 +4,9 @@
 //
 // One workgroup owns a (sequence or segment, head, block of 16 NW columns) and
 // keeps its FP32 state in matrix accumulators: wave w holds columns 16w..16w+15
-// of every 16-row state tile. A C-layout accumulator column is, unchanged, a B
-// operand of the next product under the slot order of Mma<bf16_t>::kidx, so
-// the state never leaves registers.
+// of every 16-row state tile. With the channels of a tile pair dealt as
+// state_channel() does, an accumulator column is, unchanged, an operand of the
+// next product, so the state never leaves registers.
 //
 // Arithmetic. Every product runs on the bf16 matrix cores. An fp32 operand is
 // a sum of bf16 parts (three parts hold all 24 bits), and products of parts
