@@ -177,6 +177,50 @@ def test_no_tokens():
     assert (chunk_linear_attn_bwd(h["q"], h["k"], h["v"], h["g"], h["do"], h["h0"], dht=h["dht"])["dg"] == 0).all()
 
 
+@pytest.mark.parametrize("lens", [[], [0, 0, 0], [0, 0, 0, 5]], ids=["none", "empty", "last"])
+def test_slots_without_tokens(lens):
+    """Packed batches of no slot, of empty slots only, and of empty slots before a short one."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import chunk_linear_attn, chunk_linear_attn_bwd, recurrent_linear_attn
+
+    T = 40
+    d = make(1, T, 4, 2, 64, 64, torch.bfloat16, "head", lens=lens, seed=40)
+    d["cu"] = torch.tensor([3] + [3 + sum(lens[:i + 1]) for i in range(len(lens))], dtype=torch.int32)
+    g = dev(d)
+    for f in (chunk_linear_attn, recurrent_linear_attn):
+        out = torch.full_like(g["v"], 7.0)
+        _, ht = f(g["q"], g["k"], g["v"], g["g"], g["h0"], cu_seqlens=g["cu"], output_final_state=True, out=out)
+        assert all(torch.equal(ht[i], g["h0"][i]) for i, l in enumerate(lens) if l == 0)
+        assert (out[:, :3] == 7.0).all() and (out[:, 3 + sum(lens):] == 7.0).all()
+        assert torch.isfinite(out).all()
+    got = chunk_linear_attn_bwd(g["q"], g["k"], g["v"], g["g"], g["do"], g["h0"], dht=g["dht"], cu_seqlens=g["cu"])
+    assert all(torch.equal(got["dh0"][i], g["dht"][i]) for i, l in enumerate(lens) if l == 0)
+    assert torch.isfinite(got["dg"]).all() and (sum(lens) > 0 or (got["dg"] == 0).all())
+
+
+def test_many_heads_and_slots():
+    """More (sequence, head) pairs than compute units, slots shorter and longer than a chunk, shared heads."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import chunk_linear_attn, chunk_linear_attn_bwd
+
+    lens = [1, 70, 0, 33, 64, 128, 7, 100, 3, 17]
+    d = make(1, sum(lens) + 2, 48, 16, 64, 72, torch.bfloat16, "token", lens=lens, seed=41)
+    g = dev(d)
+    o, ht = chunk_linear_attn(g["q"], g["k"], g["v"], g["g"], g["h0"], cu_seqlens=g["cu"], output_final_state=True)
+    end, n = sum(lens), ref.roundings(64, 72, 128)
+    want, size = ref.attn(*inputs64(d), cu=d["cu"]), ref.attn_sizes(*inputs64(d), cu=d["cu"])
+    within(o[:, :end], want[0][:, :end], size[0][:, :end], torch.bfloat16, n, "o", PARTS[torch.bfloat16])
+    within(ht, want[1], size[1], torch.float32, n, "ht")
+    do = f64(d["do"]).clone()
+    do[:, end:] = 0
+    got = chunk_linear_attn_bwd(g["q"], g["k"], g["v"], g["g"], g["do"], g["h0"], dht=g["dht"], cu_seqlens=g["cu"])
+    want, size = (f(*inputs64(d), do, f64(d["dht"]), cu=d["cu"]) for f in (ref.attn_grads, ref.grad_sizes))
+    for i, name in enumerate(("dq", "dk", "dv", "dg")):
+        t = torch.float32 if name == "dg" else torch.bfloat16
+        within(got[name][:, :end], want[i][:, :end], size[i][:, :end], t, n + 3, name, PARTS[t] if name == "dv" else 0.0)
+    within(got["dh0"], want[4], size[4], torch.float32, n, "dh0")
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
 def test_resets_and_strong_decays(dtype):
     """-inf, decays far below fp32's range, zero decays, and weak ones next to them in one chunk."""
