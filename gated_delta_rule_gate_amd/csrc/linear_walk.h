@@ -676,17 +676,30 @@ void linear_walk_kernel(LinearWalk p) {
 
     // ---- the state ----
     const float dec = tab[256];
+    // two tiles at a time: products into one accumulator lie two apart
 #pragma unroll
-    for (int t = 0; t < F::NT; ++t) {
+    for (int t = 0; t < F::NT; t += 2) {
+      bf16x8_t a[2][KS][IN];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int pl = 0; pl < IN; ++pl)
+            a[u][s][pl] = load_frag32_at(sZ + pl * F::XPL + 32 * s * F::LDX + state_channel(t + u, 0), F::LDX, tz);
       S[t] *= dec;
+      S[t + 1] *= dec;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        bf16x8_t a[IN];
+      for (int s = 0; s < KS; ++s)
 #pragma unroll
-        for (int pl = 0; pl < IN; ++pl) a[pl] = load_frag32_at(sZ + pl * F::XPL + 32 * s * F::LDX + state_channel(t, 0), F::LDX, tz);
-        S[t] = mma_parts(a, wc[s], S[t]);
-      }
-      if (KEEP && (t & 1)) split_state(t / 2);
+        for (int i = IN - 1; i >= 0; --i)
+#pragma unroll
+          for (int j = 2; j >= 0; --j)
+            if (i + j < 3) {
+#pragma unroll
+              for (int u = 0; u < 2; ++u) S[t + u] = Mma<bf16_t>::mma(a[u][s][i], wc[s][j], S[t + u]);
+            }
+      if (KEEP) split_state(t / 2);
     }
     if (!REV && anchored(t0, L)) {
       float *dst = p.ckpt + ((t0 + L) / kLinearAnchor) * fragH + frag;
