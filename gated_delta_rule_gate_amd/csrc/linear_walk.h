@@ -210,8 +210,8 @@ struct RowsMove {
 //                 loads of c + 2
 // so the state's chain holds no load, no decay and no score. Where LDS holds one
 // chunk's scores the helpers form those of c beside a (x S) and bring c + 1
-// afterwards; where it holds one chunk's rows (fp32 from 128 wide), those go to
-// LDS in a period of their own. Products that give y and scores are taken
+// afterwards; where it holds one chunk's rows (fp32 by 128 columns or 256
+// wide), those go to LDS in a period of their own. Products that give y and scores are taken
 // transposed, so that a lane holds four neighbouring columns of one row and both
 // leave in 8-byte pieces.
 template <typename T, int PT, int NW, bool REV, int OPL, int MODE>
