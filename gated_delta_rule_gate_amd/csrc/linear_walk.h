@@ -770,7 +770,7 @@ hipError_t launch_modes(const LinearWalk &p, hipStream_t st) {
     // The state pass's segments (all but a sequence's last; packed, about the
     // multiples of seg) by 64 columns where by 128 they leave half the compute
     // units idle: the same waves, two to a SIMD less (one segment of 1024 tokens
-    // on each of 128 (sequence, head) pairs: 42 us by 128, 33 us by 64).
+    // on each of 128 (sequence, head) pairs: 43 us by 128, 36 us by 64).
     const int64_t segs = p.cu ? ((int64_t)p.B * p.T) / p.seg : (int64_t)p.N * ((p.T + p.seg - 1) / p.seg - 1);
     const bool halves = NW > 4 && segs * p.H * ((p.Q + 127) / 128) * 2 <= device_cus();
     hipError_t e = halves ? launch_one<T, PT, 4, REV, 1, kState>(p, st) : launch_one<T, PT, NW, REV, 1, kState>(p, st);
