@@ -78,14 +78,16 @@ _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getC
 
 def _on_device(f):
     """Runs f with its first tensor's device current: workspace sizes and launches go by it."""
+    first = f.__code__.co_varnames[0]
 
     @functools.wraps(f)
-    def g(x, *args, **kw):
-        i = x.get_device()
+    def g(*args, **kw):
+        x = args[0] if args else kw.get(first)
+        i = x.get_device() if isinstance(x, torch.Tensor) else -1
         if i < 0 or i == _current_device():
-            return f(x, *args, **kw)
+            return f(*args, **kw)
         with torch.cuda.device(i):
-            return f(x, *args, **kw)
+            return f(*args, **kw)
 
     return g
 

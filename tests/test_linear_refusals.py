@@ -143,6 +143,22 @@ def test_python_checks():
         block_norm_bwd(q, None)
 
 
+def test_tensors_by_keyword():
+    """Every argument can be named, the first too; one that is left out is named in the error."""
+    from gated_delta_rule_gate_amd import (block_norm, block_norm_bwd, chunk_linear_attn, chunk_linear_attn_bwd,
+                                           linear_workspace_bytes, recurrent_linear_attn)
+
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    t = dict(q=q, k=q, v=q, g=torch.zeros(1, 4, 2))
+    for f, kw in ((chunk_linear_attn, t), (recurrent_linear_attn, t), (chunk_linear_attn_bwd, dict(t, do=q)),
+                  (block_norm, dict(x=q)), (block_norm_bwd, dict(x=q, dy=q))):
+        with pytest.raises(ValueError, match="must be on a GPU"):
+            f(**kw)
+        with pytest.raises(TypeError, match="missing"):
+            f()
+    assert linear_workspace_bytes(**t) == linear_workspace_bytes(*t.values())
+
+
 @pytest.mark.gpu
 def test_python_checks_on_the_device():
     from kda_testlib import need_gpu
