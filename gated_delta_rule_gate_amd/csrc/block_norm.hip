@@ -450,7 +450,7 @@ hipError_t launch_nv(const BlockNorm &p, bool bwd, hipStream_t st) {
   const int64_t need = (p.rows + RPB - 1) / RPB;
   if (bwd) {
     const int blocks = bwd_blocks(p.rows, p.D);
-    if (p.dz)
+    if (p.dz || p.dnext_weight)  // without rows dz has no address, and dnext_weight is zero
       hipLaunchKernelGGL((block_norm_bwd_kernel<Tx, Tr, LPR, NV, true>), dim3(blocks), dim3(block_threads(LPR)), 0, st, p);
     else
       hipLaunchKernelGGL((block_norm_bwd_kernel<Tx, Tr, LPR, NV, false>), dim3(blocks), dim3(block_threads(LPR)), 0, st, p);

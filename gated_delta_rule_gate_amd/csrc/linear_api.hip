@@ -354,7 +354,7 @@ extern "C" kda_status kda_block_norm_fwd(const kda_norm_args *a, const void *x, 
                                          void *y, void *z, void *stream) {
   const kda_status s = check_norm(a);
   if (s != KDA_OK) return s;
-  if (!residual && a->res_dtype != a->dtype) return KDA_ERR_DTYPE;
+  if (a->rows > 0 && !residual && a->res_dtype != a->dtype) return KDA_ERR_DTYPE;  // no rows: no address
   if (a->rows > 0 && (!x || !y)) return KDA_ERR_NULL;
   if (!aligned16(x) || !aligned16(weight) || !aligned16(gate) || !aligned16(residual) || !aligned16(scale_vec) ||
       !aligned16(next_weight) || !aligned16(y) || !aligned16(z))
@@ -376,8 +376,9 @@ extern "C" kda_status kda_block_norm_bwd(const kda_norm_args *a, const void *x, 
                                          size_t ws_bytes, void *stream) {
   const kda_status s = check_norm(a);
   if (s != KDA_OK) return s;
-  if (!residual && a->res_dtype != a->dtype) return KDA_ERR_DTYPE;
-  if (a->rows > 0 && (!x || !dx || (!dy && !dz) || (gate && !dgate))) return KDA_ERR_NULL;
+  if (a->rows > 0 && !residual && a->res_dtype != a->dtype) return KDA_ERR_DTYPE;  // no rows: no address
+  if (a->rows > 0 && (!x || !dx || (!dy && !dz) || (gate && !dgate) || (dnext_weight && !dz)))
+    return KDA_ERR_NULL;
   if (!aligned16(x) || !aligned16(weight) || !aligned16(gate) || !aligned16(residual) || !aligned16(scale_vec) ||
       !aligned16(next_weight) || !aligned16(dy) || !aligned16(dz) || !aligned16(dx) || !aligned16(dgate) ||
       !aligned16(dresidual) || !aligned16(dweight) || !aligned16(dscale_vec) || !aligned16(dnext_weight))

@@ -65,7 +65,7 @@ size_t kda_block_norm_bwd_workspace_bytes(const kda_norm_args *args);
  *   dx          [rows, D]
  *   dgate       [rows, D], with gate; dresidual [rows, D] (res_dtype), or NULL.
  *               dresidual may be dy itself
- *   dweight, dscale_vec, dnext_weight   fp32 [D] or NULL (not wanted)
+ *   dweight, dscale_vec, dnext_weight   fp32 [D] or NULL (not wanted); dnext_weight needs dz
  *   workspace   ws_bytes >= kda_block_norm_bwd_workspace_bytes(args), 256-byte aligned
  * Every sum over rows has a fixed order.
  */

@@ -139,6 +139,25 @@ def test_rows_without_weights(rows, D, kind):
     run_both(make(rows, D, FP32, None, True, None, True, weights=False), "sigmoid", True, eps=1e-5, kind=kind)
 
 
+@pytest.mark.parametrize("dtype,res", [(BF16, None), (BF16, BF16), (BF16, FP32), (FP32, FP32)])
+def test_no_rows(dtype, res):
+    """A batch without rows: empty outputs, and weights' gradients of zero."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import block_norm, block_norm_bwd
+
+    d = on(make(0, 136, dtype, res, True, "channel", True))
+    common = dict(weight=d["weight"], gate=d["gate"], residual=d["residual"], scale=d["scale"],
+                  next_weight=d["next_weight"])
+    y, z = block_norm(d["x"], **common)
+    assert y.shape == z.shape == (0, 136) and y.dtype == (res or dtype) and z.dtype == dtype
+    # a workspace of NaN: every part that is summed has to be written
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+    got = block_norm_bwd(d["x"], d["dy"], dz=d["dz"], workspace=ws, **common)
+    assert got["dx"].shape == (0, 136)
+    for n in ("dweight", "dscale", "dnext_weight"):
+        assert got[n].shape == (136,) and not got[n].any(), n
+
+
 def test_only_the_next_gradient():
     """dy may be left out beside dz."""
     need_gpu()

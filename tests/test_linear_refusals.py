@@ -115,6 +115,12 @@ def test_norm_pointers(L):
     assert bwd(FAKE, None, FAKE, dw=FAKE, ws=None) == 7 and bwd(FAKE, None, FAKE, dw=FAKE, n=16) == 7
 
 
+def test_norm_gradient_of_a_next_weight_needs_dz(L):
+    a = nrm()
+    assert L.kda_block_norm_bwd(a, FAKE, None, None, None, None, None, FAKE, None, FAKE, None, None, None, None, FAKE,
+                                FAKE, 1 << 40, None) == 1
+
+
 def test_python_checks():
     from gated_delta_rule_gate_amd import block_norm, block_norm_bwd, chunk_linear_attn, recurrent_linear_attn
 
