@@ -109,6 +109,9 @@ def _attn_args(q, k, v, g, h0, cu_seqlens, scale):
     _require(v.shape[:2] == q.shape[:2] and Hk > 0 and H % Hk == 0,
              "v must be [B, T, H, V] with H a multiple of q's heads Hk")
     _require(q.dtype in (torch.bfloat16, torch.float32), "q, k, v must share dtype bf16 or fp32")
+    # the library takes 0 for "not given", so what would round to it is refused too
+    c_scale = 0.0 if scale is None else ctypes.c_float(scale).value
+    _require(scale is None or 0.0 < c_scale < float("inf"), "scale must be a positive fp32 number")
     dev, N = q.get_device(), B
     if cu_seqlens is not None:
         _require(B == 1, "packed inputs (cu_seqlens) need batch 1")
@@ -120,7 +123,7 @@ def _attn_args(q, k, v, g, h0, cu_seqlens, scale):
             _tensor("initial_state", h0, (N, H, K, V), torch.float32, dev),
             _tensor("cu_seqlens", cu_seqlens, (N + 1,), torch.int32, dev))
     a = LinearArgs(B, T, H, K, V, N, 0 if Hk == H else Hk, KDA_BF16 if q.dtype == torch.bfloat16 else KDA_F32,
-                   DECAY_HEAD if head else DECAY_TOKEN, 0.0 if scale is None else float(scale))
+                   DECAY_HEAD if head else DECAY_TOKEN, c_scale)
     return a, N, dev, ptrs
 
 
@@ -148,7 +151,7 @@ def chunk_linear_attn(q, k, v, g, initial_state=None, *, cu_seqlens=None, output
                       final_state=None, out=None, workspace=None):
     """Chunked linear attention with one decay per head. Returns (o, ht); ht is None unless requested.
 
-    S_t = exp(g_t) S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t,  scale 1/sqrt(K) unless given.
+    S_t = exp(g_t) S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t,  scale 1/sqrt(K) unless given (> 0).
     q, k are [B, T, Hk, K], v [B, T, H, V] (bf16 or fp32, H a multiple of Hk); g is the fp32
     natural-log decay, g <= 0: [B, T, H], or [H] for one fixed decay per head. -inf resets the
     state. ``initial_state`` is fp32 [N, H, K, V]; ``final_state`` may preallocate the final

@@ -149,6 +149,16 @@ def test_python_checks():
         block_norm_bwd(q, None)
 
 
+@pytest.mark.parametrize("scale", [0, 0.0, -0.125, 1e-60, float("nan"), float("inf"), 1e60])
+def test_scales(scale):
+    from gated_delta_rule_gate_amd import chunk_linear_attn, chunk_linear_attn_bwd, recurrent_linear_attn
+
+    q, g = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 4, 2)
+    for f, do in ((chunk_linear_attn, ()), (recurrent_linear_attn, ()), (chunk_linear_attn_bwd, (q,))):
+        with pytest.raises(ValueError, match="scale must be"):
+            f(q, q, q, g, *do, scale=scale)
+
+
 def test_tensors_by_keyword():
     """Every argument can be named, the first too; one that is left out is named in the error."""
     from gated_delta_rule_gate_amd import (block_norm, block_norm_bwd, chunk_linear_attn, chunk_linear_attn_bwd,
