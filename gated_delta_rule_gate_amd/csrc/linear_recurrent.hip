@@ -68,7 +68,8 @@ __global__ __launch_bounds__(256) void linear_recurrent_kernel(LinearRecurrent p
     S[r] = (p.h0 && (FULL || (col_ok && row0 + r < K))) ? load_once(p.h0 + sbase + (int64_t)(row0 + r) * p.V + col0)
                                                         : f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  __shared__ float s_k[2][KP], s_q[2][KP], s_v[2][BV];
+  __shared__ float s_k[2][KP], s_q[2][KP];
+  __shared__ __align__(16) float s_v[2][BV];
   __shared__ __align__(16) float s_red[2][4][BV];
   for (int i = 0; i < sr.len; ++i) {
     const int buf = i & 1;
