@@ -172,6 +172,10 @@ struct Raw8 {
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(T) / 2); ++i) asm volatile("" : "+v"(v[i]));
   }
+  __device__ __forceinline__ void keep(bool ok) {  // or zeros
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v[i] = ok ? v[i] : u32x4_t{0u, 0u, 0u, 0u};
+  }
   __device__ __forceinline__ void get(float (&x)[8], bool ok) const {  // zeros where !ok
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -245,15 +249,17 @@ __global__ __launch_bounds__(block_threads(LPR)) void block_norm_bwd_kernel(Bloc
   for (; row0 < p.rows; row0 += step) {
     if constexpr (!AHEAD) fetch(row0);
     const int64_t row = row0 + threadIdx.x / LPR;
+    const bool live = RPB == 1 || row < p.rows;
     const int64_t base = row * p.D;
     Raw8<Tx> cx[NV], cg[NV], cz[NEXT ? NV : 1];
     float t[NV][8], y[NEXT ? NV : 1][8];
     bool ok[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      ok[v] = row < p.rows && (v * LPR + lane) * 8 < p.D;
+      ok[v] = live && (v * LPR + lane) * 8 < p.D;
       cx[v] = rx[v];
       cg[v] = rg[v];
+      if constexpr (sizeof(Tx) == 2) cg[v].keep(ok[v]);
       rt[v].get(t[v], ok[v] && has_dy);
       if constexpr (NEXT) {
         cz[v] = rz[v];
@@ -262,9 +268,15 @@ __global__ __launch_bounds__(block_threads(LPR)) void block_norm_bwd_kernel(Bloc
     }
     if (AHEAD && row0 + step < p.rows) fetch(row0 + step);
 
+    // Past the last row and column every input is taken as zero, and a row there has
+    // no norm: with eps = 0 its statistic would be infinite, and its zeros NaN, which
+    // the parameters' sums would keep. (A bf16 gate is zeroed as it lies in memory, an
+    // fp32 gate where it is used: 8192 x 8192 with every part, bf16 323 us against 328
+    // the other way, fp32 628 us against 668.)
+    auto norm_of = [&](float mean) { return live ? 1.0f / sqrtf(mean + p.eps) : 0.f; };
     // act(gate) and its derivative; no gate: 1 and 0
     auto gate = [&](int v, float(&act)[8], float(&dact)[8]) {
-      cg[v].get(act, has_gate);
+      cg[v].get(act, has_gate && (sizeof(Tx) == 2 || ok[v]));
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float g = act[e], sg = sigmoid_f32(g), ds = sg * (1.0f - sg);
@@ -295,7 +307,7 @@ __global__ __launch_bounds__(block_threads(LPR)) void block_norm_bwd_kernel(Bloc
         for (int e = 0; e < 8; ++e) s[0] += x[e] * x[e];
       }
       row_sums<LPR, 1>(s, red, turn);
-      rho = 1.0f / sqrtf(s[0] * inv + p.eps);
+      rho = norm_of(s[0] * inv);
       apart();
       float s2[2] = {0.f, 0.f};
 #pragma unroll
@@ -315,7 +327,7 @@ __global__ __launch_bounds__(block_threads(LPR)) void block_norm_bwd_kernel(Bloc
         }
       }
       row_sums<LPR, 2>(s2, red, turn);
-      const float rho2 = 1.0f / sqrtf(s2[0] * inv2 + p.eps), m = s2[1] * inv2 * rho2 * rho2;
+      const float rho2 = norm_of(s2[0] * inv2), m = s2[1] * inv2 * rho2 * rho2;
       apart();
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
@@ -347,7 +359,7 @@ __global__ __launch_bounds__(block_threads(LPR)) void block_norm_bwd_kernel(Bloc
       }
     }
     row_sums<LPR, 2>(s3, red, turn);
-    if constexpr (!NEXT) rho = 1.0f / sqrtf(s3[0] * inv + p.eps);
+    if constexpr (!NEXT) rho = norm_of(s3[0] * inv);
     const float m = s3[1] * inv * rho * rho;
     apart();
 #pragma unroll

@@ -37,7 +37,7 @@ typedef struct {
   kda_norm_kind norm;     /* of the first norm; the second is always RMS                     */
   kda_gate_act gate_act;  /* of gate, where given                                            */
   float scale;            /* residual scale where scale_vec is NULL                          */
-  float eps;              /* >= 0                                                            */
+  float eps;              /* >= 0; with 0 a row of zeros has no norm: its results are NaN     */
 } kda_norm_args;
 
 /*

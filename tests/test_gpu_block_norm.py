@@ -312,3 +312,28 @@ def test_layer_as_used():
     A, dt = torch.zeros(H, device="cuda"), torch.zeros(H, K, device="cuda")
     ok, _ = chunk_kda(qn, kn, c(v), c(f(B, T, H, K)), torch.sigmoid(c(f(B, T, H))), A_log=A, dt_bias=dt)
     assert torch.isfinite(block_norm(ok, c(w), gate=c(gate))).all()
+
+
+@pytest.mark.parametrize("nxt", [False, True])
+@pytest.mark.parametrize("rows,D", [(5, 8), (37, 8), (5, 128), (37, 128), (5, 512), (37, 512), (3, 520)])
+def test_without_eps(rows, D, nxt):
+    """eps = 0: the places past the last row in a workgroup of several rows hold zeros, whose norm is no
+    number; they enter no sum."""
+    need_gpu()
+    for kind in ("rms", "l2"):
+        run_both(make(rows, D, BF16, FP32, True, "channel", nxt), "silu", nxt, eps=0.0, kind=kind)
+
+
+def test_infinite_gate_in_the_last_row():
+    """An infinite gate makes its own column's sums infinite and leaves the others finite: what stands past
+    the last row in a workgroup of several rows enters no sum."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import block_norm_bwd
+
+    d = make(5, 128, FP32, None, True, "channel", False)
+    d["gate"][4, 9] = float("inf")
+    g = on(d)
+    got = block_norm_bwd(g["x"], g["dy"], g["weight"], gate=g["gate"], gate_act="silu", scale=g["scale"])
+    for n in ("dweight", "dscale"):
+        assert torch.isinf(got[n][9]), n
+        assert torch.isfinite(torch.cat([got[n][:9], got[n][10:]])).all(), n
