@@ -468,7 +468,7 @@ hipError_t launch_nv(const BlockNorm &p, bool bwd, hipStream_t st) {
       hipLaunchKernelGGL((block_norm_bwd_kernel<Tx, Tr, LPR, NV, false>), dim3(blocks), dim3(block_threads(LPR)), 0, st, p);
   } else {
     if (need == 0) return hipSuccess;
-    const int64_t grid = need < 0x7fffffff ? need : 0x7fffffff;
+    const int64_t most = most_blocks(block_threads(LPR)), grid = need < most ? need : most;
     hipLaunchKernelGGL((block_norm_fwd_kernel<Tx, Tr, LPR, NV>), dim3((unsigned)grid), dim3(block_threads(LPR)), 0, st, p);
   }
   return hipGetLastError();

@@ -90,6 +90,14 @@ kda::LinearWalk walk_base(const kda_linear_args *a, const float *g, const int32_
   return w;
 }
 
+bool walk_fits(const kda_linear_args *a, int P, int Q, int seg) {
+  kda::LinearWalk w = walk_base(a, nullptr, nullptr);
+  w.P = P;
+  w.Q = Q;
+  w.seg = seg;
+  return kda::linear_walk_fits(w);
+}
+
 // The backward's workspace.
 struct BwdPlan {
   SegPlan seg;  // of all three walks: dk's starts from the boundary states of dv's
@@ -140,6 +148,7 @@ extern "C" kda_status kda_linear_chunk_fwd(const kda_linear_args *a, const void 
   const kda_status s = check_common(a, q, k, v, g, h0, cu, o, ht);
   if (s != KDA_OK) return s;
   const SegPlan plan = seg_plan(a, cu != nullptr, a->K, a->V, false);
+  if (!walk_fits(a, a->K, a->V, plan.seg)) return KDA_ERR_UNSUPPORTED;
   if (plan.total() > 0 && (!workspace || ws_bytes < plan.total())) return KDA_ERR_WORKSPACE;
   if (plan.total() > 0 && !aligned256(workspace)) return KDA_ERR_ALIGN;
   kda::LinearWalk w = walk_base(a, g, cu);
@@ -178,6 +187,10 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   if (!aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(dg) || !aligned16(dh0)) return KDA_ERR_ALIGN;
   if (s != KDA_OK) return s;
   const BwdPlan b = bwd_plan(a, cu != nullptr);
+  if (!walk_fits(a, a->V, a->K, b.seg.seg) || !walk_fits(a, a->K, a->V, b.seg.seg) ||
+      (b.heads > 0 && !kda::linear_group_sum_fits((int64_t)a->B * a->T, qk_heads(a), a->K)) ||
+      !kda::linear_dg_fits(b.items, a->H))
+    return KDA_ERR_UNSUPPORTED;
   if (!workspace || ws_bytes < b.total()) return KDA_ERR_WORKSPACE;
   if (!aligned256(workspace)) return KDA_ERR_ALIGN;
   char *at = static_cast<char *>(workspace);
@@ -307,6 +320,7 @@ extern "C" kda_status kda_linear_recurrent_fwd(const kda_linear_args *a, const v
   p.V = a->V;
   p.N = a->N;
   p.Hk = qk_heads(a);
+  if (!kda::linear_recurrent_fits(p)) return KDA_ERR_UNSUPPORTED;
   return kda::report_hip(kda::launch_linear_recurrent(p, (hipStream_t)stream));
 }
 

@@ -196,10 +196,17 @@ int linear_segment(int T, int slots, int H, int P, int Q, bool is_bf16, bool pac
   return take == 1 ? 0 : (int)((chunks + take - 1) / take * 64);
 }
 
+static int64_t chain_blocks(const LinearWalk &p) { return ((int64_t)p.P * p.Q / 4 + 255) / 256 * p.H * p.N; }
+
+bool linear_walk_fits(const LinearWalk &p) {
+  int ncb;
+  const int qt = linear_cols(p.P, p.Q, p.is_bf16, (int64_t)p.N * p.H, &ncb);
+  return linear_walk_blocks(p, ncb) <= most_blocks(64 * (qt / 16 + 4)) && (!p.seg || chain_blocks(p) <= most_blocks(256));
+}
+
 hipError_t launch_linear_chain(const LinearWalk &p, bool rev, hipStream_t st) {
-  const int64_t elems = (int64_t)p.P * p.Q;
-  const int64_t grid = (elems / 4 + 255) / 256 * p.H * p.N;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  const int64_t elems = (int64_t)p.P * p.Q, grid = chain_blocks(p);
+  if (grid > most_blocks(256)) return hipErrorInvalidValue;
   hipLaunchKernelGGL(linear_chain_kernel, dim3((unsigned)grid), dim3(256), 0, st, p, rev, elems);
   return hipGetLastError();
 }
@@ -210,11 +217,15 @@ hipError_t launch_linear_walk(const LinearWalk &p, hipStream_t st) {
   return p.reverse ? launch_linear_walk_f32_rev(p, st) : launch_linear_walk_f32_fwd(p, st);
 }
 
+static int64_t group_sum_blocks(int64_t rows, int Hk, int D) { return (rows * Hk * (D / 4) + 255) / 256; }
+
+bool linear_group_sum_fits(int64_t rows, int Hk, int D) { return group_sum_blocks(rows, Hk, D) <= most_blocks(256); }
+
 hipError_t launch_linear_group_sum(const float *in, void *out, bool is_bf16, const int32_t *cu, int N, int64_t rows,
                                    int H, int Hk, int D, hipStream_t st) {
-  const int64_t grid = (rows * Hk * (D / 4) + 255) / 256;
+  const int64_t grid = group_sum_blocks(rows, Hk, D);
   if (grid == 0) return hipSuccess;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (grid > most_blocks(256)) return hipErrorInvalidValue;
   if (is_bf16)
     hipLaunchKernelGGL(linear_group_sum_kernel<bf16_t>, dim3((unsigned)grid), dim3(256), 0, st, in,
                        reinterpret_cast<bf16_t *>(out), cu, N, rows, H, Hk, D);
@@ -228,10 +239,12 @@ int linear_chunk_rows(int P, bool is_bf16) { return !is_bf16 || linear_tile(P) =
 
 int64_t linear_dg_items(int B, int T, int N) { return N + ((int64_t)B * T) / kLinearAnchor; }
 
+bool linear_dg_fits(int64_t items, int H) { return items * ((H + 3) / 4) <= most_blocks(256); }
+
 hipError_t launch_linear_dg(const LinearDg &p, hipStream_t st) {
   const int64_t items = linear_dg_items(p.B, p.T, p.N);
   const int64_t grid = items * ((p.H + 3) / 4);
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (!linear_dg_fits(items, p.H)) return hipErrorInvalidValue;
   if (grid > 0) {
     hipLaunchKernelGGL(linear_dg_kernel, dim3((unsigned)grid), dim3(256), 0, st, p);
     hipError_t e = hipGetLastError();

@@ -15,6 +15,9 @@ kda_status report_hip(hipError_t e);
 
 int device_cus();  // compute units of the current device (chunk_fused.hip)
 
+// Workgroups of one launch: its threads are counted in 32 bits.
+constexpr int64_t most_blocks(int threads) { return 0xffffffffLL / threads; }
+
 constexpr int kLinearAnchor = 256;  // tokens between the states that anchor dg
 
 // One walk over the chunks of every sequence. With per-chunk cumulative decays
@@ -66,6 +69,17 @@ int linear_tile(int width);              // padded P: 64, 128 or 256
 int linear_cols(int P, int width, bool is_bf16, int64_t pairs, int *ncb);
 // tokens per segment for one walk with Q columns, or 0 for none; dots: a walk with row dots
 int linear_segment(int T, int slots, int H, int P, int Q, bool is_bf16, bool packed, bool dots);
+// Workgroups of a walk of ncb column blocks: a unit of those that read the same q/k
+// rows after another, units dealt to the eight XCDs.
+inline int64_t linear_walk_blocks(const LinearWalk &p, int ncb) {
+  const int64_t items = p.N + (p.seg ? ((int64_t)p.B * p.T) / p.seg : 0);
+  return (items * p.Hk + 7) / 8 * 8 * (p.H / p.Hk) * ncb;
+}
+// Whether the launches of these sizes are within HIP's limits: asked before the first
+// of a call, so that none fails behind others. (A state pass by 64 columns is taken
+// for few pairs only.)
+bool linear_walk_fits(const LinearWalk &p);
+bool linear_group_sum_fits(int64_t rows, int Hk, int D);
 hipError_t launch_linear_walk(const LinearWalk &p, hipStream_t st);
 hipError_t launch_linear_walk_bf16_fwd(const LinearWalk &p, hipStream_t st);
 hipError_t launch_linear_walk_bf16_rev(const LinearWalk &p, hipStream_t st);
@@ -95,6 +109,7 @@ struct LinearDg {
 };
 int linear_chunk_rows(int P, bool is_bf16);
 int64_t linear_dg_items(int B, int T, int N);
+bool linear_dg_fits(int64_t items, int H);
 hipError_t launch_linear_dg(const LinearDg &p, hipStream_t st);
 
 struct LinearRecurrent {
@@ -107,6 +122,7 @@ struct LinearRecurrent {
   bool g_head, is_bf16;
   int B, T, H, K, V, N, Hk;
 };
+bool linear_recurrent_fits(const LinearRecurrent &p);
 hipError_t launch_linear_recurrent(const LinearRecurrent &p, hipStream_t st);
 
 struct BlockNorm {

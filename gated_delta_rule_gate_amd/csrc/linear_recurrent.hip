@@ -110,7 +110,7 @@ template <typename T, int KP, int BV>
 hipError_t launch_rec(const LinearRecurrent &p, hipStream_t st) {
   const int64_t grid = (int64_t)p.N * p.H * ((p.V + BV - 1) / BV);
   if (grid == 0) return hipSuccess;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (grid > most_blocks(256)) return hipErrorInvalidValue;
   const bool full = p.K == KP && p.V % BV == 0, one = !p.cu && p.T == 1;
   auto kern = full ? (one ? linear_recurrent_kernel<T, KP, BV, true, true> : linear_recurrent_kernel<T, KP, BV, true, false>)
                    : (one ? linear_recurrent_kernel<T, KP, BV, false, true> : linear_recurrent_kernel<T, KP, BV, false, false>);
@@ -132,6 +132,11 @@ hipError_t launch_rec_t(const LinearRecurrent &p, hipStream_t st) {
 }
 
 }  // namespace
+
+// (blocks of 32 columns are for launches far below the limit)
+bool linear_recurrent_fits(const LinearRecurrent &p) {
+  return (int64_t)p.N * p.H * ((p.V + 127) / 128) <= most_blocks(256);
+}
 
 hipError_t launch_linear_recurrent(const LinearRecurrent &p, hipStream_t st) {
   return p.is_bf16 ? launch_rec_t<bf16_t>(p, st) : launch_rec_t<float>(p, st);

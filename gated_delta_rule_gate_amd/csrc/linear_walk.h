@@ -757,9 +757,8 @@ hipError_t launch_one(const LinearWalk &p, hipStream_t st) {
     return e;
   }
   const int ncb = (p.Q + F::QT - 1) / F::QT;
-  const int64_t items = p.N + (p.seg ? ((int64_t)p.B * p.T) / p.seg : 0);
-  const int64_t grid = (items * p.Hk + 7) / 8 * 8 * (p.H / p.Hk) * ncb;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  const int64_t grid = linear_walk_blocks(p, ncb);
+  if (grid > most_blocks(F::THREADS)) return hipErrorInvalidValue;
   hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(F::THREADS), F::total, st, p);
   return hipGetLastError();
 }

@@ -74,7 +74,9 @@ size_t kda_linear_chunk_workspace_bytes(const kda_linear_args *args);
  *              aligned; may be NULL when that is 0
  * Supported: K and V multiples of 8 in [8, 256], equal or not. Errors:
  * KDA_ERR_NULL, _SHAPE, _DTYPE, _GATE (unknown decay kind), _ALIGN,
- * _WORKSPACE, _UNSUPPORTED (widths), _HIP.
+ * _WORKSPACE, _UNSUPPORTED (widths, or more work than one launch takes: about
+ * 5.5 million (sequence, head, 128 columns) here and in the gradient, 16.7
+ * million in the recurrence; found before anything is launched), _HIP.
  */
 kda_status kda_linear_chunk_fwd(const kda_linear_args *args, const void *q, const void *k, const void *v,
                                 const float *g, const float *h0, const int32_t *cu_seqlens, void *o, float *ht,

@@ -337,3 +337,30 @@ def test_infinite_gate_in_the_last_row():
     for n in ("dweight", "dscale"):
         assert torch.isinf(got[n][9]), n
         assert torch.isfinite(torch.cat([got[n][:9], got[n][10:]])).all(), n
+
+
+def test_more_rows_than_a_launch_has_workgroups():
+    """A launch's threads are counted in 32 bits: 2^25 rows of a 128-thread workgroup each go through twice."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import block_norm
+
+    D, most = 520, (2 ** 32 - 1) // 128
+    rows = most + 70
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 90e9:
+        pytest.skip("needs 70 GB of GPU memory")
+    x = torch.empty(rows, D, dtype=BF16, device="cuda").fill_(0.5)
+    y = torch.empty_like(x).fill_(float("nan"))
+    w = torch.from_numpy(np.random.Generator(np.random.PCG64(8)).standard_normal(D).astype(np.float32)).cuda()
+    at = [0, 1, 69, 70, most - 1, most, most + 1, rows - 1]
+    own = torch.from_numpy(np.random.Generator(np.random.PCG64(9)).standard_normal((len(at), D)).astype(np.float32))
+    own = own.to(BF16).cuda()
+    for i, r in zip(at, own):
+        x[i].copy_(r)
+    block_norm(x, w, out=y)
+    assert torch.equal(torch.stack([y[i] for i in at]), block_norm(own, w))
+    rest = block_norm(torch.full((1, D), 0.5, dtype=BF16, device="cuda"), w)
+    other = sum((y[i:i + (1 << 22)] != rest).any(-1).sum().item() for i in range(0, rows, 1 << 22))
+    assert other == len(at)
+    del x, y
+    torch.cuda.empty_cache()

@@ -203,3 +203,38 @@ def test_python_checks_on_the_device():
         chunk_linear_attn(z, z, q, g)
     with pytest.raises(KdaError, match="UNSUPPORTED"):
         block_norm(torch.zeros(3, 12, device="cuda"))
+
+
+@pytest.mark.parametrize("sizes,wide", [
+    # (sequence, head) pairs times threads of a workgroup: 2^32 and more than a launch counts
+    (dict(B=4096, N=4096, H=4096), False),             # the recurrence: 256 threads
+    (dict(B=2048, N=2048, H=4096, K=64, V=64), True),  # chunked by 64 columns: 512 threads
+    (dict(B=1366, N=1366, H=4096), True),              # by 128 columns: 768
+    (dict(B=683, N=683, H=4096, V=256), True),
+    (dict(N=2048, H=4096, K=64, V=64), True),          # packed
+])
+def test_more_workgroups_than_a_launch_takes(L, sizes, wide):
+    """Refused before the first launch, so that no output is written by half."""
+    a = lin(T=1, **sizes)
+    cu = FAKE if a.B != a.N else None
+    if wide:
+        assert L.kda_linear_chunk_fwd(a, FAKE, FAKE, FAKE, FAKE, None, cu, FAKE, None, FAKE, 1 << 50, None) == 8
+        assert L.kda_linear_chunk_bwd(a, FAKE, FAKE, FAKE, FAKE, None, cu, FAKE, None, FAKE, FAKE, FAKE, FAKE, None, FAKE,
+                                      1 << 50, None) == 8
+    else:
+        assert L.kda_linear_recurrent_fwd(a, FAKE, FAKE, FAKE, FAKE, None, cu, FAKE, None, None) == 8
+
+
+def test_the_largest_launches_are_not_refused(L):
+    """One pair of a sequence fewer: the sizes are taken, and the missing workspace is what is wrong."""
+    for kw in (dict(B=2047, N=2047, H=4096, K=64, V=64), dict(B=1365, N=1365, H=4096)):
+        a = lin(T=1, **kw)
+        assert L.kda_linear_chunk_bwd(a, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE, FAKE, FAKE, FAKE, None,
+                                      None, 0, None) == 7
+    # shared heads: their gradients' sum, 2^32 pieces of four values
+    big = lin(B=1, N=1, T=1 << 24, H=8, Hk=4, K=256, V=8)
+    assert L.kda_linear_chunk_bwd(big, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE, FAKE, FAKE, FAKE, None, None,
+                                  0, None) == 8
+    big.T -= 1
+    assert L.kda_linear_chunk_bwd(big, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE, FAKE, FAKE, FAKE, None, None,
+                                  0, None) == 7
