@@ -73,7 +73,9 @@ def _tensor(name, t, shape, dtype, device):
     return t.data_ptr()
 
 
-_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# PyTorch's own cheap forms of the public calls, which a build without a GPU does not have
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _on_device(f):

@@ -238,3 +238,28 @@ def test_the_largest_launches_are_not_refused(L):
     big.T -= 1
     assert L.kda_linear_chunk_bwd(big, FAKE, FAKE, FAKE, FAKE, None, None, FAKE, None, FAKE, FAKE, FAKE, FAKE, None, None,
                                   0, None) == 7
+
+
+def test_import_without_gpu_bindings():
+    """A PyTorch build without a GPU imports the package; calls are refused for their tensors' device."""
+    import subprocess
+    import sys
+
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import gated_delta_rule_gate_amd as p
+q = torch.zeros(1, 4, 2, 64)
+try:
+    p.chunk_linear_attn(q, q, q, torch.zeros(2))
+except ValueError as e:
+    assert "must be on a GPU" in str(e), e
+else:
+    raise AssertionError("not refused")
+print("imported", p.linear_workspace_bytes(q, q, q, torch.zeros(2)))
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=300)
+    assert r.returncode == 0 and r.stdout.startswith("imported"), r.stderr[-2000:]
