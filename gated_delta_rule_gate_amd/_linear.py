@@ -1,6 +1,8 @@
 """Bindings of include/kda_linear.h and include/kda_norm.h: linear attention with one decay
 per head, and the norms round an attention block. Argument checks and marshalling only;
-everything runs in libkda.so, on the tensors' device and its current stream.
+everything runs in libkda.so, on the tensors' device and its current stream. Nothing is
+recorded for autograd: a tensor that requires grad is refused while gradients are recorded,
+and taken under torch.no_grad() and inside an autograd.Function.
 """
 import ctypes
 import functools
@@ -60,15 +62,16 @@ def _refuse(name, t, shape, dtype, device):
         raise ValueError("%s must be on %s" % (name, "a GPU" if device < 0 else "cuda:%d" % device))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    raise RuntimeError("%s requires grad: this op does not track gradients; call its _bwd for them" % name)
+    raise RuntimeError("%s requires grad: this op records no gradients; call it under torch.no_grad() or inside an "
+                       "autograd.Function, and its _bwd for them" % name)
 
 
 def _tensor(name, t, shape, dtype, device):
     """A tensor's pointer, after its checks; None for None. device: the GPU's index, -1 for none."""
     if t is None:
         return None
-    if (t.shape != shape or t.dtype is not dtype or device < 0 or t.get_device() != device or t.requires_grad
-            or not t.is_contiguous()):
+    if (t.shape != shape or t.dtype is not dtype or device < 0 or t.get_device() != device
+            or (t.requires_grad and torch.is_grad_enabled()) or not t.is_contiguous()):
         _refuse(name, t, shape, dtype, device)
     return t.data_ptr()
 

@@ -263,3 +263,64 @@ print("imported", p.linear_workspace_bytes(q, q, q, torch.zeros(2)))
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=300)
     assert r.returncode == 0 and r.stdout.startswith("imported"), r.stderr[-2000:]
+
+
+def _calls(q, w, g):
+    """Every entry point, on inputs of which any may require a gradient."""
+    from gated_delta_rule_gate_amd import (block_norm, block_norm_bwd, chunk_linear_attn, chunk_linear_attn_bwd,
+                                           recurrent_linear_attn)
+
+    d = q.detach()
+    return dict(chunk=lambda: chunk_linear_attn(q, d, d, g), recurrent=lambda: recurrent_linear_attn(q, d, d, g),
+                chunk_bwd=lambda: chunk_linear_attn_bwd(q, d, d, g, d), norm=lambda: block_norm(d, w),
+                norm_bwd=lambda: block_norm_bwd(d, d, w))
+
+
+@pytest.mark.gpu
+def test_gradients_that_are_not_recorded():
+    """Parameters are taken as they are where no gradient is recorded (no_grad, inference mode, inside an
+    autograd.Function) and refused where one would be lost, naming the way out."""
+    from kda_testlib import need_gpu
+
+    need_gpu()
+    plain = (torch.randn(1, 4, 2, 64, device="cuda").bfloat16(), torch.randn(64, device="cuda"),
+             -torch.rand(1, 4, 2, device="cuda"))
+    leaves = tuple(t.clone().requires_grad_(True) for t in plain)
+    flat = lambda r: [t for t in (r.values() if isinstance(r, dict) else r if isinstance(r, tuple) else [r])  # noqa: E731
+                      if t is not None]
+    for name, want in _calls(*plain).items():
+        want, call = flat(want()), _calls(*leaves)[name]
+        with pytest.raises(RuntimeError, match="requires grad.*no_grad"):
+            call()
+        for mode in (torch.no_grad, torch.inference_mode):
+            with mode():
+                got = flat(call())
+            assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want)), name
+            assert not any(t.requires_grad for t in got)
+
+
+@pytest.mark.gpu
+def test_inside_an_autograd_function():
+    """The forward and its _bwd as a user's autograd.Function calls them."""
+    from kda_testlib import need_gpu
+
+    need_gpu()
+    from gated_delta_rule_gate_amd import block_norm, block_norm_bwd
+
+    class Norm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight):
+            ctx.save_for_backward(x, weight)
+            return block_norm(x, weight)
+
+        @staticmethod
+        def backward(ctx, dy):
+            x, weight = ctx.saved_tensors
+            got = block_norm_bwd(x, dy.contiguous(), weight)
+            return got["dx"], got["dweight"]
+
+    x, w = (torch.randn(*s, device="cuda").requires_grad_(True) for s in ((5, 64), (64,)))
+    dy = torch.randn(5, 64, device="cuda")
+    (Norm.apply(x, w) * dy).sum().backward()
+    want = block_norm_bwd(x.detach(), dy, w.detach())
+    assert torch.equal(x.grad, want["dx"]) and torch.equal(w.grad, want["dweight"])
