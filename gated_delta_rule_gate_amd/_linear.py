@@ -259,6 +259,7 @@ def block_norm(x, weight=None, *, gate=None, gate_act="sigmoid", residual=None, 
     """
     nxt = next_weight is not None if next_norm is None else bool(next_norm)
     _require(nxt or next_weight is None, "next_weight needs the next norm")
+    _require(nxt or next_out is None, "next_out needs the next norm")
     a, (px, pw, pg, pr, ps, pn), res, _ = _norm_args(x, weight, gate, gate_act, residual, scale, next_weight, eps, norm)
     y = torch.empty_like(x, dtype=res) if out is None else out
     dev = x.get_device()

@@ -324,3 +324,12 @@ def test_inside_an_autograd_function():
     (Norm.apply(x, w) * dy).sum().backward()
     want = block_norm_bwd(x.detach(), dy, w.detach())
     assert torch.equal(x.grad, want["dx"]) and torch.equal(w.grad, want["dweight"])
+
+
+def test_a_next_output_needs_the_next_norm():
+    from gated_delta_rule_gate_amd import block_norm
+
+    x = torch.zeros(3, 64)
+    for kw in (dict(), dict(next_norm=False)):
+        with pytest.raises(ValueError, match="next_out needs the next norm"):
+            block_norm(x, next_out=torch.zeros(3, 64), **kw)
