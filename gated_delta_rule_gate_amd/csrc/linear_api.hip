@@ -101,12 +101,12 @@ bool walk_fits(const kda_linear_args *a, int P, int Q, int seg) {
 // The backward's workspace.
 struct BwdPlan {
   SegPlan seg;  // of all three walks: dk's starts from the boundary states of dv's
-  size_t segs, ckpt, dots, adot, edot, heads, part;
+  size_t segs, ckpt, dots, adot, ends, heads, part;
   int ncb;
   int64_t anchors, items;
   size_t total() const {
-    return align_up(segs) + align_up(ckpt) + 4 * align_up(dots) + align_up(adot) + align_up(edot) + align_up(heads) +
-           align_up(part);
+    return align_up(segs) + align_up(ckpt) + 4 * align_up(dots) + align_up(adot) + 2 * align_up(ends) +
+           align_up(heads) + align_up(part);
   }
 };
 
@@ -120,7 +120,7 @@ BwdPlan bwd_plan(const kda_linear_args *a, bool packed) {
   b.ckpt = 4 * (size_t)b.anchors * a->H * b.ncb * kda::linear_tile(a->V) * qt;
   b.dots = 4 * (size_t)b.ncb * a->H * rows;
   b.adot = 4 * (size_t)b.anchors * a->H * b.ncb;
-  b.edot = 4 * (size_t)a->N * a->H * b.ncb;
+  b.ends = 4 * (size_t)a->N * a->H * b.ncb;
   b.heads = qk_heads(a) != a->H ? 4 * (size_t)rows * a->H * a->K : 0;
   b.items = kda::linear_dg_items(a->B, a->T, a->N);
   b.part = a->decay == KDA_DECAY_HEAD ? 8 * (size_t)b.items * a->H : 0;
@@ -203,7 +203,8 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   float *ckpt = reinterpret_cast<float *>(take(b.ckpt));
   float *dot_q = reinterpret_cast<float *>(take(b.dots)), *dot_k = reinterpret_cast<float *>(take(b.dots));
   float *far_q = reinterpret_cast<float *>(take(b.dots)), *far_k = reinterpret_cast<float *>(take(b.dots));
-  float *adot = reinterpret_cast<float *>(take(b.adot)), *edot = reinterpret_cast<float *>(take(b.edot));
+  float *adot = reinterpret_cast<float *>(take(b.adot));
+  float *sdot = reinterpret_cast<float *>(take(b.ends)), *edot = reinterpret_cast<float *>(take(b.ends));
   float *heads = reinterpret_cast<float *>(take(b.heads));
   double *part = reinterpret_cast<double *>(take(b.part));
   const int Hk = qk_heads(a);
@@ -256,7 +257,7 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   e = kda::launch_linear_walk(r, st);
   if (e != hipSuccess) return kda::report_hip(e);
 
-  // dk: the reverse walk of dh^T, with <h, dh> at the anchors
+  // dk: the reverse walk of dh^T, with <h, dh> at the anchors and at its end
   w.reverse = true;
   w.x = v;
   w.z = d_o;
@@ -266,8 +267,8 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   w.dot = dot_k;
   w.dot_far = far_k;
   w.s0 = dht;
-  w.s_dot = nullptr;
-  w.end_dot = nullptr;
+  w.s_dot = h0;
+  w.end_dot = h0 ? sdot : nullptr;
   w.anchor_dot = adot;
   set_segments(w, b.seg, segs, false);
   w.seg_ready = true;  // dv's boundary states, read across
@@ -283,6 +284,7 @@ extern "C" kda_status kda_linear_chunk_bwd(const kda_linear_args *a, const void 
   d.b_far = far_k;
   d.chunk = kda::linear_chunk_rows(a->V, a->dtype == KDA_BF16);
   d.anchor_dot = adot;
+  d.start_dot = h0 ? sdot : nullptr;
   d.end_dot = dht ? edot : nullptr;
   d.cu = cu;
   d.dg = dg;

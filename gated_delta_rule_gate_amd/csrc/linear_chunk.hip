@@ -61,6 +61,10 @@ __global__ __launch_bounds__(256) void linear_group_sum_kernel(const float *in, 
 
 // dg over one anchored stretch of one (sequence, head): a wave takes the
 // stretch, a lane kDgPer neighbouring tokens, all of one chunk; sums in fp64.
+// Each token's value comes from the side whose squares add up to less: a large
+// <ht, dht> at the end is then not carried to tokens that it has decayed away from,
+// where only its error would be left (fp32, 256 x 256, 1000 tokens: dg off by 3.2e-6
+// of its norm summed from the end, by 0.8e-6 so).
 // 9 us for 4 x 2048 tokens of 32 heads (5 MB of dots): latency of its few waves.
 constexpr int kDgPer = kLinearAnchor / 64;
 static_assert(32 % kDgPer == 0, "a lane's tokens lie in one chunk");
@@ -80,47 +84,63 @@ __global__ __launch_bounds__(256) void linear_dg_kernel(LinearDg p) {
   double sum = 0.0;
   if (ok) {
     const int64_t rows = (int64_t)p.B * p.T;
-    double carry = 0.0;  // <h, dh> behind the stretch
+    double before = 0.0, behind = 0.0;  // <h, dh> at the stretch's ends
     for (int cb = 0; cb < p.ncb; ++cb) {
-      if (sg.out >= 0) carry += p.anchor_dot[(sg.out * p.H + h) * p.ncb + cb];
-      else if (p.end_dot) carry += p.end_dot[((int64_t)sg.n * p.H + h) * p.ncb + cb];
+      const int64_t slot = ((int64_t)sg.n * p.H + h) * p.ncb + cb;
+      if (sg.in >= 0) before += p.anchor_dot[(sg.in * p.H + h) * p.ncb + cb];
+      else if (p.start_dot) before += p.start_dot[slot];
+      if (sg.out >= 0) behind += p.anchor_dot[(sg.out * p.H + h) * p.ncb + cb];
+      else if (p.end_dot) behind += p.end_dot[slot];
     }
-    double x[kDgPer], own = 0.0, far = 0.0;
+    // of each token a - b and a^2 + b^2, and over the lane's tokens the same of the far parts
+    double x[kDgPer], m[kDgPer], own = 0.0, own_m = 0.0, far = 0.0, far_m = 0.0;
 #pragma unroll
     for (int i = 0; i < kDgPer; ++i) {
       const int64_t t = sg.lo + lane * kDgPer + i;
-      x[i] = 0.0;
+      double a = 0.0, b = 0.0, fa = 0.0, fb = 0.0;
       if (t < sg.hi)
         for (int cb = 0; cb < p.ncb; ++cb) {
           const int64_t at = ((int64_t)cb * p.H + h) * rows + t;
-          x[i] += (double)p.a[at] - (double)p.b[at];
-          far += (double)p.a_far[at] - (double)p.b_far[at];
+          a += p.a[at];
+          b += p.b[at];
+          fa += p.a_far[at];
+          fb += p.b_far[at];
         }
-      own += x[i];
+      own += x[i] = a - b;
+      own_m += m[i] = a * a + b * b;
+      far += fa - fb;
+      far_m += fa * fa + fb * fb;
     }
     const int lanes = p.chunk / kDgPer, place = lane % lanes;
-    double run = 0.0;  // a - b of the chunk's later lanes
-    for (int off = 1; off < lanes; ++off) {
-      const double v = __shfl_down(own, off);
-      if (place + off < lanes) run += v;
-    }
-    double after = far;  // of this lane's tokens and all later ones
+    // of this lane's tokens and all later ones: to the chunk's end, and of the far parts to the stretch's
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
-      const double v = __shfl_down(after, off);
-      if (lane + off < 64) after += v;
-    }
-    const int next = lane - place + lanes;  // the next chunk's first lane
-    const double later = __shfl(after, next & 63);
-    run += carry + (next < 64 ? later : 0.0);
-#pragma unroll
-    for (int i = kDgPer - 1; i >= 0; --i) {
-      run += x[i];
-      const int64_t t = sg.lo + lane * kDgPer + i;
-      if (t < sg.hi) {
-        sum += run;
-        if (!p.g_head) p.dg[t * p.H + h] = (float)run;
+      const double v = __shfl_down(far, off), vm = __shfl_down(far_m, off);
+      if (lane + off < 64) far += v, far_m += vm;
+      if (off < lanes) {
+        const double w = __shfl_down(own, off), wm = __shfl_down(own_m, off);
+        if (place + off < lanes) own += w, own_m += wm;
       }
+    }
+    const int head = lane - place, next = head + lanes;  // first lanes of this chunk and of the next
+    const double all = __shfl(far, 0), all_m = __shfl(far_m, 0);
+    const double here = __shfl(far, head), here_m = __shfl(far_m, head);
+    double later = __shfl(far, next & 63), later_m = __shfl(far_m, next & 63);
+    if (next >= 64) later = later_m = 0.0;
+    const double whole = __shfl(own, head), whole_m = __shfl(own_m, head);
+    // from the end, and from the start, where <h, dh> less all that came before is what is left
+    double back = behind + later + own, back_m = behind * behind + later_m + own_m;
+    double fore = before - (all - here) - (whole - own), fore_m = before * before + (all_m - here_m) + (whole_m - own_m);
+#pragma unroll
+    for (int i = 0; i < kDgPer; ++i) {
+      const int64_t t = sg.lo + lane * kDgPer + i;
+      const double d = fore_m < back_m ? fore : back;
+      if (t < sg.hi) {
+        sum += d;
+        if (!p.g_head) p.dg[t * p.H + h] = (float)d;
+      }
+      back -= x[i], back_m -= m[i];
+      fore -= x[i], fore_m += m[i];
     }
   }
   if (p.g_head) {

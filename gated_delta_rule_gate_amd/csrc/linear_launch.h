@@ -44,7 +44,7 @@ struct LinearWalk {
   const float *s0;        // state at the start of the walk or null, [N, H, P x Q]
   float *sT;              // state at its end or null
   int64_t sp, sq;         // strides of the state's P and Q axes in s0, sT and s_dot
-  const float *s_dot;     // with end_dot: state-shaped partner of the last state
+  const float *s_dot;     // with end_dot (and sp == 1): state-shaped partner of the last state
   float *end_dot;         // [N, H, ncb] or null
   float *ckpt;            // with u: states every kLinearAnchor tokens of a sequence, written by a
   float *anchor_dot;      // forward walk; a reverse walk leaves <ckpt, S> there, [.., H, ncb]
@@ -96,10 +96,11 @@ hipError_t launch_linear_group_sum(const float *in, void *out, bool is_bf16, con
 // that the cancelled terms' roundings do not add up, that sum runs to the end of
 // t's chunk only; there it is <h, dh>, which is carried over chunks by the dots'
 // parts through the states alone (a chunk's own pairs sum to zero) from every
-// kLinearAnchor-th token, where the states themselves are at hand.
+// kLinearAnchor-th token, where the states themselves are at hand; or the same
+// from the other side, <h, dh> before t less a - b of the tokens up to t.
 struct LinearDg {
   const float *a, *b, *a_far, *b_far;  // [ncb][H][rows]
-  const float *anchor_dot, *end_dot;  // end_dot null: zero
+  const float *anchor_dot, *start_dot, *end_dot;  // <h0, dh0> and <ht, dht>, null: zero
   const int32_t *cu;
   float *dg;
   double *part;        // head decays: [items][H] sums

@@ -256,7 +256,8 @@ void linear_walk_kernel(LinearWalk p) {
     return reinterpret_cast<bf16_t *>(smem + F::oP + (F::PBUF == 2 && (cc & 1) ? F::nP : 0u));
   };
   auto tab_at = [&](int cc) { return reinterpret_cast<float *>(smem + F::oTab + ((cc & 1) ? F::tab : 0u)); };
-  float *const sRed = reinterpret_cast<float *>(smem + F::oRed), *const sAnc = sRed + (MODE == kDots ? 2 * NW * 64 : 0);
+  float *const sRed = reinterpret_cast<float *>(smem + F::oRed);
+  double *const sAnc = reinterpret_cast<double *>(sRed + (MODE == kDots ? 2 * NW * 64 : 0));  // a value of every state wave
   // whole multiples of kLinearAnchor tokens into the sequence, before its end
   auto anchored = [&](int64_t t0, int L) {
     return MODE == kDots && (((uint32_t)(t0 - sg.a) + L) % kLinearAnchor) == 0 && t0 + L < sg.e;
@@ -405,10 +406,10 @@ void linear_walk_kernel(LinearWalk p) {
       const int L = rows_of(cc);
       const int64_t t0 = first + (int64_t)cc * STEP;
       if (anchored(t0, L) && ht == 0) {
-        float d = 0.f;
+        double d = 0.0;
 #pragma unroll
         for (int w = 0; w < NW; ++w) d += sAnc[w];
-        p.anchor_dot[(((t0 + L) / kLinearAnchor) * p.H + h) * ncb + cb] = d;
+        p.anchor_dot[(((t0 + L) / kLinearAnchor) * p.H + h) * ncb + cb] = (float)d;
       }
     };
 
@@ -449,9 +450,9 @@ void linear_walk_kernel(LinearWalk p) {
     if (MODE == kDots && p.end_dot && sg.out < 0) {
       __syncthreads();
       if (ht == 0) {
-        float d = 0.f;
+        double d = 0.0;
         for (int w = 0; w < NW; ++w) d += sAnc[w];
-        p.end_dot[((int64_t)sg.n * p.H + h) * ncb + cb] = d;
+        p.end_dot[((int64_t)sg.n * p.H + h) * ncb + cb] = (float)d;
       }
     }
     return;
@@ -730,14 +731,18 @@ void linear_walk_kernel(LinearWalk p) {
         }
     }
     if (MODE == kDots && p.end_dot) {
-      float d = 0.f;
+      // fp64: in fp32 a lane's 32 or 64 sums in a row were off by twice what the states are.
+      // (the P axis of these states is the inner one: four channels to a load)
+      double d = 0.0;
 #pragma unroll
-      for (int t = 0; t < F::NT; ++t)
+      for (int t = 0; t < F::NT; ++t) {
+        const int r = state_channel(t, grp);
+        if (r < P && q < Q) {
+          const f32x4_t u = *reinterpret_cast<const f32x4_t *>(p.s_dot + sbase + r + q * p.sq);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = state_channel(t, grp) + e;
-          if (r < P && q < Q) d += S[t][e] * p.s_dot[sbase + r * p.sp + q * p.sq];
+          for (int e = 0; e < 4; ++e) d += (double)S[t][e] * (double)u[e];
         }
+      }
 #pragma unroll
       for (int off = 32; off > 0; off >>= 1) d += __shfl_xor(d, off);
       if (lane == 0) sAnc[wave] = d;
