@@ -364,3 +364,50 @@ def test_more_rows_than_a_launch_has_workgroups():
     assert other == len(at)
     del x, y
     torch.cuda.empty_cache()
+
+
+def walk_of(rows, D):
+    """(rows of a workgroup at a time, the most rows that one of its lanes adds up)."""
+    lanes = 1
+    while lanes < 512 and lanes * 8 < D:
+        lanes *= 2
+    at_once = max(1, 256 // lanes) if lanes < 128 else 1
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    blocks = min(-(-rows // at_once), cus * (1 if D > 4096 else 1024 // lanes if D > 512 else 4))
+    return at_once, -(-rows // (blocks * at_once))
+
+
+@pytest.mark.parametrize("rows,D,dtype,res", [
+    (300007, 8, BF16, FP32), (40001, 64, FP32, FP32), (16421, 128, BF16, BF16), (9001, 512, BF16, FP32),
+    (1500, 1032, BF16, BF16), (1100, 4096, BF16, FP32), (700, 8192, BF16, BF16), (600, 8200, FP32, FP32),
+    (300, 16384, BF16, FP32),
+])
+@pytest.mark.parametrize("nxt", [False, True])
+def test_workgroups_that_walk_their_rows(rows, D, dtype, res, nxt):
+    """More rows than the workgroups hold at once: each walks several groups of rows, with parameter sums
+    over all of them and over more workgroups than are added at a time. A sum passes a rounding for every
+    row that its lane adds, and one for each lane that holds the column; over workgroups it is fp64. Leaving
+    out one workgroup's rows of one step is outside the tolerance."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import block_norm, block_norm_bwd
+
+    d = on(make(rows, D, dtype, res, True, "channel", nxt))
+    kw = dict(gate=d["gate"], gate_act="silu", residual=d["residual"], scale=d["scale"], next_weight=d["next_weight"])
+    want, grads = reference(d, "silu", nxt, 1e-6, "rms")
+    size, osize = sizes(d, "silu", nxt, 1e-6, "rms")
+    n = count(D, rows, nxt)
+    outs = block_norm(d["x"], d["weight"], next_norm=nxt, **kw)
+    for o, w, s, t in zip(outs if nxt else [outs], want, osize, (res, dtype)):
+        check(o, w.cpu(), s.cpu(), t, n, "y or z")
+    got = block_norm_bwd(d["x"], d["dy"], d["weight"], dz=d["dz"], **kw)
+    at_once, steps = walk_of(rows, D)
+    assert steps > 1
+    cut = slice(rows // 2, rows // 2 + at_once)
+    part = {k: v[cut] if k in ("x", "gate", "residual", "dy", "dz") and v is not None else v for k, v in d.items()}
+    lost = reference(part, "silu", nxt, 1e-6, "rms")[1]
+    for name, w in grads.items():
+        extra = steps + at_once if name in ("dweight", "dscale", "dnext_weight") else 0
+        check(got[name], w.cpu(), size[name].cpu(), got[name].dtype, n + extra, name)
+        if extra:
+            with pytest.raises(AssertionError, match="times the tolerance"):
+                check(got[name], (w - lost[name]).cpu(), size[name].cpu(), got[name].dtype, n + extra, name)

@@ -473,3 +473,101 @@ def test_prompt_then_tokens():
     n = ref.roundings(64, 64, 90) + 10 * 3
     within(torch.cat(rows, 1), want[0], size[0], torch.float32, n, "o")
     within(state, want[1], size[1], torch.float32, n, "state")
+
+
+# Shapes whose kernels the ones above do not reach: with more than 32 (sequence, head) pairs fp32 goes by 128
+# columns, and with more than 128 (segment, head) pairs the state pass does too.
+MANY_HEADS = [
+    # B, T, H, Hk, K, V, lens, in segments
+    (1, 150, 40, 20, 128, 128, None, False),
+    (2, 97, 24, 8, 64, 72, None, False),
+    (1, 150, 48, 16, 72, 40, None, False),
+    (1, 200, 36, 36, 128, 72, [70, 0, 33, 90], False),
+    (1, 1100, 48, 16, 72, 72, None, True),
+    (1, 1100, 80, 80, 40, 72, None, True),
+    (1, 2600, 48, 48, 72, 24, [1500, 0, 1060], True),
+    (1, 1100, 48, 24, 136, 72, None, True),
+]
+
+
+def on_gpu64(d):
+    """The 64-bit reference's arguments, on the GPU: (q, k, v, g, h0), do without rows outside, dht."""
+    up = lambda x: d[x].cuda().double()  # noqa: E731
+    return [up(x) for x in ("q", "k", "v", "g", "h0")], up("do"), up("dht")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("shape", MANY_HEADS, ids=_id)
+def test_many_heads(shape, dtype):
+    need_gpu()
+    from gated_delta_rule_gate_amd import chunk_linear_attn, chunk_linear_attn_bwd, linear_workspace_bytes
+
+    B, T, H, Hk, K, V, lens, cut = shape
+    d = make(B, T, H, Hk, K, V, dtype, "head" if H == 40 else "token", lens, seed=70)
+    g = dev(d)
+    need = linear_workspace_bytes(g["q"], g["k"], g["v"], g["g"], slots=None if lens is None else len(lens))
+    assert (need > 0) == cut
+    end = T if lens is None else sum(lens)
+    args, do, dht = on_gpu64(d)
+    do[:, end:] = 0
+    n = ref.roundings(K, V, T) + H // Hk
+    o, ht = chunk_linear_attn(g["q"], g["k"], g["v"], g["g"], g["h0"], cu_seqlens=g["cu"], output_final_state=True)
+    got = chunk_linear_attn_bwd(g["q"], g["k"], g["v"], g["g"], g["do"], g["h0"], dht=g["dht"], cu_seqlens=g["cu"])
+    with torch.device("cuda"):
+        want = [*ref.attn(*args, cu=d["cu"]), *ref.attn_grads(*args, do, dht, cu=d["cu"])]
+        size = [*ref.attn_sizes(*args, cu=d["cu"]), *ref.grad_sizes(*args, do, dht, cu=d["cu"])]
+    for name, w, s in zip(("o", "ht", "dq", "dk", "dv", "dg", "dh0"), want, size):
+        x = dict(got, o=o, ht=ht)[name]
+        rows = name in ("o", "dq", "dk", "dv") or (name == "dg" and x.dim() == 3)
+        c = (lambda t: t[:, :end]) if rows else (lambda t: t)
+        within(c(x), c(w), c(s).cpu(), x.dtype, n, name, PARTS[dtype] if name in ("o", "dv") else 0.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("shape", [
+    # 512 and more (sequence, head, 128 columns): blocks of 128 columns, over several tokens and partial widths
+    (130, 3, 4, 2, 72, 136, None), (256, 2, 2, 1, 128, 128, None), (130, 2, 4, 4, 200, 256, None),
+    (520, 1, 1, 1, 40, 72, None), (256, 2, 2, 2, 256, 128, None), (1, 215, 4, 1, 64, 128, [i % 4 for i in range(140)]),
+    (1, 100, 16, 16, 136, 40, [0, 7, 1, 2] * 9),
+], ids=_id)
+def test_recurrent_with_many_sequences(shape, dtype):
+    need_gpu()
+    from gated_delta_rule_gate_amd import recurrent_linear_attn
+
+    B, T, H, Hk, K, V, lens = shape
+    assert (B if lens is None else len(lens)) * H * -(-V // 128) >= 512
+    d = make(B, T, H, Hk, K, V, dtype, "token", lens, seed=71)
+    g = dev(d)
+    out = torch.full((B, T, H, V), 7.0, dtype=dtype, device="cuda")
+    o, ht = recurrent_linear_attn(g["q"], g["k"], g["v"], g["g"], g["h0"], cu_seqlens=g["cu"], output_final_state=True,
+                                  out=out)
+    args = on_gpu64(d)[0]
+    with torch.device("cuda"):
+        want, size = ref.attn(*args, cu=d["cu"]), ref.attn_sizes(*args, cu=d["cu"])
+    end, n = T if lens is None else sum(lens), ref.roundings(K, V, T)
+    within(o[:, :end], want[0][:, :end], size[0][:, :end].cpu(), dtype, n, "o")
+    within(ht, want[1], size[1].cpu(), torch.float32, n, "ht")
+    assert (o[:, end:] == 7.0).all()
+    recurrent_linear_attn(g["q"], g["k"], g["v"], g["g"], g["h0"], cu_seqlens=g["cu"], final_state=g["h0"])
+    assert torch.equal(g["h0"], ht)
+
+
+@pytest.mark.parametrize("lens", [None, [1500, 0, 1, 599]], ids=["dense", "packed"])
+def test_calls_repeat_themselves(lens):
+    """The same call gives the same bits, whatever lay in the memory that it takes."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import chunk_linear_attn, chunk_linear_attn_bwd
+
+    g = dev(make(1, 2100, 8, 4, 64, 128, torch.bfloat16, "token", lens, seed=72))
+
+    def call():
+        dirty = [torch.full((n,), float("nan"), device="cuda") for n in (1 << 16, 1 << 20, 1 << 23)]
+        del dirty
+        o, ht = chunk_linear_attn(g["q"], g["k"], g["v"], g["g"], g["h0"], cu_seqlens=g["cu"], output_final_state=True)
+        b = chunk_linear_attn_bwd(g["q"], g["k"], g["v"], g["g"], g["do"], g["h0"], dht=g["dht"], cu_seqlens=g["cu"])
+        return [o, ht] + list(b.values())
+
+    first = call()
+    assert all(torch.isfinite(x).all() for x in first)
+    for _ in range(4):
+        assert all(torch.equal(a, b) for a, b in zip(first, call()))
