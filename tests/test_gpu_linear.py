@@ -486,7 +486,7 @@ MANY_HEADS = [
     (1, 1100, 48, 16, 72, 72, None, True),
     (1, 1100, 80, 80, 40, 72, None, True),
     (1, 2600, 48, 48, 72, 24, [1500, 0, 1060], True),
-    (1, 1100, 48, 24, 136, 72, None, True),
+    (1, 1100, 48, 24, 136, 72, None, "bf16"),  # fp32 has two column blocks, and pairs enough
 ]
 
 
@@ -506,7 +506,7 @@ def test_many_heads(shape, dtype):
     d = make(B, T, H, Hk, K, V, dtype, "head" if H == 40 else "token", lens, seed=70)
     g = dev(d)
     need = linear_workspace_bytes(g["q"], g["k"], g["v"], g["g"], slots=None if lens is None else len(lens))
-    assert (need > 0) == cut
+    assert (need > 0) == (dtype == torch.bfloat16 if cut == "bf16" else cut)
     end = T if lens is None else sum(lens)
     args, do, dht = on_gpu64(d)
     do[:, end:] = 0
