@@ -15,12 +15,15 @@
 // row sums are taken there, and each output is written once. A row of D values
 // is held by LPR lanes of eight values each: up to 512 values by part of a wave
 // or a wave (no barrier), longer rows by a whole workgroup of 128 to 512
-// threads, which past 4096 values take two or four vectors a lane (NV). Parameter gradients stay in registers while a workgroup walks its
-// rows; its sums go to the workspace and are added over workgroups in order.
-// Forward 1048576 x 128 with a gate, bf16: 140 us, 5.8 TB/s. Backward 262144 x
+// threads, which past 4096 values take two or four vectors a lane (NV).
+// Parameter gradients stay in registers while a workgroup walks its rows; its
+// sums go to the workspace and are added over workgroups in order.
+// Forward 1048576 x 128 with a gate, bf16: 140 us, 5.7 TB/s. Backward 262144 x
 // 128 with a gate: 84 us, 4.0 TB/s; 8192 x 4096 with gate, residual, channel
-// scale and next norm: 115 us, 4.7 TB/s. Past 8192 columns the backward spills
-// (16384: 1.05 TB/s).
+// scale and next norm: 115 us, 4.6 TB/s; 8192 x 8192: 321 us, 3.3 TB/s. Past
+// 8192 columns the backward spills 50 to 310 registers a lane (4096 x 16384: 920
+// us, 1.2 TB/s), and in fp32 with the next norm 28 past 4096 (8192 x 8192: 630
+// us, 3.4 TB/s).
 #include "kda_device.h"
 #include "linear_launch.h"
 

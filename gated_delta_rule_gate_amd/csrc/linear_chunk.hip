@@ -188,10 +188,14 @@ int linear_cols(int P, int width, bool is_bf16, int64_t pairs, int *ncb) {
 // Dense: rounds of equal segments. Packed, lengths unknown: the work shared out
 // evenly plus half a segment behind the last, or one segment if that is longer,
 // and 7 chunks for each segment's start and end, of which every slot adds about
-// 0.6; the longest slot is taken to be as long as four average ones. (32
-// heads, 10 slots, 15872 tokens, segments of 512, 1024, 1536, 1984, none: 259,
-// 236, 223, 249, 300 us; gradient, 16 heads, 7 slots, 4999 tokens, of 320, 512, 768: 192,
-// 175, 217 us.)
+// 0.6; the longest slot is taken to be as long as four average ones. How well it
+// chooses, in turn on one box: 32 heads, 10 slots, 15872 tokens, segments of 512,
+// 768, 1024, 1152 (its choice), 1280, 1408, 1536, 1792, none: 266, 250, 245, 236,
+// 215, 215, 222, 248, 306 us; the gradient of 16 heads, 7 slots, 4999 tokens, of
+// 256, 320, 384, 448, 512 (its choice), 640, 768: 202, 186, 176, 160, 168, 182,
+// 200 us. Dense, its choices are the best measured: 1 x 32768 tokens, 16 heads, of
+// 1024, 1536, 2048 (its choice), 4096: 242, 284, 220, 300 us; the gradient of 4 x
+// 2048, 32 heads, of 512, 1024 (its choice), none: 428, 353, 434 us.
 int linear_segment(int T, int slots, int H, int P, int Q, bool is_bf16, bool packed, bool dots) {
   int ncb;
   linear_cols(P, Q, is_bf16, (int64_t)slots * H, &ncb);

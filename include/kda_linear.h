@@ -27,9 +27,11 @@
  *     carry fp32 rounding, not bf16's.
  *   - Outputs must not overlap inputs, other than ht on h0 itself.
  *   - fp32 inputs above 3.38e38 (bf16's largest value) count as infinite.
- *   - A NaN or infinity in q, k, v or g makes the outputs of its (sequence,
- *     head) non-finite from the start of the 64-token chunk that holds it (the
- *     backward: throughout the sequence), and no other sequence's or head's.
+ *   - A NaN or infinity in q, k or v, or a g that is NaN or +infinity, makes
+ *     outputs of its (sequence, head) non-finite, from the start of the 64-token
+ *     chunk that holds it (the backward: throughout the sequence), and no other
+ *     sequence's or head's, but for sums over them: dq and dk of a shared q/k
+ *     head, and dg [H].
  *   - With T == 0 the per-token tensors may be NULL and every final state is
  *     its h0.
  */

@@ -58,10 +58,9 @@ kda_status kda_block_norm_fwd(const kda_norm_args *args, const void *x, const fl
 size_t kda_block_norm_bwd_workspace_bytes(const kda_norm_args *args);
 
 /*
- * Gradients of sum(dy * y) + sum(dz * z) for the forward of the same arguments
- * (has_next: the forward wrote z, dz is then required).
+ * Gradients of sum(dy * y) + sum(dz * z) for the forward of the same arguments.
  *   dy          [rows, D], res_dtype, or NULL (zero; only with dz)
- *   dz          [rows, D] or NULL
+ *   dz          [rows, D] or NULL (z was not written, or has no gradient)
  *   dx          [rows, D]
  *   dgate       [rows, D], with gate; dresidual [rows, D] (res_dtype), or NULL.
  *               dresidual may be dy itself
