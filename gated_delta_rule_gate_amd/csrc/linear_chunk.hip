@@ -189,7 +189,7 @@ int linear_cols(int P, int width, bool is_bf16, int64_t pairs, int *ncb) {
 // evenly plus half a segment behind the last, or one segment if that is longer,
 // and 7 chunks for each segment's start and end, of which every slot adds about
 // 0.6; the longest slot is taken to be as long as four average ones. How well it
-// chooses, in turn on one box: 32 heads, 10 slots, 15872 tokens, segments of 512,
+// chooses, all in one run: 32 heads, 10 slots, 15872 tokens, segments of 512,
 // 768, 1024, 1152 (its choice), 1280, 1408, 1536, 1792, none: 266, 250, 245, 236,
 // 215, 215, 222, 248, 306 us; the gradient of 16 heads, 7 slots, 4999 tokens, of
 // 256, 320, 384, 448, 512 (its choice), 640, 768: 202, 186, 176, 160, 168, 182,
