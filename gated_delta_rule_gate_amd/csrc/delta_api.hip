@@ -88,11 +88,11 @@ kda::DeltaWalk walk_base(const kda_delta_args *a, const void *q, const void *k, 
 // The backward's workspace.
 struct BwdPlan {
   size_t inv, row, state, heads;
-  size_t total() const { return 2 * inv + 2 * align_up(row) + 2 * align_up(state) + 2 * align_up(heads); }
+  size_t total() const { return inv + 2 * align_up(row) + 2 * align_up(state) + 2 * align_up(heads); }
 };
 BwdPlan bwd_plan(const kda_delta_args *a) {
   BwdPlan b;
-  b.inv = inverse_bytes(a);                                       // the inverses, and transposed
+  b.inv = inverse_bytes(a);
   b.row = 4 * (size_t)rows_of(a) * a->H * a->V;                   // u, du
   b.state = 4 * (size_t)slots_of(a) * a->H * a->K * a->V;         // states and their gradients
   b.heads = qk_heads(a) != a->H ? 4 * (size_t)rows_of(a) * a->H * a->K : 0;  // dq, dk of each value head
@@ -119,6 +119,7 @@ extern "C" kda_status kda_delta_chunk_fwd(const kda_delta_args *a, const void *q
   const hipStream_t st = (hipStream_t)stream;
   if (a->T > 0) {
     p.inv = static_cast<char *>(workspace);
+    p.fold = true;
     const hipError_t e = kda::launch_delta_prep(p, st);
     if (e != hipSuccess) return kda::report_hip(e);
   }
@@ -211,7 +212,6 @@ extern "C" kda_status kda_delta_chunk_bwd(const kda_delta_args *a, const void *q
   r.sT = dh0;
   if (a->T == 0) return kda::report_hip(dh0 ? kda::launch_delta_walk_rev(r, st) : hipSuccess);
   p.inv = take(b.inv);
-  p.inv_t = take(b.inv);
   f.rows_out = reinterpret_cast<float *>(take(b.row));
   r.rows_out = reinterpret_cast<float *>(take(b.row));
   f.states = reinterpret_cast<float *>(take(b.state));
@@ -220,7 +220,7 @@ extern "C" kda_status kda_delta_chunk_bwd(const kda_delta_args *a, const void *q
   f.v = v;
   f.s0 = h0;
   f.inv = p.inv;
-  r.inv = p.inv_t;
+  r.inv = p.inv;
   d.u = f.rows_out;
   d.du = r.rows_out;
   d.h = f.states;

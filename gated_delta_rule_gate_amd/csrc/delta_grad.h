@@ -106,14 +106,7 @@ __global__ __launch_bounds__(512) void delta_grad_kernel(DeltaGrad p) {
       fd[it] = __builtin_bit_cast(f32x4_t, tile_load16(rD, at));
     }
   };
-  auto put3 = [&](f32x4_t x, bf16_t *dst, int plane) {
-#pragma unroll
-    for (int pl = 0; pl < 3; ++pl) {
-      const bf16x4_t part = to_bf16x4(x);
-      *reinterpret_cast<bf16x4_t *>(dst + pl * plane) = part;
-      if (pl < 2) x -= to_f32x4(part);
-    }
-  };
+  auto put3 = [&](const f32x4_t &x, bf16_t *dst, int plane) { put_parts<3>(x, dst, plane); };
 
   fetch(0, 0);
   if (wave == 0) {

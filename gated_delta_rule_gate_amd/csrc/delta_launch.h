@@ -17,17 +17,18 @@ inline __host__ __device__ constexpr int delta_chunk(int tile, bool is_bf16) { r
 // after its first that starts in such a window, and no two share one).
 inline __host__ __device__ int64_t delta_slots(int64_t rows, int N, int chunk) { return N + rows / chunk; }
 
-// (I + beta M)^{-1} of every chunk as operands of the walks: 16 x 32 pieces that are
-// not above the diagonal (or, transposed, below it), three bf16 parts each, a lane's
-// eight values together.
+// (I + beta M)^{-1} of every chunk in memory: its 16 x 16 blocks on and below the
+// diagonal, row by row of blocks, fp32; lane l of a block has row l % 16, columns 4 (l /
+// 16).. of it. In LDS the walks hold 16 x 32 pieces in bf16 parts.
 inline __host__ __device__ constexpr int delta_frags(int chunk) { return chunk == 64 ? 6 : 2; }
-inline __host__ __device__ constexpr int64_t delta_inverse_bytes(int chunk) { return (int64_t)delta_frags(chunk) * 3 * 1024; }
+inline __host__ __device__ constexpr int64_t delta_inverse_bytes(int chunk) { return chunk == 64 ? 10240 : 3072; }
 
 struct DeltaPrep {
   const void *k;
   const float *g, *beta;  // g null: no decay
   const int32_t *cu;
-  char *inv, *inv_t;      // inv_t null: not wanted
+  char *inv;
+  bool fold;              // times beta's diagonal, from the right
   int B, T, H, K, N, Hk;
   bool is_bf16;
 };
@@ -38,7 +39,7 @@ struct DeltaWalk {
   const void *q, *k, *v;  // v: d_o in the gradient's walk
   const float *g, *beta;
   const int32_t *cu;
-  const char *inv;        // of every chunk (the gradient's walk: transposed)
+  const char *inv;        // of every chunk; with o: times beta's diagonal
   const float *s0;        // [N, H, K, V] or null
   float *sT;              // [N, H, K, V] or null
   void *o;                // forward, or null: nothing but the state (and what is kept)

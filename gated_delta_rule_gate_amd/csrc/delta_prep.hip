@@ -2,13 +2,18 @@
 //
 //     T = (I + A)^{-1},   A_rs = beta_r 2^{b_r - b_s} k_r . k_s  for s < r,
 //
-// which needs no state and so runs over all chunks at once. One workgroup of four
-// waves takes a chunk and a q/k head: k's rows go to LDS, the causal 16 x 16 blocks
-// of k k^T stay in accumulators for all value heads that share them. Per head the
-// decays and beta make A; the 16 x 16 diagonal blocks are inverted by forward
-// substitution, a wave each, and the blocks below, level by level, are
-// T_ij = -T_ii sum over m of A_im T_mj in fp32 matrix products. T leaves as the
-// walks' operands: three bf16 parts (24 bits) of 16 x 32 pieces.
+// which needs no state and so runs over all chunks at once. A wave takes a chunk and
+// a q/k head by itself, with no barrier: rows of k come from memory as operands of
+// the causal 16 x 16 blocks of k k^T, which stay in accumulators for all value heads
+// that share them. Per head the decays and beta make A; the diagonal blocks are
+// inverted by forward substitution, and the blocks below, level by level, come from
+// T (I + A) = I as
+//
+//     T_ij^T = -T_jj^T sum over m = j+1..i of A_mj^T T_im^T
+//
+// in fp32 matrix products whose operands are accumulators as they stand: of A_mj, of
+// T_jj, and of T_im^T. A lane of T_ij^T holds four neighbours of a row of T, which
+// leave in 16-byte stores. For the forward T takes beta as factors of its columns.
 #include "delta_chunk.h"
 
 namespace kda {
@@ -19,15 +24,15 @@ template <typename T, int PT>
 struct PrepCfg {
   static constexpr bool F32 = sizeof(T) == 4;
   static constexpr int IN = F32 ? 3 : 1, C = delta_chunk(PT, !F32), NC = C / 16, PS = PT / 32, NB = NC * (NC + 1) / 2;
-  static constexpr int LDX = PT + 16, XPL = C * LDX, LDA = C + 4;
-  static constexpr unsigned oA = 2u * IN * XPL, oT = oA + 4u * C * LDA, oTab = oT + 4u * C * LDA, total = oTab + 4u * 3 * 64;
-  static_assert(total <= 160 * 1024, "LDS");
+  static constexpr int LDD = 20;                  // rows of a 16 x 16 block in LDS, 16 bytes past 64
+  static constexpr int WAVE = NC * 16 * LDD;      // floats a wave: its diagonal blocks
+  static constexpr int TAB = 3 * 64;              // hi, lo, beta of every row
 };
 
 // x <- column c of (I + A_ii)^{-1} for one 16 x 16 block, lane (g, c) the rows 4g..4g+3,
 // -A_ii at its origin A (fp32, row stride lda). Group g's four rows are solved
 // among themselves, broadcast, and taken off the later groups' rows.
-__device__ __forceinline__ void unit_inverse16(const float *A0, int lda, float (&x)[4]) {
+__device__ __forceinline__ void unit_inverse16(const float *A0, int lda, f32x4_t &x) {
   const int lane = tid_opaque() & 63, g = lane >> 4, c = lane & 15;
   const float *A = A0 + 4 * g * lda;
   f32x4_t a[4][4];  // rows 4g + e, column quads q
@@ -62,154 +67,140 @@ __device__ __forceinline__ void unit_inverse16(const float *A0, int lda, float (
   }
 }
 
+// acc += P Q of 16 x 16 blocks, P^T and Q in accumulator layout.
+__device__ __forceinline__ f32x4_t mma_block(const f32x4_t &pt, const f32x4_t &q, f32x4_t acc) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(pt[e], q[e], acc, 0, 0, 0);
+  return acc;
+}
+
 template <typename T, int PT>
-__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaPrep p) {
+__global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaPrep p, int64_t items) {
   using F = PrepCfg<T, PT>;
-  constexpr int C = F::C, NC = F::NC, NB = F::NB, IN = F::IN, LDA = F::LDA, MB = (NB + 3) / 4;
-  using MX = RowsMove<T, 256, C, PT>;
-  extern __shared__ __align__(16) char smem[];
-  const int hk = (int)(blockIdx.x % p.Hk);
-  const int64_t slot = blockIdx.x / p.Hk;
+  constexpr int C = F::C, NC = F::NC, NB = F::NB, IN = F::IN, LDD = F::LDD;
+  __shared__ __align__(16) float sAll[4][F::WAVE + F::TAB];
+  const int wave = wave_id(), lane = threadIdx.x & 63, grp = lane >> 4, l16 = lane & 15;
+  const int64_t item = (int64_t)blockIdx.x * 4 + wave;
+  if (item >= items) return;
+  const int hk = (int)(item % p.Hk);
+  const int64_t slot = item / p.Hk;
   SegLoc sg;
   if (!locate_chunk(p, slot, C, sg)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), grp = lane >> 4, l16 = lane & 15;
   const int L = (int)(sg.hi - sg.lo), G = p.H / p.Hk;
-  bf16_t *const sK = reinterpret_cast<bf16_t *>(smem);
-  float *const sA = reinterpret_cast<float *>(smem + F::oA), *const sT = reinterpret_cast<float *>(smem + F::oT);
-  float *const tab = reinterpret_cast<float *>(smem + F::oTab);  // hi, lo, beta of every row
+  float *const sD = sAll[wave], *const tab = sD + F::WAVE;
 
-  const int64_t ldk = (int64_t)p.Hk * p.K;
-  {
-    u32x4_t buf[MX::IT];
-    MX::load(buf, reinterpret_cast<const T *>(p.k) + (sg.lo * p.Hk + hk) * p.K, ldk, L, p.K,
-             MX::lane_offset(tid, ldk, p.K), (uint32_t)(MX::RPI * ldk * sizeof(T)));
-    MX::put(buf, sK + MX::lds_offset(tid, F::LDX), F::LDX, F::XPL);
-  }
   const int64_t row0 = sg.lo * p.H + hk * G;
   float fg = 0.f, fb = 0.f;
-  auto fetch = [&](int j) {  // the last wave forms the rows' decays
+  auto fetch = [&](int j) {
     if (p.g) fg = row_scalar(p.g + row0 + j, lane, L, p.H);
     fb = row_scalar(p.beta + row0 + j, lane, L, p.H);
   };
-  if (wave == 3) fetch(0);
-  __syncthreads();
+  fetch(0);
 
-  f32x4_t gram[MB];
+  // ---- k k^T: block (i, j), row 4 grp + e of tile i, column l16 of tile j ----
+  f32x4_t gram[NB];
 #pragma unroll
-  for (int m = 0; m < MB; ++m) {
-    const int blk = 4 * m + wave;
-    gram[m] = zero4();
-    if (blk < NB) {
-      const int i = blk < 1 ? 0 : (blk < 3 ? 1 : (blk < 6 ? 2 : 3)), j = blk - i * (i + 1) / 2;
-      const bf16_t *r = sK + (16 * i + l16) * F::LDX + 8 * grp, *c = sK + (16 * j + l16) * F::LDX + 8 * grp;
+  for (int b = 0; b < NB; ++b) gram[b] = zero4();
+  {
+    const int ldk = p.Hk * p.K;
+    const T *const base = reinterpret_cast<const T *>(p.k) + (sg.lo * p.Hk + hk) * p.K;
+    const auto rs = tile_rsrc(base, (uint32_t)(((L - 1) * ldk + p.K) * (int)sizeof(T)));
+    const uint32_t off = (uint32_t)((l16 * ldk + 8 * grp) * (int)sizeof(T));
 #pragma unroll
-      for (int s = 0; s < F::PS; ++s) {
-        bf16x8_t a[IN], b[IN];
+    for (int s = 0; s < F::PS; ++s) {
+      const bool in = 32 * s + 8 * grp < p.K;
+      bf16x8_t a[NC][IN];
 #pragma unroll
-        for (int pl = 0; pl < IN; ++pl) {
-          a[pl] = row_frag(r + pl * F::XPL + 32 * s);
-          b[pl] = row_frag(c + pl * F::XPL + 32 * s);
+      for (int i = 0; i < NC; ++i) {
+        const uint32_t at = in ? off + (uint32_t)((16 * i * ldk + 32 * s) * (int)sizeof(T)) : kOffNone;
+        if constexpr (F::F32) {
+          const f32x4_t lo = __builtin_bit_cast(f32x4_t, tile_load16(rs, at)), hi = __builtin_bit_cast(f32x4_t, tile_load16(rs, at + 16));
+          split_pair<3>(lo, hi, a[i]);
+        } else {
+          a[i][0] = __builtin_bit_cast(bf16x8_t, tile_load16(rs, at));
         }
-        gram[m] = mma_parts(a, b, gram[m]);  // row 4 grp + e of block i, column l16 of block j
       }
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j <= i; ++j) gram[i * (i + 1) / 2 + j] = mma_parts(a[i], a[j], gram[i * (i + 1) / 2 + j]);
     }
   }
 
   for (int jh = 0; jh < G; ++jh) {
-    if (wave == 3) {
-      const RowDecay d = row_decay(fg);
-      tab[lane] = d.hi;
-      tab[64 + lane] = d.lo;
-      tab[128 + lane] = fb;
-      if (jh + 1 < G) fetch(jh + 1);
-    }
-    __syncthreads();
+    const RowDecay d = row_decay(fg);
+    tab[lane] = d.hi;
+    tab[64 + lane] = d.lo;
+    tab[128 + lane] = fb;
+    if (jh + 1 < G) fetch(jh + 1);
+    lds_wave_order();
+    // -A: the diagonal blocks to LDS, the others in place
+    f32x4_t A[NB];
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      const int blk = 4 * m + wave;
-      if (blk < NB) {
-        const int i = blk < 1 ? 0 : (blk < 3 ? 1 : (blk < 6 ? 2 : 3)), j = blk - i * (i + 1) / 2;
+    for (int i = 0; i < NC; ++i) {
+      const f32x4_t hr = *reinterpret_cast<const f32x4_t *>(tab + 16 * i + 4 * grp);
+      const f32x4_t lr = *reinterpret_cast<const f32x4_t *>(tab + 64 + 16 * i + 4 * grp);
+      const f32x4_t be = *reinterpret_cast<const f32x4_t *>(tab + 128 + 16 * i + 4 * grp);
+#pragma unroll
+      for (int j = 0; j <= i; ++j) {
         const float hs = tab[16 * j + l16], ls = tab[64 + 16 * j + l16];
+        f32x4_t &x = A[i * (i + 1) / 2 + j];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int r = 16 * i + 4 * grp + e;
-          const float d = fast_exp2((tab[r] - hs) + (tab[64 + r] - ls));
-          const bool keep = i != j || 4 * grp + e > l16;
-          sA[r * LDA + 16 * j + l16] = keep ? -gram[m][e] * (d * tab[128 + r]) : 0.f;
+          const float w = fast_exp2((hr[e] - hs) + (lr[e] - ls)) * be[e];
+          x[e] = i != j || 4 * grp + e > l16 ? -gram[i * (i + 1) / 2 + j][e] * w : 0.f;
+          if (i == j) sD[(16 * i + 4 * grp + e) * LDD + l16] = x[e];
         }
       }
     }
-    __syncthreads();
-    if (wave < NC) {
-      float x[4];
-      unit_inverse16(sA + 16 * wave * (LDA + 1), LDA, x);
+    lds_wave_order();
+    // T_ii, and transposed
+    f32x4_t D[NC], Tt[NB];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sT[(16 * wave + 4 * grp + e) * LDA + 16 * wave + l16] = x[e];
-    }
-    __syncthreads();
+    for (int i = 0; i < NC; ++i) unit_inverse16(sD + 16 * i * LDD, LDD, D[i]);
+    lds_wave_order();
 #pragma unroll
-    for (int d = 1; d < NC; ++d) {
-      if (wave < NC - d) {
-        const int j = wave, i = wave + d;
+    for (int i = 0; i < NC; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sD[(16 * i + 4 * grp + e) * LDD + l16] = D[i][e];
+    lds_wave_order();
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      Tt[i * (i + 1) / 2 + i] = *reinterpret_cast<const f32x4_t *>(sD + (16 * i + l16) * LDD + 4 * grp);
+#pragma unroll
+    for (int n = 1; n < NC; ++n)
+#pragma unroll
+      for (int j = 0; j + n < NC; ++j) {
+        const int i = j + n;
         f32x4_t P = zero4();
 #pragma unroll
-        for (int n = 0; n < d; ++n) {
-          const int m = j + n;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            P = __builtin_amdgcn_mfma_f32_16x16x4f32(sA[(16 * i + l16) * LDA + 16 * m + 4 * grp + e],
-                                                     sT[(16 * m + 4 * grp + e) * LDA + 16 * j + l16], P, 0, 0, 0);
-        }
-        f32x4_t R = zero4();
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          R = __builtin_amdgcn_mfma_f32_16x16x4f32(sT[(16 * i + l16) * LDA + 16 * i + 4 * grp + e], P[e], R, 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sT[(16 * i + 4 * grp + e) * LDA + 16 * j + l16] = R[e];
+        for (int m = j + 1; m <= i; ++m) P = mma_block(A[m * (m + 1) / 2 + j], Tt[i * (i + 1) / 2 + m], P);
+        Tt[i * (i + 1) / 2 + j] = mma_block(D[j], P, zero4());
       }
-      __syncthreads();
+    // out: row l16 of tile i, columns 4 grp + e of tile j
+    char *const dst = p.inv + (slot * p.H + hk * G + jh) * delta_inverse_bytes(C) + lane * 16;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      f32x4_t be{1.f, 1.f, 1.f, 1.f};
+      if (p.fold) be = *reinterpret_cast<const f32x4_t *>(tab + 128 + 16 * j + 4 * grp);
+#pragma unroll
+      for (int i = j; i < NC; ++i)
+        *reinterpret_cast<f32x4_t *>(dst + (i * (i + 1) / 2 + j) * 1024) = Tt[i * (i + 1) / 2 + j] * be;
     }
-    const int64_t at = (slot * p.H + hk * G + jh) * delta_inverse_bytes(C) + lane * 16;
-    for (int tr = 0; tr < (p.inv_t ? 2 : 1); ++tr) {
-      char *dst = (tr ? p.inv_t : p.inv) + at;
-      for (int f = wave; f < delta_frags(C); f += 4) {
-        // piece f: rows of tile i, columns of tiles 2 s and 2 s + 1
-        const int i = C == 32 ? f : (tr ? (f < 4 ? f >> 1 : f - 2) : (f < 2 ? f : 2 + ((f - 2) >> 1)));
-        const int s = C == 32 ? 0 : (tr ? (f < 4 ? f & 1 : 1) : (f < 2 ? 0 : f & 1));
-        float x[8];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int c = 2 * s + half;
-          const bool in = tr ? c >= i : c <= i;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = 16 * i + l16, k = 16 * c + 4 * grp + e;
-            x[4 * half + e] = in ? (tr ? sT[k * LDA + r] : sT[r * LDA + k]) : 0.f;
-          }
-        }
-        bf16x8_t part[3];
-        split8<3>(x, part);
-#pragma unroll
-        for (int pl = 0; pl < 3; ++pl) *reinterpret_cast<bf16x8_t *>(dst + (f * 3 + pl) * 1024) = part[pl];
-      }
-    }
+    lds_wave_order();
   }
+}
+
+int64_t prep_items(const DeltaPrep &p) {
+  return delta_slots((int64_t)p.B * p.T, p.N, delta_chunk(linear_tile(p.K), p.is_bf16)) * p.Hk;
 }
 
 template <typename T, int PT>
 hipError_t launch_prep(const DeltaPrep &p, hipStream_t st) {
-  using F = PrepCfg<T, PT>;
-  auto kern = delta_prep_kernel<T, PT>;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)F::total);
-  if (e != hipSuccess) {
-    (void)hipGetLastError();
-    return e;
-  }
-  const int64_t grid = delta_slots((int64_t)p.B * p.T, p.N, F::C) * p.Hk;
+  const int64_t items = prep_items(p), grid = (items + 3) / 4;
   if (grid == 0) return hipSuccess;
   if (grid > most_blocks(256)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), F::total, st, p);
+  hipLaunchKernelGGL((delta_prep_kernel<T, PT>), dim3((unsigned)grid), dim3(256), 0, st, p, items);
   return hipGetLastError();
 }
 
@@ -224,10 +215,14 @@ hipError_t launch_prep_width(const DeltaPrep &p, hipStream_t st) {
 
 }  // namespace
 
-// Columns of a workgroup: 128, or 64 where V has no more, and for fp32 inputs, whose
-// three parts leave no LDS for more.
+// Columns of a workgroup: 128, a wave on every SIMD beside another; 64 where V has no
+// more, for fp32 inputs, whose three parts leave no registers for more, and where 128
+// would leave half the compute units idle (a chunk of 128 x 128 then takes 3.1 us
+// instead of 4.8: 128 (sequence, head) pairs of 2048 tokens 147 us by 64, 211 us by
+// 128; with 256 pairs of 4096 tokens 497 us by 64, 403 us by 128).
 int delta_cols(const DeltaWalk &p, int *ncb) {
-  const int qt = p.V <= 64 || !p.is_bf16 ? 64 : 128;
+  const int64_t wide = (int64_t)p.N * p.H * ((p.V + 127) / 128);
+  const int qt = p.V <= 64 || !p.is_bf16 || 2 * wide <= device_cus() ? 64 : 128;
   *ncb = (p.V + qt - 1) / qt;
   return qt;
 }
@@ -238,9 +233,7 @@ bool delta_walk_fits(const DeltaWalk &p) {
   return delta_walk_blocks(p, ncb) <= most_blocks(64 * (qt / 16 + 4));
 }
 
-bool delta_prep_fits(const DeltaPrep &p) {
-  return delta_slots((int64_t)p.B * p.T, p.N, delta_chunk(linear_tile(p.K), p.is_bf16)) * p.Hk <= most_blocks(256);
-}
+bool delta_prep_fits(const DeltaPrep &p) { return (prep_items(p) + 3) / 4 <= most_blocks(256); }
 
 hipError_t launch_delta_prep(const DeltaPrep &p, hipStream_t st) {
   return p.is_bf16 ? launch_prep_width<bf16_t>(p, st) : launch_prep_width<float>(p, st);

@@ -83,8 +83,8 @@ void delta_rev_kernel(DeltaWalk p) {
     const T *const xf = reinterpret_cast<const T *>(p.q) + (sr.t0 * p.Hk + hk) * K;
     const T *const zf = reinterpret_cast<const T *>(p.k) + (sr.t0 * p.Hk + hk) * K;
     const T *const wf = reinterpret_cast<const T *>(p.v) + (sr.t0 * p.H + h) * V + col0;
-    constexpr int TIT = (F::NF * 3 * 64 + F::HT - 1) / F::HT;
-    u32x4_t fx[MX::IT], fz[MX::IT], fw[MW::IT], ft[TIT];
+    using MI = InverseMove<C>;
+    u32x4_t fx[MX::IT], fz[MX::IT], fw[MW::IT], ft[MI::IT];
     float fg = 0.f, fb = 0.f;
     constexpr int DW = 3;  // the helper that forms the decays: one with fewer blocks of the scores
     auto fetch_rows = [&](int cc) {
@@ -102,9 +102,7 @@ void delta_rev_kernel(DeltaWalk p) {
       const int64_t t = start_of(cc);
       MW::load(fw, wf + t * ldw, ldw, rows_of(cc), ncol, gw, rw);
       const int64_t slot = delta_slot(p.N, n, sr.t0, sr.t0 + t, C);
-      const auto rs = tile_rsrc(p.inv + (slot * p.H + h) * delta_inverse_bytes(C), (uint32_t)delta_inverse_bytes(C));
-#pragma unroll
-      for (int it = 0; it < TIT; ++it) ft[it] = tile_load16(rs, (uint32_t)((it * F::HT + ht) * 16));
+      MI::load(ft, p.inv + (slot * p.H + h) * delta_inverse_bytes(C), ht);
     };
     auto put_rows = [&](int cc) {
       bf16_t *s = rows_at(cc);
@@ -123,10 +121,7 @@ void delta_rev_kernel(DeltaWalk p) {
     };
     auto put_vt = [&]() {
       MW::put(fw, sW + pw, F::LDW, F::WPL);
-#pragma unroll
-      for (int it = 0; it < TIT; ++it)
-        if ((it + 1) * F::HT <= F::NF * 192 || it * F::HT + ht < F::NF * 192)
-          *reinterpret_cast<u32x4_t *>(sT + (it * F::HT + ht) * 8) = ft[it];
+      MI::template put<true>(ft, sT, hw, lane);
     };
     // transposed scores: lane has row l16 of k, four later rows of q
     auto scores = [&](int cc) {
@@ -159,22 +154,21 @@ void delta_rev_kernel(DeltaWalk p) {
             v[e] = keep ? acc[e] * (fast_exp2((hr[e] - hs) + (lr[e] - ls)) * p.scale) : 0.f;
           }
           bf16_t *dst = sP + (16 * j + l16) * F::LDP + 32 * (i >> 1) + 8 * grp + 4 * (i & 1);
-#pragma unroll
-          for (int pl = 0; pl < 3; ++pl) {
-            const bf16x4_t part = to_bf16x4(v);
-            *reinterpret_cast<bf16x4_t *>(dst + pl * F::PPL) = part;
-            if (pl < 2) v -= to_f32x4(part);
-          }
+          put_parts<3>(v, dst, F::PPL);
         }
       }
     };
 
     // the blocks of the scores beyond the triangle stay zero
     for (int i = ht; i < (int)(F::nP / 4); i += F::HT) reinterpret_cast<unsigned *>(smem + F::oP)[i] = 0u;
+    MI::clear(sT, ht);
     if (nch > 0) {
       fetch_rows(0);
       fetch_vt(0);
       put_rows(0);
+    }
+    __syncthreads();  // cleared
+    if (nch > 0) {
       put_vt();
       if (nch > 1) {
         fetch_rows(1);
@@ -217,6 +211,7 @@ void delta_rev_kernel(DeltaWalk p) {
   float *const uc = p.rows_out + (sr.t0 * p.H + h) * V + col0;
   const uint32_t gu = qin ? (uint32_t)((4 * grp * ldy + 16 * wave + l16) * 4) : kOffNone;
 
+  __syncthreads();
   __syncthreads();
   __syncthreads();
   for (int cc = 0; cc < nch; ++cc) {
@@ -271,13 +266,20 @@ void delta_rev_kernel(DeltaWalk p) {
         x[e] *= a0[e];
         x[e + 4] *= a1[e];
       }
-      split8<3>(x, wc[s]);
+      split_pair<3>(f32x4_t{x[0], x[1], x[2], x[3]}, f32x4_t{x[4], x[5], x[6], x[7]}, wc[s]);
     }
     // ---- du = T^T d0 ----
     bf16x8_t wu[KS][3];
 #pragma unroll
     for (int s = 0; s < KS; ++s) split_pair<3>(z[2 * s], z[2 * s + 1], wu[s]);
-    times_inverse<C, true>(sT, lane, wu, u);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) u[i] = zero4();
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      InverseTimes<C, true> ti;
+      ti.read(sT, lane, s);
+      ti.add(wu[s], u, s);
+    }
 #pragma unroll
     for (int s = 0; s < KS; ++s) {  // -beta 2^b du in parts
       const f32x4_t b0 = *reinterpret_cast<const f32x4_t *>(tab + 320 + 32 * s + 4 * grp);
