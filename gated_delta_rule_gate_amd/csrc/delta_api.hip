@@ -85,6 +85,28 @@ kda::DeltaWalk walk_base(const kda_delta_args *a, const void *q, const void *k, 
   return w;
 }
 
+// What the segments of a walk keep in the workspace.
+struct SegPlan {
+  int seg = 0;
+  size_t state = 0, map = 0, first = 0;
+  size_t total() const { return align_up(state) + align_up(map) + align_up(first); }
+};
+SegPlan seg_plan(const kda_delta_args *a, bool packed) {
+  SegPlan s;
+  kda::DeltaWalk w = walk_base(a, nullptr, nullptr, nullptr, nullptr, nullptr);
+  s.seg = kda::delta_segment(w, packed);
+  if (!s.seg) return s;
+  const size_t bounds = (size_t)(rows_of(a) / s.seg + 1) * a->H;
+  s.state = 4 * bounds * a->K * a->V;
+  s.map = 4 * bounds * a->K * a->K;
+  s.first = 4 * (size_t)a->N * a->H * a->K * a->V;
+  return s;
+}
+// Whether these sizes describe a dense batch, and whether a packed one (a workspace query
+// sees no cu_seqlens; N == B == 1 can be either).
+bool maybe_dense(const kda_delta_args *a) { return a->N == a->B; }
+bool maybe_packed(const kda_delta_args *a) { return a->B == 1; }
+
 // The backward's workspace.
 struct BwdPlan {
   size_t inv, row, state, heads;
@@ -102,7 +124,11 @@ BwdPlan bwd_plan(const kda_delta_args *a) {
 }  // namespace
 
 extern "C" size_t kda_delta_chunk_workspace_bytes(const kda_delta_args *a) {
-  return check_sizes(a) == KDA_OK ? inverse_bytes(a) : 0;
+  if (check_sizes(a) != KDA_OK || a->T == 0) return 0;
+  size_t n = 0;
+  if (maybe_dense(a)) n = std::max(n, seg_plan(a, false).total());
+  if (maybe_packed(a)) n = std::max(n, seg_plan(a, true).total());
+  return n + inverse_bytes(a);
 }
 
 extern "C" kda_status kda_delta_chunk_fwd(const kda_delta_args *a, const void *q, const void *k, const void *v,
@@ -112,8 +138,10 @@ extern "C" kda_status kda_delta_chunk_fwd(const kda_delta_args *a, const void *q
   if (s != KDA_OK) return s;
   kda::DeltaPrep p = prep_base(a, k, g, beta, cu);
   kda::DeltaWalk w = walk_base(a, q, k, g, beta, cu);
+  const SegPlan plan = a->T > 0 ? seg_plan(a, cu != nullptr) : SegPlan{};
+  w.seg = plan.seg;
   if (!kda::delta_prep_fits(p) || !kda::delta_walk_fits(w)) return KDA_ERR_UNSUPPORTED;
-  const size_t need = inverse_bytes(a);
+  const size_t need = inverse_bytes(a) + plan.total();
   if (need > 0 && (!workspace || ws_bytes < need)) return KDA_ERR_WORKSPACE;
   if (need > 0 && !aligned256(workspace)) return KDA_ERR_ALIGN;
   const hipStream_t st = (hipStream_t)stream;
@@ -125,6 +153,13 @@ extern "C" kda_status kda_delta_chunk_fwd(const kda_delta_args *a, const void *q
   }
   w.v = v;
   w.inv = static_cast<const char *>(workspace);
+  w.fold = true;
+  if (plan.seg) {
+    char *at = static_cast<char *>(workspace) + inverse_bytes(a);
+    w.seg_state = reinterpret_cast<float *>(at);
+    w.seg_map = reinterpret_cast<float *>(at + align_up(plan.state));
+    w.seg_first = h0 && ht == h0 ? reinterpret_cast<float *>(at + align_up(plan.state) + align_up(plan.map)) : nullptr;
+  }
   w.s0 = h0;
   w.sT = ht;
   w.o = o;

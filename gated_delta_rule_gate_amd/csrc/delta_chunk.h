@@ -13,16 +13,22 @@ __device__ __forceinline__ int64_t delta_slot(int N, int n, int64_t a, int64_t l
   return lo == a ? n : (int64_t)N + lo / chunk - 1;
 }
 
-// The chunk with workspace place `slot`: its sequence and rows; false: none.
+// Part `item` of the batch cut into parts of `part` tokens (linear_segments.h); part 0:
+// whole sequences.
 template <typename P>
-__device__ __forceinline__ bool locate_chunk(const P &p, int64_t slot, int chunk, SegLoc &s) {
+__device__ __forceinline__ bool locate_part(const P &p, int64_t item, int part, SegLoc &s) {
   LinearWalk w{};
   w.cu = p.cu;
   w.B = p.B;
   w.T = p.T;
   w.N = p.N;
-  w.seg = chunk;
-  return locate_segment(w, slot, false, s) && s.hi > s.lo;
+  w.seg = part;
+  return locate_segment(w, item, false, s);
+}
+// The chunk with workspace place `slot`: its sequence and rows; false: none.
+template <typename P>
+__device__ __forceinline__ bool locate_chunk(const P &p, int64_t slot, int chunk, SegLoc &s) {
+  return locate_part(p, slot, chunk, s) && s.hi > s.lo;
 }
 
 // A row's decays within its chunk. b is summed in fp64 and kept as an integer and a

@@ -48,13 +48,31 @@ struct DeltaWalk {
   int B, T, H, K, V, N, Hk;
   float scale;
   bool is_bf16;
+  // Long sequences on few heads: cut into segments of seg tokens (0: whole
+  // sequences) that are walked side by side. A segment maps the state that enters it
+  // affinely, S -> M S + B: a first pass walks it from zeros (B; a sequence's first from
+  // its own start) and, with no rows written, from the identity (M), and leaves both at
+  // the boundary behind it; a second chains them; then every segment is walked from its
+  // boundary.
+  int seg;
+  bool fold;              // inv is times beta's diagonal (with o it is)
+  float *seg_state;       // [boundary, H, K, V]
+  float *seg_map;         // [boundary, H, K, K]
+  float *seg_map_t;       // transposed, or null
+  float *seg_first;       // copies of s0 where sT is s0 itself, [N, H, K, V], or null
 };
 int delta_cols(const DeltaWalk &p, int *ncb);  // columns of a workgroup and column blocks
+// tokens per segment of a walk, or 0 for none
+int delta_segment(const DeltaWalk &p, bool packed);
 // Workgroups of a walk of ncb column blocks: a unit of those that read the same q/k
 // rows after another, units dealt to the eight XCDs.
 inline int64_t delta_walk_blocks(const DeltaWalk &p, int ncb) {
-  return ((int64_t)p.N * p.Hk + 7) / 8 * 8 * (p.H / p.Hk) * ncb;
+  const int64_t items = p.N + (p.seg ? ((int64_t)p.B * p.T) / p.seg : 0);
+  return (items * p.Hk + 7) / 8 * 8 * (p.H / p.Hk) * ncb;
 }
+// The states at the boundaries from the segments' own, in place: forward S += M S of the
+// boundary before, in reverse (transposed maps) of the one behind.
+hipError_t launch_delta_chain(const DeltaWalk &p, bool rev, hipStream_t st);
 bool delta_walk_fits(const DeltaWalk &p);
 hipError_t launch_delta_walk_bf16(const DeltaWalk &p, hipStream_t st);
 hipError_t launch_delta_walk_f32(const DeltaWalk &p, hipStream_t st);

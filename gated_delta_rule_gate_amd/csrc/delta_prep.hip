@@ -215,24 +215,6 @@ hipError_t launch_prep_width(const DeltaPrep &p, hipStream_t st) {
 
 }  // namespace
 
-// Columns of a workgroup: 128, a wave on every SIMD beside another; 64 where V has no
-// more, for fp32 inputs, whose three parts leave no registers for more, and where 128
-// would leave half the compute units idle (a chunk of 128 x 128 then takes 3.1 us
-// instead of 4.8: 128 (sequence, head) pairs of 2048 tokens 147 us by 64, 211 us by
-// 128; with 256 pairs of 4096 tokens 497 us by 64, 403 us by 128).
-int delta_cols(const DeltaWalk &p, int *ncb) {
-  const int64_t wide = (int64_t)p.N * p.H * ((p.V + 127) / 128);
-  const int qt = p.V <= 64 || !p.is_bf16 || 2 * wide <= device_cus() ? 64 : 128;
-  *ncb = (p.V + qt - 1) / qt;
-  return qt;
-}
-
-bool delta_walk_fits(const DeltaWalk &p) {
-  int ncb;
-  const int qt = delta_cols(p, &ncb);
-  return delta_walk_blocks(p, ncb) <= most_blocks(64 * (qt / 16 + 4));
-}
-
 bool delta_prep_fits(const DeltaPrep &p) { return (prep_items(p) + 3) / 4 <= most_blocks(256); }
 
 hipError_t launch_delta_prep(const DeltaPrep &p, hipStream_t st) {

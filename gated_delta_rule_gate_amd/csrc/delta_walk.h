@@ -24,7 +24,9 @@ namespace kda {
 
 namespace {
 
-enum DeltaMode : int { kDeltaOut = 0, kDeltaKeep = 1 };
+// With o; with u and the states kept (the gradient's); of a segment, nothing but the
+// state, or the map, left at the boundary behind it.
+enum DeltaMode : int { kDeltaOut = 0, kDeltaKeep = 1, kDeltaState = 2 };
 
 template <typename T, int PT_, int NW_, int OPL_, int MODE_>
 struct DeltaCfg {
@@ -55,26 +57,31 @@ void delta_walk_kernel(DeltaWalk p) {
   using MX = RowsMove<T, F::HT, C, PT>;
   extern __shared__ __align__(16) char smem[];
 
-  // workgroups that read the same q/k rows go to one XCD, next to each other
-  const int ncb = (p.V + QT - 1) / QT;
+  // workgroups that read the same q/k rows go to one XCD, next to each other; whole
+  // segments come before the sequences' first, which may be short
+  const int nvb = (p.V + QT - 1) / QT, ncb = nvb + (MODE == kDeltaState ? (p.K + QT - 1) / QT : 0);
   const int G = p.H / p.Hk, U = G * ncb;
   const int xcd = blockIdx.x & 7, sl = blockIdx.x >> 3;
   const int64_t unit = (int64_t)(sl / U) * 8 + xcd;
   const int member = sl % U;
-  const int64_t n64 = unit / p.Hk;
-  if (n64 >= p.N) return;
-  const int n = (int)n64;
-  const int hk = (int)(unit % p.Hk), h = hk * G + member / ncb, cb = member % ncb;
-  const SlotRange sr = slot_range(p.cu, n, p.T);
+  const int64_t n_items = p.N + (p.seg ? ((int64_t)p.B * p.T) / p.seg : 0);
+  const int64_t item = n_items - 1 - unit / p.Hk;
+  const int hk = (int)(unit % p.Hk), h = hk * G + member / ncb, cbk = member % ncb;
+  SegLoc sg;
+  if (item < 0 || !locate_part(p, item, p.seg, sg)) return;
+  if (MODE == kDeltaState && sg.out < 0) return;  // nothing follows the last segment
+  const bool map = MODE == kDeltaState && cbk >= nvb;  // columns of M, not of B
+  if (map && sg.in < 0) return;                   // a first segment starts from its own state
+  const int cb = map ? cbk - nvb : cbk, n = sg.n, len = (int)(sg.hi - sg.lo);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   const int grp = lane >> 4, l16 = lane & 15;
-  const int K = p.K, V = p.V, col0 = cb * QT, ncol = min(QT, V - col0);
+  const int K = p.K, V = map ? p.K : p.V, col0 = cb * QT, ncol = min(QT, V - col0);  // V: the state's columns
   const int64_t sbase = ((int64_t)n * p.H + h) * K * V;
 
   constexpr int SZ = sizeof(T);
-  const int nch = (sr.len + C - 1) / C;
-  auto rows_of = [&](int cc) { return min(C, sr.len - cc * C); };
+  const int nch = (len + C - 1) / C;
+  auto rows_of = [&](int cc) { return min(C, len - cc * C); };
   auto rows_at = [&](int cc) { return reinterpret_cast<bf16_t *>(smem + (F::NBUF == 2 && (cc & 1) ? F::rows : 0u)); };
   auto inverse_at = [&](int cc) { return reinterpret_cast<bf16_t *>(smem + F::oT + ((cc & 1) ? F::nT : 0u)); };
   auto scores_at = [&](int cc) { return reinterpret_cast<bf16_t *>(smem + F::oP + ((cc & 1) ? F::nP : 0u)); };
@@ -89,9 +96,9 @@ void delta_walk_kernel(DeltaWalk p) {
     const uint32_t rx = (uint32_t)(MX::RPI * ldx * SZ);
     const int px = MX::lds_offset(ht, F::LDX);
     const int ax = l16 * F::LDX + 8 * grp;  // a row of q or k as an operand
-    const T *xf = reinterpret_cast<const T *>(p.q) + (sr.t0 * p.Hk + hk) * K;
-    const T *zf = reinterpret_cast<const T *>(p.k) + (sr.t0 * p.Hk + hk) * K;
-    const float *gf = p.g + sr.t0 * p.H + h, *bf = p.beta + sr.t0 * p.H + h;
+    const T *xf = reinterpret_cast<const T *>(p.q) + (sg.lo * p.Hk + hk) * K;
+    const T *zf = reinterpret_cast<const T *>(p.k) + (sg.lo * p.Hk + hk) * K;
+    const float *gf = p.g + sg.lo * p.H + h, *bf = p.beta + sg.lo * p.H + h;
     using MI = InverseMove<C>;
     u32x4_t fx[OUT ? MX::IT : 1], fz[MX::IT], ft[MI::IT];
     float fg = 0.f, fb = 0.f;
@@ -108,7 +115,7 @@ void delta_walk_kernel(DeltaWalk p) {
       zf += (int64_t)C * ldx;
       gf += (int64_t)C * p.H;
       bf += (int64_t)C * p.H;
-      const int64_t slot = delta_slot(p.N, n, sr.t0, sr.t0 + (int64_t)cc * C, C);
+      const int64_t slot = delta_slot(p.N, n, sg.a, sg.lo + (int64_t)cc * C, C);
       MI::load(ft, p.inv + (slot * p.H + h) * delta_inverse_bytes(C), ht);
     };
     auto put = [&](int cc) {
@@ -122,8 +129,9 @@ void delta_walk_kernel(DeltaWalk p) {
         t[64 + lane] = d.lo;
         t[128 + lane] = d.from * p.scale;
         t[192 + lane] = d.rest;
-        t[256 + lane] = OUT ? d.from : fb * d.from;
-        if constexpr (!OUT) t[320 + lane] = fb;
+        const float be = OUT || p.fold ? 1.f : fb;
+        t[256 + lane] = be * d.from;
+        if constexpr (!OUT) t[320 + lane] = be;
         if (lane == 0) t[384] = d.all;
       }
       MI::template put<false>(ft, inverse_at(cc), hw, lane);
@@ -192,14 +200,29 @@ void delta_walk_kernel(DeltaWalk p) {
 
   // ---- the state at the start: channels state_channel(t, grp) + e of its column ----
   f32x4_t S[F::NT];
-  load_state<F::NT>(p.s0 ? p.s0 + sbase : nullptr, K, V, grp, q, S);
+  {
+    // over a boundary, or the sequence's own start: h0 or its copy, made by the state
+    // pass where the final state goes over it
+    const float *src = sg.in >= 0 ? p.seg_state + ((int64_t)sg.in * p.H + h) * K * V
+                       : MODE != kDeltaState && p.seg_first && sg.out >= 0 ? p.seg_first + sbase
+                       : p.s0 ? p.s0 + sbase : nullptr;
+    if (MODE == kDeltaState && sg.in >= 0) src = nullptr;  // its own change only
+    load_state<F::NT>(src, K, V, grp, q, S);
+    if (map) {
+#pragma unroll
+      for (int t = 0; t < F::NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[t][e] = state_channel(t, grp) + e == q ? 1.f : 0.f;
+    }
+    if (MODE == kDeltaState && sg.in < 0 && p.seg_first) store_state<F::NT>(p.seg_first + sbase, K, V, grp, q, S);
+  }
 
   const int ax = l16 * F::LDX + 8 * grp;  // a row of q or k as an operand
   const int tz = (4 * grp + (l16 >> 2)) * F::LDX + 8 * (l16 & 3);
-  const int ldv = p.H * V;
-  const int64_t vrow = (sr.t0 * p.H + h) * V + col0;
+  const int ldv = p.H * p.V;
+  const int64_t vrow = map ? 0 : (sg.lo * p.H + h) * V + col0;
   const T *vc = reinterpret_cast<const T *>(p.v) + vrow;
-  const uint32_t gv = qin ? (uint32_t)((4 * grp * ldv + wcol + l16) * SZ) : kOffNone;
+  const uint32_t gv = qin && !map ? (uint32_t)((4 * grp * ldv + wcol + l16) * SZ) : kOffNone;
   T *yc = reinterpret_cast<T *>(p.o) + vrow;
   const uint32_t gy = wcol + 4 * grp < ncol ? (uint32_t)((l16 * ldv + wcol + 4 * grp) * SZ) : kOffNone;
   float *uc = MODE == kDeltaKeep ? p.rows_out + vrow : nullptr;
@@ -250,7 +273,7 @@ void delta_walk_kernel(DeltaWalk p) {
     const float *const tab = tab_at(cc);
 
     if constexpr (MODE == kDeltaKeep) {  // the state at the chunk's start
-      const int64_t slot = delta_slot(p.N, n, sr.t0, sr.t0 + (int64_t)cc * C, C);
+      const int64_t slot = delta_slot(p.N, n, sg.a, sg.lo + (int64_t)cc * C, C);
       store_state<F::NT>(p.states + (slot * p.H + h) * K * V, K, V, grp, q, S);
     }
 
@@ -389,7 +412,18 @@ void delta_walk_kernel(DeltaWalk p) {
     store(nch - 1);
   }
 
-  if (p.sT && !(nch == 0 && p.sT == p.s0)) store_state<F::NT>(p.sT + sbase, K, V, grp, q, S);
+  if constexpr (MODE == kDeltaState) {
+    const int64_t at = (int64_t)sg.out * p.H + h;
+    store_state<F::NT>((map ? p.seg_map : p.seg_state) + at * K * V, K, V, grp, q, S);
+    if (map && p.seg_map_t && qin) {
+#pragma unroll
+      for (int t = 0; t < F::NT; ++t)
+        if (state_channel(t, grp) < K)
+          *reinterpret_cast<f32x4_t *>(p.seg_map_t + at * K * K + (int64_t)q * K + state_channel(t, grp)) = S[t];
+    }
+  } else if (sg.out < 0) {
+    if (p.sT && !(nch == 0 && p.sT == p.s0)) store_state<F::NT>(p.sT + sbase, K, V, grp, q, S);
+  }
 }
 
 template <typename T, int PT, int NW, int OPL, int MODE>
@@ -402,7 +436,7 @@ hipError_t launch_delta_one(const DeltaWalk &p, hipStream_t st) {
     (void)hipGetLastError();  // do not leave the error for the next launch to report
     return e;
   }
-  const int ncb = (p.V + F::QT - 1) / F::QT;
+  const int ncb = (p.V + F::QT - 1) / F::QT + (MODE == kDeltaState ? (p.K + F::QT - 1) / F::QT : 0);
   const int64_t grid = delta_walk_blocks(p, ncb);
   if (grid == 0) return hipSuccess;
   if (grid > most_blocks(F::THREADS)) return hipErrorInvalidValue;
@@ -412,6 +446,11 @@ hipError_t launch_delta_one(const DeltaWalk &p, hipStream_t st) {
 
 template <typename T, int PT, int NW, int OPL>
 hipError_t launch_delta_mode(const DeltaWalk &p, hipStream_t st) {
+  if (p.seg) {
+    hipError_t e = launch_delta_one<T, PT, NW, 1, kDeltaState>(p, st);
+    if (e == hipSuccess) e = launch_delta_chain(p, false, st);
+    if (e != hipSuccess) return e;
+  }
   return p.o ? launch_delta_one<T, PT, NW, OPL, kDeltaOut>(p, st) : launch_delta_one<T, PT, NW, OPL, kDeltaKeep>(p, st);
 }
 

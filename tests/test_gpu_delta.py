@@ -115,6 +115,32 @@ def test_forward(shape, dtype, decay):
                 assert torch.equal(ht[i].cpu(), d["h0"][i])
 
 
+LONG = [  # cut into segments: few heads, several times as many chunks
+    (1, 1500, 2, 2, 64, 64, None),
+    (2, 1090, 2, 1, 40, 136, None),
+    (1, 1700, 2, 1, 128, 136, [3, 1100, 0, 520, 60]),
+    (1, 1300, 2, 1, 256, 72, None),
+    (1, 2100, 1, 1, 128, 128, [64, 1984, 52]),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("shape", LONG, ids=_id)
+def test_long_forward(shape, dtype):
+    need_gpu()
+    from gated_delta_rule_gate_amd import chunk_gated_delta
+
+    B, T, H, Hk, K, V, lens = shape
+    # weak decays: a segment's map matters to the next
+    d = make(B, T, H, Hk, K, V, dtype, lens, seed=80, strength=0.01)
+    out = torch.full((B, T, H, V), 7.0, dtype=dtype, device="cuda")
+    o, ht, inside = check_forward(d, chunk_gated_delta, out)
+    assert (o[:, ~inside] == 7.0).all()
+    g = dev(d)  # in place
+    o2, h2 = on(g, chunk_gated_delta, final_state=g["h0"])
+    assert torch.equal(o2[:, inside], o[:, inside]) and torch.equal(h2, ht)
+
+
 def check_backward(d, scale=None):
     from gated_delta_rule_gate_amd import chunk_gated_delta_bwd
 
