@@ -88,24 +88,35 @@ kda::DeltaWalk walk_base(const kda_delta_args *a, const void *q, const void *k, 
 // What the segments of a walk keep in the workspace.
 struct SegPlan {
   int seg = 0;
-  size_t state = 0, map = 0, first = 0;
-  size_t total() const { return align_up(state) + align_up(map) + align_up(first); }
+  size_t state = 0, map = 0, first = 0, bound = 0, zero = 0;
+  size_t total() const { return align_up(state) + align_up(map) + align_up(first) + align_up(bound) + align_up(zero); }
 };
-SegPlan seg_plan(const kda_delta_args *a, bool packed) {
+SegPlan seg_plan(const kda_delta_args *a, bool packed, bool gated) {
   SegPlan s;
   kda::DeltaWalk w = walk_base(a, nullptr, nullptr, nullptr, nullptr, nullptr);
-  s.seg = kda::delta_segment(w, packed);
+  s.seg = kda::delta_segment(w, packed, gated);
   if (!s.seg) return s;
   const size_t bounds = (size_t)(rows_of(a) / s.seg + 1) * a->H;
   s.state = 4 * bounds * a->K * a->V;
   s.map = 4 * bounds * a->K * a->K;
   s.first = 4 * (size_t)a->N * a->H * a->K * a->V;
+  s.bound = 4 * (size_t)slots_of(a) * a->H;
+  s.zero = 4 * bounds;
   return s;
 }
 // Whether these sizes describe a dense batch, and whether a packed one (a workspace query
 // sees no cu_seqlens; N == B == 1 can be either).
 bool maybe_dense(const kda_delta_args *a) { return a->N == a->B; }
 bool maybe_packed(const kda_delta_args *a) { return a->B == 1; }
+// What segments may need for these sizes, with g or without.
+size_t most_segments(const kda_delta_args *a) {
+  size_t n = 0;
+  for (int gated = 0; gated < 2; ++gated) {
+    if (maybe_dense(a)) n = std::max(n, seg_plan(a, false, gated).total());
+    if (maybe_packed(a)) n = std::max(n, seg_plan(a, true, gated).total());
+  }
+  return n;
+}
 
 // The backward's workspace.
 struct BwdPlan {
@@ -125,10 +136,7 @@ BwdPlan bwd_plan(const kda_delta_args *a) {
 
 extern "C" size_t kda_delta_chunk_workspace_bytes(const kda_delta_args *a) {
   if (check_sizes(a) != KDA_OK || a->T == 0) return 0;
-  size_t n = 0;
-  if (maybe_dense(a)) n = std::max(n, seg_plan(a, false).total());
-  if (maybe_packed(a)) n = std::max(n, seg_plan(a, true).total());
-  return n + inverse_bytes(a);
+  return most_segments(a) + inverse_bytes(a);
 }
 
 extern "C" kda_status kda_delta_chunk_fwd(const kda_delta_args *a, const void *q, const void *k, const void *v,
@@ -138,13 +146,25 @@ extern "C" kda_status kda_delta_chunk_fwd(const kda_delta_args *a, const void *q
   if (s != KDA_OK) return s;
   kda::DeltaPrep p = prep_base(a, k, g, beta, cu);
   kda::DeltaWalk w = walk_base(a, q, k, g, beta, cu);
-  const SegPlan plan = a->T > 0 ? seg_plan(a, cu != nullptr) : SegPlan{};
+  const SegPlan plan = a->T > 0 ? seg_plan(a, cu != nullptr, g != nullptr) : SegPlan{};
   w.seg = plan.seg;
   if (!kda::delta_prep_fits(p) || !kda::delta_walk_fits(w)) return KDA_ERR_UNSUPPORTED;
   const size_t need = inverse_bytes(a) + plan.total();
   if (need > 0 && (!workspace || ws_bytes < need)) return KDA_ERR_WORKSPACE;
   if (need > 0 && !aligned256(workspace)) return KDA_ERR_ALIGN;
   const hipStream_t st = (hipStream_t)stream;
+  char *at = static_cast<char *>(workspace) + inverse_bytes(a);
+  if (plan.seg) {
+    w.seg_state = reinterpret_cast<float *>(at);
+    at += align_up(plan.state);
+    w.seg_map = reinterpret_cast<float *>(at);
+    at += align_up(plan.map);
+    w.seg_first = h0 && ht == h0 ? reinterpret_cast<float *>(at) : nullptr;
+    at += align_up(plan.first);
+    p.bound = reinterpret_cast<float *>(at);
+    w.bound = p.bound;
+    w.seg_zero = reinterpret_cast<int *>(at + align_up(plan.bound));
+  }
   if (a->T > 0) {
     p.inv = static_cast<char *>(workspace);
     p.fold = true;
@@ -154,12 +174,6 @@ extern "C" kda_status kda_delta_chunk_fwd(const kda_delta_args *a, const void *q
   w.v = v;
   w.inv = static_cast<const char *>(workspace);
   w.fold = true;
-  if (plan.seg) {
-    char *at = static_cast<char *>(workspace) + inverse_bytes(a);
-    w.seg_state = reinterpret_cast<float *>(at);
-    w.seg_map = reinterpret_cast<float *>(at + align_up(plan.state));
-    w.seg_first = h0 && ht == h0 ? reinterpret_cast<float *>(at + align_up(plan.state) + align_up(plan.map)) : nullptr;
-  }
   w.s0 = h0;
   w.sT = ht;
   w.o = o;

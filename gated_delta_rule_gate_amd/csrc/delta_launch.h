@@ -28,7 +28,8 @@ struct DeltaPrep {
   const float *g, *beta;  // g null: no decay
   const int32_t *cu;
   char *inv;
-  bool fold;              // times beta's diagonal, from the right
+  float *bound;           // [slot, H] or null: log2 of what a chunk's map enlarges a state by, at most
+  bool fold;              // inv times beta's diagonal, from the right
   int B, T, H, K, N, Hk;
   bool is_bf16;
 };
@@ -56,14 +57,16 @@ struct DeltaWalk {
   // boundary.
   int seg;
   bool fold;              // inv is times beta's diagonal (with o it is)
+  const float *bound;     // of every chunk (delta_prep.hip)
   float *seg_state;       // [boundary, H, K, V]
   float *seg_map;         // [boundary, H, K, K]
   float *seg_map_t;       // transposed, or null
+  int *seg_zero;          // [boundary, H]: whether the map is zero, and not written
   float *seg_first;       // copies of s0 where sT is s0 itself, [N, H, K, V], or null
 };
 int delta_cols(const DeltaWalk &p, int *ncb);  // columns of a workgroup and column blocks
-// tokens per segment of a walk, or 0 for none
-int delta_segment(const DeltaWalk &p, bool packed);
+// tokens per segment of a walk, or 0 for none; gated: with decays (p.g is not looked at)
+int delta_segment(const DeltaWalk &p, bool packed, bool gated);
 // Workgroups of a walk of ncb column blocks: a unit of those that read the same q/k
 // rows after another, units dealt to the eight XCDs.
 inline int64_t delta_walk_blocks(const DeltaWalk &p, int ncb) {

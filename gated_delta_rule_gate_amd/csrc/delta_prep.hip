@@ -177,6 +177,21 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaPrep p, int64_t
         for (int m = j + 1; m <= i; ++m) P = mma_block(A[m * (m + 1) / 2 + j], Tt[i * (i + 1) / 2 + m], P);
         Tt[i * (i + 1) / 2 + j] = mma_block(D[j], P, zero4());
       }
+    if (p.bound) {
+      // a step I - beta k k^T enlarges by |1 - beta |k|^2| if that is above one: by nothing
+      // for rows of norm one; |k|^2 lies on the diagonals of k k^T
+      float grow = 0.f;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const f32x4_t &x = gram[i * (i + 1) / 2 + i];
+        const float kk = (l16 & 2) ? ((l16 & 1) ? x[3] : x[2]) : ((l16 & 1) ? x[1] : x[0]);
+        const float f = fabsf(1.f - tab[128 + 16 * i + l16] * kk);
+        grow += grp == (l16 >> 2) && !(f <= 1.f) ? fast_log2(f) : 0.f;
+      }
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) grow += __shfl_xor(grow, off);
+      if (lane == 0) p.bound[slot * p.H + hk * G + jh] = tab[63] + tab[127] + grow;
+    }
     // out: row l16 of tile i, columns 4 grp + e of tile j
     char *const dst = p.inv + (slot * p.H + hk * G + jh) * delta_inverse_bytes(C) + lane * 16;
 #pragma unroll

@@ -67,14 +67,23 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaWalk p, bool rev)
   fetch_state(j);
   // the map of the segment between boundaries j and j + d: left behind it, at the later one
   auto map_to = [&](int64_t to) { return rev ? to + 1 : to; };
-  if (AHEAD) fetch_map(map_to(j + d));
+  auto is_zero = [&](int64_t to) { return p.seg_zero[map_to(to) * p.H + h] != 0; };
+  bool zero = is_zero(j + d);
+  if (AHEAD && !zero) fetch_map(map_to(j + d));
   hand_over(0);
   for (int64_t i = 1; i < nb; ++i) {
     j += d;
     const int buf = (int)(i - 1) & 1;
     fetch_state(j);
-    if (!AHEAD) fetch_map(map_to(j));
+    if (!AHEAD && !zero) fetch_map(map_to(j));
     __syncthreads();
+    const bool next_zero = i + 1 < nb && is_zero(j + d);
+    if (zero) {  // the segment's own state is all there is
+      if (AHEAD && i + 1 < nb && !next_zero) fetch_map(map_to(j + d));
+      zero = next_zero;
+      hand_over(buf ^ 1);
+      continue;
+    }
     bf16x8_t b[PS][3];
 #pragma unroll
     for (int s = 0; s < PS; ++s)
@@ -88,7 +97,8 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaWalk p, bool rev)
         split_pair<3>(m[x][s][0], m[x][s][1], a);
         own[x] = mma_parts(a, b[s], own[x]);
       }
-    if (AHEAD && i + 1 < nb) fetch_map(map_to(j + d));
+    if (AHEAD && i + 1 < nb && !next_zero) fetch_map(map_to(j + d));
+    zero = next_zero;
     hand_over(buf ^ 1);
     const auto rs = tile_rsrc(state_at(j), (uint32_t)(K * V * 4));
 #pragma unroll
@@ -141,10 +151,15 @@ bool delta_walk_fits(const DeltaWalk &p) {
 // Costs in microseconds a chunk and workgroup as measured for bf16, 128 x 128, by 128 or 64
 // columns: 6.3 or 3.9 (4.8 or 3.1 alone on the device) with o, 0.8 of that in the state
 // pass, whose segments (all but a sequence's last) walk V and, but for the first, K
-// columns; two more launches and a boundary's step of the chain 2.5 us.
-int delta_segment(const DeltaWalk &p, bool packed) {
+// columns; two chunks for a segment's start and end; two more launches and a boundary's step of the chain 2.5 us. With decays most
+// maps are zero and not walked (delta_walk.h): an eighth is counted. How it chooses,
+// walks and chain together: 1 x 32768 tokens, 16 heads: 17 segments, 550 us (none: 1560);
+// 15872 tokens in 10 slots, 32 heads, segments of 12, 16, 20 (its choice), 24, 28, 32, 40,
+// 48 chunks, none: 578, 511, 472, 519, 562, 451, 498, 545, 497 us (steps of the slots'
+// own lengths); fp32, 2 x 1000 tokens, 8 heads: 4 segments, 65 us (none: 84).
+int delta_segment(const DeltaWalk &p, bool packed, bool gated) {
   const int C = delta_chunk(linear_tile(p.K), p.is_bf16);
-  const double room = device_cus();
+  const double room = device_cus(), maps = gated ? 0.12 : 1.0;
   const int64_t chunks = ((int64_t)p.T + C - 1) / C;  // of a sequence; packed: of the batch
   if (p.N < 1 || chunks < 8) return 0;
   double best = 0.0;
@@ -159,27 +174,34 @@ int delta_segment(const DeltaWalk &p, bool packed) {
     const double busy = qt == 128 ? 6.3 : 3.9, alone = qt == 128 ? 4.8 : 3.1;
     auto pass = [&](double wgs, double length, double rate) {  // wgs workgroups of `length` chunks
       const double rounds = std::max(1.0, std::ceil(wgs / room - 0.02));
-      return rounds * length * rate * (wgs > 0.6 * room ? busy : alone);
+      return rounds * (length + (s > 1 ? 2.0 : 0.0)) * rate * (wgs > 0.6 * room ? busy : alone);
     };
     double cost;
     if (!packed) {
       cost = pass((double)p.N * p.H * s * ncb, (double)len, 1.0);
       if (s > 1)
-        cost += pass((double)p.N * p.H * ((s - 1) * ncb + (s - 2) * kcb), (double)len, 0.8) + 2.5 * (double)(s + 3);
+        cost += pass((double)p.N * p.H * ((s - 1) * ncb + (s - 2) * kcb * maps), (double)len, 0.8) + 2.5 * (double)(s + 3);
     } else {
-      // lengths unknown: the longest slot is taken to be as long as three average ones
-      const double longest = std::min((double)chunks, std::max(1.0, 3.0 * (double)chunks / p.N));
-      const double share = (double)chunks * p.H * ncb / room;
+      // lengths unknown: spread as by random cuts (exponentially), the longest slot 3.2
+      // average ones. Of a slot's chunks, segments that end inside it hold the sum over
+      // i >= 1 of len P(longer than i len); the state pass walks V columns of those and K
+      // columns of all of them but the first. Work is shared out evenly, plus half a
+      // segment behind the last.
+      const double mean = (double)chunks / p.N, l = (double)len, x = std::exp(-l / mean);
+      const double share = (double)chunks * p.H * ncb / room, longest = std::min((double)chunks, 3.2 * mean);
       if (s == 1) {
         cost = std::max(longest, share + 0.5 * longest) * busy;
       } else {
-        const double l = (double)len, parts = std::max(0.0, longest / l - 1.0);
-        cost = std::max(l, share + 0.5 * l) * busy +
-               (parts > 0 ? std::max(l, (double)chunks * p.H * (ncb + kcb) * 0.6 / room + 0.5 * l) * 0.8 * busy + 2.5 * (parts + 3) : 0);
+        const double cut = l * x / (1.0 - x) / mean;
+        const double start = 1.0 + 2.0 / l;
+        cost = std::max(l, share * start + 0.5 * l) * busy +
+               std::max(l, share * cut * (1.0 + x * maps * kcb / ncb) * start + 0.5 * l) * 0.8 * busy +
+               2.5 * (std::max(0.0, longest / l - 1.0) + 3);
       }
     }
     if (s == 1 || cost < best) {
-      best = s == 1 ? 0.95 * cost : cost;
+      // (packed, cutting also bounds what a longer slot than supposed costs)
+      best = s == 1 ? (packed ? 1.05 : 0.95) * cost : cost;
       take = s;
     }
   }

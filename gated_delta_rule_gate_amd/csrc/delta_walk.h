@@ -57,22 +57,37 @@ void delta_walk_kernel(DeltaWalk p) {
   using MX = RowsMove<T, F::HT, C, PT>;
   extern __shared__ __align__(16) char smem[];
 
-  // workgroups that read the same q/k rows go to one XCD, next to each other; whole
-  // segments come before the sequences' first, which may be short
-  const int nvb = (p.V + QT - 1) / QT, ncb = nvb + (MODE == kDeltaState ? (p.K + QT - 1) / QT : 0);
-  const int G = p.H / p.Hk, U = G * ncb;
-  const int xcd = blockIdx.x & 7, sl = blockIdx.x >> 3;
-  const int64_t unit = (int64_t)(sl / U) * 8 + xcd;
-  const int member = sl % U;
+  // Workgroups that read the same q/k rows go to one XCD, next to each other; whole
+  // segments come before the sequences' first, which may be short. Maps come before all
+  // states, a head's dealt over the XCDs: most are not walked and end at once, while those
+  // that are would else start behind a round of states, or on one XCD.
+  const int G = p.H / p.Hk, nvb = (p.V + QT - 1) / QT;
   const int64_t n_items = p.N + (p.seg ? ((int64_t)p.B * p.T) / p.seg : 0);
+  const int64_t maps = MODE == kDeltaState ? (n_items * p.Hk + 7) / 8 * 8 * G * ((p.K + QT - 1) / QT) : 0;  // workgroups
+  const bool map = MODE == kDeltaState && blockIdx.x < maps;  // columns of M, not of B
+  const int64_t block = map ? blockIdx.x : blockIdx.x - maps;
+  const int ncb = map ? (p.K + QT - 1) / QT : nvb, U = G * ncb;
+  const int64_t unit = (block >> 3) / U * 8 + (block & 7);
+  const int member = (int)((block >> 3) % U);
   const int64_t item = n_items - 1 - unit / p.Hk;
-  const int hk = (int)(unit % p.Hk), h = hk * G + member / ncb, cbk = member % ncb;
+  const int hk = (int)((map ? unit + item : unit) % p.Hk), h = hk * G + member / ncb, cb = member % ncb;
   SegLoc sg;
   if (item < 0 || !locate_part(p, item, p.seg, sg)) return;
   if (MODE == kDeltaState && sg.out < 0) return;  // nothing follows the last segment
-  const bool map = MODE == kDeltaState && cbk >= nvb;  // columns of M, not of B
   if (map && sg.in < 0) return;                   // a first segment starts from its own state
-  const int cb = map ? cbk - nvb : cbk, n = sg.n, len = (int)(sg.hi - sg.lo);
+  const int n = sg.n, len = (int)(sg.hi - sg.lo);
+  if (map) {
+    // A map whose decays leave nothing (under 2^-160, the chunks' bounds summed) is zero:
+    // most heads of a gated model over a few thousand tokens.
+    float b = 0.f;
+    for (int c = threadIdx.x & 63; c < len / C; c += 64)
+      b += p.bound[delta_slot(p.N, n, sg.a, sg.lo + (int64_t)c * C, C) * p.H + h];
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) b += __shfl_xor(b, off);
+    const bool zero = b <= -160.f;
+    if (cb == 0 && threadIdx.x == 0) p.seg_zero[(int64_t)sg.out * p.H + h] = zero;
+    if (zero) return;
+  }
 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   const int grp = lane >> 4, l16 = lane & 15;
