@@ -23,15 +23,14 @@ struct DeltaRevCfg {
   static constexpr int IN = F32 ? 3 : 1, C = delta_chunk(PT, !F32);
   static constexpr int NC = C / 16, KS = C / 32, PS = PT / 32, NT = PT / 16, QT = 16 * NW, NF = delta_frags(C);
   static constexpr int HELPERS = 4, THREADS = 64 * (NW + HELPERS), HT = 64 * HELPERS;
-  static constexpr int LDX = PT + 16, LDW = QT + 16, LDP = C + 16;
-  static constexpr int XPL = C * LDX, WPL = C * LDW, PPL = C * LDP;
+  static constexpr int LDX = PT + 16, XPL = C * LDX;
   static constexpr unsigned nX = 2u * IN * XPL, rows = 2 * nX;  // q and k
-  static constexpr unsigned nW = 2u * IN * WPL, nT = NF * 3 * 1024u, nP = 2u * 3 * PPL;
-  static constexpr unsigned tab = 4u * (6 * 64 + 4);  // hi, lo, a scale, c, beta, beta a; the chunk's decay
-  // two chunks' q and k rows where they fit; d_o, the inverse and the scores are used
-  // in the first period only and replaced in the second
-  static constexpr int NBUF = 2 * rows + nW + nT + nP + 2 * tab <= 160 * 1024 ? 2 : 1;
-  static constexpr unsigned oW = NBUF * rows, oT = oW + nW, oP = oT + nT, oTab = oP + nP, total = oTab + 2 * tab;
+  static constexpr unsigned nT = InverseMove<C>::bytes, nP = NF * 3 * 1024u;  // the inverse and the scores, as pieces
+  static constexpr unsigned tab = 4u * (5 * 64 + 4);  // hi, lo, a scale, c, beta a; the chunk's decay
+  static constexpr unsigned oB = 2 * (nT + nP + tab);
+  // two chunks of everything; one chunk's q and k rows where two do not fit
+  static constexpr int NBUF = 2 * rows + oB <= 160 * 1024 ? 2 : 1;
+  static constexpr unsigned oT = NBUF * rows, oP = oT + 2 * nT, oTab = oP + 2 * nP, total = oTab + 2 * tab;
   static_assert(total <= 160 * 1024, "LDS");
 };
 
@@ -41,7 +40,6 @@ void delta_rev_kernel(DeltaWalk p) {
   using F = DeltaRevCfg<T, PT, NW>;
   constexpr int C = F::C, NC = F::NC, KS = F::KS, IN = F::IN, QT = F::QT, NB = NC * (NC + 1) / 2;
   using MX = RowsMove<T, F::HT, C, PT>;
-  using MW = RowsMove<T, F::HT, C, QT>;
   extern __shared__ __align__(16) char smem[];
 
   // workgroups that read the same q/k rows go to one XCD, next to each other
@@ -68,26 +66,24 @@ void delta_rev_kernel(DeltaWalk p) {
   auto rows_of = [&](int cc) { return cc == 0 ? sr.len - (nch - 1) * C : C; };
   auto rows_at = [&](int cc) { return reinterpret_cast<bf16_t *>(smem + (F::NBUF == 2 && (cc & 1) ? F::rows : 0u)); };
   auto tab_at = [&](int cc) { return reinterpret_cast<float *>(smem + F::oTab + ((cc & 1) ? F::tab : 0u)); };
-  bf16_t *const sW = reinterpret_cast<bf16_t *>(smem + F::oW), *const sT = reinterpret_cast<bf16_t *>(smem + F::oT);
-  bf16_t *const sP = reinterpret_cast<bf16_t *>(smem + F::oP);
+  auto inverse_at = [&](int cc) { return reinterpret_cast<bf16_t *>(smem + F::oT + ((cc & 1) ? F::nT : 0u)); };
+  auto scores_at = [&](int cc) { return reinterpret_cast<bf16_t *>(smem + F::oP + ((cc & 1) ? F::nP : 0u)); };
 
   if (wave >= NW) {
     // =================================== helper waves ===================================
-    __builtin_amdgcn_s_setprio(2);  // what a helper holds up, all state waves wait for
     const int hw = wave - NW, ht = tid - 64 * NW;
-    const int ldx = p.Hk * K, ldw = p.H * V;  // row strides, elements
-    const uint32_t gx = MX::lane_offset(ht, ldx, K), gw = MW::lane_offset(ht, ldw, ncol);
-    const uint32_t rx = (uint32_t)(MX::RPI * ldx * SZ), rw = (uint32_t)(MW::RPI * ldw * SZ);
-    const int px = MX::lds_offset(ht, F::LDX), pw = MW::lds_offset(ht, F::LDW);
+    const int ldx = p.Hk * K;  // row stride, elements
+    const uint32_t gx = MX::lane_offset(ht, ldx, K);
+    const uint32_t rx = (uint32_t)(MX::RPI * ldx * SZ);
+    const int px = MX::lds_offset(ht, F::LDX);
     const int ax = l16 * F::LDX + 8 * grp;  // a row of q or k as an operand
     const T *const xf = reinterpret_cast<const T *>(p.q) + (sr.t0 * p.Hk + hk) * K;
     const T *const zf = reinterpret_cast<const T *>(p.k) + (sr.t0 * p.Hk + hk) * K;
-    const T *const wf = reinterpret_cast<const T *>(p.v) + (sr.t0 * p.H + h) * V + col0;
     using MI = InverseMove<C>;
-    u32x4_t fx[MX::IT], fz[MX::IT], fw[MW::IT], ft[MI::IT];
+    u32x4_t fx[MX::IT], fz[MX::IT], ft[MI::IT];
     float fg = 0.f, fb = 0.f;
     constexpr int DW = 3;  // the helper that forms the decays: one with fewer blocks of the scores
-    auto fetch_rows = [&](int cc) {
+    auto fetch = [&](int cc) {
       const int L = rows_of(cc);
       const int64_t t = start_of(cc);
       MX::load(fx, xf + t * ldx, ldx, L, K, gx, rx);
@@ -97,14 +93,10 @@ void delta_rev_kernel(DeltaWalk p) {
         if (p.g) fg = row_scalar(p.g + at, lane, L, p.H);
         fb = row_scalar(p.beta + at, lane, L, p.H);
       }
-    };
-    auto fetch_vt = [&](int cc) {
-      const int64_t t = start_of(cc);
-      MW::load(fw, wf + t * ldw, ldw, rows_of(cc), ncol, gw, rw);
       const int64_t slot = delta_slot(p.N, n, sr.t0, sr.t0 + t, C);
       MI::load(ft, p.inv + (slot * p.H + h) * delta_inverse_bytes(C), ht);
     };
-    auto put_rows = [&](int cc) {
+    auto put = [&](int cc) {
       bf16_t *s = rows_at(cc);
       MX::put(fx, s + px, F::LDX, F::XPL);
       MX::put(fz, s + F::nX / 2 + px, F::LDX, F::XPL);
@@ -115,18 +107,16 @@ void delta_rev_kernel(DeltaWalk p) {
         t[64 + lane] = d.lo;
         t[128 + lane] = d.from * p.scale;
         t[192 + lane] = d.rest;
-        t[320 + lane] = fb * d.from;
-        if (lane == 0) t[384] = d.all;
+        t[256 + lane] = fb * d.from;
+        if (lane == 0) t[320] = d.all;
       }
-    };
-    auto put_vt = [&]() {
-      MW::put(fw, sW + pw, F::LDW, F::WPL);
-      MI::template put<true>(ft, sT, hw, lane);
+      MI::template put<true>(ft, inverse_at(cc), hw, lane);
     };
     // transposed scores: lane has row l16 of k, four later rows of q
     auto scores = [&](int cc) {
       const bf16_t *const sX = rows_at(cc), *const sZ = sX + F::nX / 2;
       const float *const tab = tab_at(cc);
+      bf16_t *const sP = scores_at(cc);
 #pragma unroll
       for (int b0 = 0; b0 < NB; b0 += F::HELPERS) {
         const int blk = b0 + hw;
@@ -153,45 +143,29 @@ void delta_rev_kernel(DeltaWalk p) {
             const bool keep = i != j || 4 * grp + e >= l16;
             v[e] = keep ? acc[e] * (fast_exp2((hr[e] - hs) + (lr[e] - ls)) * p.scale) : 0.f;
           }
-          bf16_t *dst = sP + (16 * j + l16) * F::LDP + 32 * (i >> 1) + 8 * grp + 4 * (i & 1);
-          put_parts<3>(v, dst, F::PPL);
+          // frag_index with a tile that is known here only: row tile j, contraction i >> 1
+          const int f = C == 32 ? j : (j < 2 ? 2 * j + (i >> 1) : 2 + j);
+          put_parts<3>(v, sP + (f * 192 + lane) * 8 + 4 * (i & 1), 512);
         }
       }
     };
 
-    // the blocks of the scores beyond the triangle stay zero
-    for (int i = ht; i < (int)(F::nP / 4); i += F::HT) reinterpret_cast<unsigned *>(smem + F::oP)[i] = 0u;
-    MI::clear(sT, ht);
+    // the halves of pieces beyond the triangles stay zero
+    for (int i = ht; i < (int)(2 * (F::nT + F::nP) / 4); i += F::HT) reinterpret_cast<unsigned *>(smem + F::oT)[i] = 0u;
+    if (nch > 0) fetch(0);
+    __syncthreads();
     if (nch > 0) {
-      fetch_rows(0);
-      fetch_vt(0);
-      put_rows(0);
-    }
-    __syncthreads();  // cleared
-    if (nch > 0) {
-      put_vt();
-      if (nch > 1) {
-        fetch_rows(1);
-        fetch_vt(1);
-      }
+      put(0);
+      if (nch > 1) fetch(1);
     }
     __syncthreads();
     if (nch > 0) scores(0);
     __syncthreads();
     for (int cc = 0; cc < nch; ++cc) {  // beside chunk cc of the state waves
-      if constexpr (F::NBUF == 2) {
-        if (cc + 1 < nch) put_rows(cc + 1);
-        if (cc + 2 < nch) fetch_rows(cc + 2);
-      }
+      if constexpr (F::NBUF == 1) __syncthreads();
+      if (cc + 1 < nch) put(cc + 1);
+      if (cc + 2 < nch) fetch(cc + 2);
       __syncthreads();
-      if (cc + 1 < nch) put_vt();
-      if (cc + 2 < nch) fetch_vt(cc + 2);
-      if constexpr (F::NBUF == 1) {
-        __syncthreads();
-        if (cc + 1 < nch) put_rows(cc + 1);
-        if (cc + 2 < nch) fetch_rows(cc + 2);
-        __syncthreads();
-      }
       if (cc + 1 < nch) scores(cc + 1);
       __syncthreads();
     }
@@ -205,21 +179,51 @@ void delta_rev_kernel(DeltaWalk p) {
   load_state<F::NT>(p.s0 ? p.s0 + sbase : nullptr, K, V, grp, q, S);
 
   const int ax = l16 * F::LDX + 8 * grp;  // a row of k as an operand
-  const int tz = (4 * grp + (l16 >> 2)) * F::LDX + 8 * (l16 & 3), tw = cfrag_lane_off(F::LDW) + 16 * wave;
-  const int ap = l16 * F::LDP + 8 * grp;  // a row of the scores
-  const int ldy = p.H * V;
-  float *const uc = p.rows_out + (sr.t0 * p.H + h) * V + col0;
-  const uint32_t gu = qin ? (uint32_t)((4 * grp * ldy + 16 * wave + l16) * 4) : kOffNone;
+  const int tz = (4 * grp + (l16 >> 2)) * F::LDX + 8 * (l16 & 3);
+  const int ldv = p.H * V, wcol = 16 * wave;
+  const int64_t vrow = (sr.t0 * p.H + h) * V + col0;
+  const T *const oc = reinterpret_cast<const T *>(p.v) + vrow;  // d_o
+  float *const uc = p.rows_out + vrow;
+  const uint32_t go = qin ? (uint32_t)((4 * grp * ldv + wcol + l16) * SZ) : kOffNone;
 
+  ColumnRows<T, NC> fo;
+  auto fetch_o = [&](int cc) {
+    fo.load(tile_rsrc(oc + start_of(cc) * ldv, (uint32_t)(((rows_of(cc) - 1) * ldv + ncol) * SZ)), go, ldv);
+  };
+  if (nch > 0) fetch_o(0);
   __syncthreads();
   __syncthreads();
   __syncthreads();
   for (int cc = 0; cc < nch; ++cc) {
     const int L = rows_of(cc);
     const int64_t t0 = start_of(cc);
-    const bf16_t *const sX = rows_at(cc), *const sZ = sX + F::nX / 2;
+    const bf16_t *const sX = rows_at(cc), *const sZ = sX + F::nX / 2, *const sT = inverse_at(cc), *const sP = scores_at(cc);
     const float *const tab = tab_at(cc);
     store_state<F::NT>(p.states + (delta_slot(p.N, n, sr.t0, sr.t0 + t0, C) * p.H + h) * K * V, K, V, grp, q, S);
+
+    // as in the forward walk, what LDS has is asked for before its use and the order pinned
+    bf16x8_t kf[NC][IN], sb[2][3];
+    auto read_rows = [&](int s) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int pl = 0; pl < IN; ++pl) kf[i][pl] = row_frag(sZ + pl * F::XPL + 16 * i * F::LDX + ax + 32 * s);
+    };
+    auto split_state = [&](int s) { split_pair<3>(S[2 * s], S[2 * s + 1], sb[s & 1]); };
+    read_rows(0);
+    // ---- d_o as an operand, and scale 2^b d_o in parts ----
+    bf16x8_t w[KS][IN], wc[KS][3];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const f32x4_t o0 = fo.get(2 * s), o1 = fo.get(2 * s + 1);
+      const f32x4_t a0 = *reinterpret_cast<const f32x4_t *>(tab + 128 + 32 * s + 4 * grp);
+      const f32x4_t a1 = *reinterpret_cast<const f32x4_t *>(tab + 128 + 32 * s + 16 + 4 * grp);
+      split_pair<IN>(o0, o1, w[s]);
+      split_pair<3>(o0 * a0, o1 * a1, wc[s]);
+    }
+    if (cc + 1 < nch) fetch_o(cc + 1);
+    split_state(0);
+    pin();
 
     // ---- d0 = c (k D) + scores^T d_o ----
     f32x4_t z[NC], u[NC];
@@ -227,108 +231,107 @@ void delta_rev_kernel(DeltaWalk p) {
     for (int i = 0; i < NC; ++i) z[i] = zero4();
 #pragma unroll
     for (int s = 0; s < F::PS; ++s) {
-      bf16x8_t a[NC][IN], sb[3];
-#pragma unroll
-      for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int pl = 0; pl < IN; ++pl) a[i][pl] = row_frag(sZ + pl * F::XPL + 16 * i * F::LDX + ax + 32 * s);
-      split_pair<3>(S[2 * s], S[2 * s + 1], sb);
-      mma_cols<NC>(a, sb, z);
+      mma_cols<NC>(kf, sb[s & 1], z);
+      if (s + 1 < F::PS) {
+        split_state(s + 1);
+        pin();
+        read_rows(s + 1);
+      }
     }
+    InverseTimes<C, true> ti;  // the scores, and then the inverse: both of the same shape
+    ti.read(sP, lane, 0);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const f32x4_t c = *reinterpret_cast<const f32x4_t *>(tab + 192 + 16 * i + 4 * grp);
-      z[i] *= c;
-    }
-    bf16x8_t wc[KS][3];  // scale 2^b d_o in parts
+    for (int i = 0; i < NC; ++i) z[i] *= *reinterpret_cast<const f32x4_t *>(tab + 192 + 16 * i + 4 * grp);
+    pin();
+    // two tiles of the state at a time, products into one accumulator two apart
+    bf16x8_t zt[2][KS][IN];  // channels of two state tiles by the chunk's rows
+    auto read_channels = [&](const bf16_t *src, int t) {
+#pragma unroll
+      for (int w2 = 0; w2 < 2; ++w2)
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int pl = 0; pl < IN; ++pl)
+            zt[w2][s][pl] = load_frag32_at(src + pl * F::XPL + 32 * s * F::LDX + state_channel(t + w2, 0), F::LDX, tz);
+    };
+    auto add_channels = [&](const bf16x8_t (&x)[KS][3], int t) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = IN - 1; i >= 0; --i)
+#pragma unroll
+          for (int j = 2; j >= 0; --j)
+            if (i + j < 3) {
+#pragma unroll
+              for (int w2 = 0; w2 < 2; ++w2) S[t + w2] = Mma<bf16_t>::mma(zt[w2][s][i], x[s][j], S[t + w2]);
+            }
+    };
+    const float dec = tab[320];
+#pragma unroll
+    for (int t = 0; t < F::NT; ++t) S[t] *= dec;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      bf16x8_t w[IN];
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int pl = IN - 1; pl >= 0; --pl) {
-        w[pl] = load_frag32_at(sW + pl * F::WPL + 32 * s * F::LDW, F::LDW, tw);
+      for (int a = 2; a >= 0; --a)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] += static_cast<float>(w[pl][e]);
-      }
+        for (int b = IN - 1; b >= 0; --b)
+          if (a + b < 3) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i)
-        if (s >= i / 2) {
-          bf16x8_t a[3];
-#pragma unroll
-          for (int pl = 0; pl < 3; ++pl) a[pl] = row_frag(sP + pl * F::PPL + 16 * i * F::LDP + ap + 32 * s);
-          z[i] = mma_parts(a, w, z[i]);
-        }
-      const f32x4_t a0 = *reinterpret_cast<const f32x4_t *>(tab + 128 + 32 * s + 4 * grp);
-      const f32x4_t a1 = *reinterpret_cast<const f32x4_t *>(tab + 128 + 32 * s + 16 + 4 * grp);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] *= a0[e];
-        x[e + 4] *= a1[e];
-      }
-      split_pair<3>(f32x4_t{x[0], x[1], x[2], x[3]}, f32x4_t{x[4], x[5], x[6], x[7]}, wc[s]);
+            for (int i = 0; i < NC; ++i)
+              if (InverseTimes<C, true>::has(i, s)) z[i] = Mma<bf16_t>::mma(ti.t[i][a], w[s][b], z[i]);
+          }
+      ti.read(s + 1 < KS ? sP : sT, lane, s + 1 < KS ? s + 1 : 0);
+      pin();
     }
-    // ---- du = T^T d0 ----
+    // ---- du = T^T d0; what q and d_o add to the state fills the pauses of the chain ----
+    read_channels(sX, 0);
     bf16x8_t wu[KS][3];
 #pragma unroll
     for (int s = 0; s < KS; ++s) split_pair<3>(z[2 * s], z[2 * s + 1], wu[s]);
 #pragma unroll
     for (int i = 0; i < NC; ++i) u[i] = zero4();
+    pin();
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-      InverseTimes<C, true> ti;
-      ti.read(sT, lane, s);
       ti.add(wu[s], u, s);
+      if (s + 1 < KS) {
+        ti.read(sT, lane, s + 1);
+        pin();
+      }
     }
 #pragma unroll
+    for (int t = 0; t < F::NT; t += 2) {
+      add_channels(wc, t);
+      if (t + 2 < F::NT) read_channels(sX, t + 2);
+    }
+    read_channels(sZ, 0);
+    pin();
+#pragma unroll
     for (int s = 0; s < KS; ++s) {  // -beta 2^b du in parts
-      const f32x4_t b0 = *reinterpret_cast<const f32x4_t *>(tab + 320 + 32 * s + 4 * grp);
-      const f32x4_t b1 = *reinterpret_cast<const f32x4_t *>(tab + 320 + 32 * s + 16 + 4 * grp);
+      const f32x4_t b0 = *reinterpret_cast<const f32x4_t *>(tab + 256 + 32 * s + 4 * grp);
+      const f32x4_t b1 = *reinterpret_cast<const f32x4_t *>(tab + 256 + 32 * s + 16 + 4 * grp);
       split_pair<3>(-(u[2 * s] * b0), -(u[2 * s + 1] * b1), wu[s]);
     }
     {
-      const auto rs = tile_rsrc(uc + t0 * ldy, (uint32_t)(((L - 1) * ldy + ncol) * 4));
-      uint32_t off = gu;
+      const auto rs = tile_rsrc(uc + t0 * ldv, (uint32_t)(((L - 1) * ldv + ncol) * 4));
+      uint32_t off = qin ? (uint32_t)((4 * grp * ldv + wcol + l16) * 4) : kOffNone;
       asm volatile("" : "+v"(off));  // formed here, not held in registers over the chunks
 #pragma unroll
       for (int i = 0; i < NC; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(u[i][e]), rs, (int)(off + (16 * i + e) * ldy * 4), 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(u[i][e]), rs, (int)(off + (16 * i + e) * ldv * 4), 0, 0);
     }
-    __syncthreads();
-
-    // ---- the state's gradient: two tiles at a time, products into one accumulator two apart ----
-    const float dec = tab[384];
+    if constexpr (F::NBUF == 2) __syncthreads();
+    // ---- the state's gradient ----
 #pragma unroll
     for (int t = 0; t < F::NT; t += 2) {
-      S[t] *= dec;
-      S[t + 1] *= dec;
-#pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        const bf16_t *const src = which ? sZ : sX;
-        bf16x8_t a[2][KS][IN];
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-#pragma unroll
-          for (int s = 0; s < KS; ++s)
-#pragma unroll
-            for (int pl = 0; pl < IN; ++pl)
-              a[w][s][pl] = load_frag32_at(src + pl * F::XPL + 32 * s * F::LDX + state_channel(t + w, 0), F::LDX, tz);
-#pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int i = IN - 1; i >= 0; --i)
-#pragma unroll
-            for (int j = 2; j >= 0; --j)
-              if (i + j < 3) {
-#pragma unroll
-                for (int w = 0; w < 2; ++w) S[t + w] = Mma<bf16_t>::mma(a[w][s][i], which ? wu[s][j] : wc[s][j], S[t + w]);
-              }
-      }
+      add_channels(wu, t);
+      if (t + 2 < F::NT) read_channels(sZ, t + 2);
     }
+    pin();
     if constexpr (F::NBUF == 1) {
-      __syncthreads();
+      __syncthreads();  // q and k are done with
       __syncthreads();
     }
     __syncthreads();

@@ -104,7 +104,10 @@ void delta_walk_kernel(DeltaWalk p) {
 
   if (wave >= NW) {
     // =================================== helper waves ===================================
-    __builtin_amdgcn_s_setprio(2);  // what a helper holds up, all state waves wait for
+    // What a helper holds up, all state waves wait for. With two state waves to a helper on
+    // a SIMD (b4 t4096 h64) 400 us for 405; with one each the state wave is the later one
+    // (b4 t2048 h32, u and states kept: 140 us without, 150 with).
+    if constexpr (NW == 8) __builtin_amdgcn_s_setprio(2);
     const int hw = wave - NW, ht = tid - 64 * NW;
     const int ldx = p.Hk * K;  // row stride, elements
     const uint32_t gx = MX::lane_offset(ht, ldx, K);
