@@ -3,17 +3,21 @@
 //     T = (I + A)^{-1},   A_rs = beta_r 2^{b_r - b_s} k_r . k_s  for s < r,
 //
 // which needs no state and so runs over all chunks at once. A wave takes a chunk and
-// a q/k head by itself, with no barrier: rows of k come from memory as operands of
-// the causal 16 x 16 blocks of k k^T, which stay in accumulators for all value heads
-// that share them. Per head the decays and beta make A; the diagonal blocks are
-// inverted by forward substitution, and the blocks below, level by level, come from
-// T (I + A) = I as
+// a head by itself, with no barrier: rows of k come from memory as operands of the
+// causal 16 x 16 blocks of k k^T, and the decays and beta make -A of these accumulators
+// in place. The diagonal blocks are inverted by forward substitution, and the blocks
+// below, level by level, come from T (I + A) = I as
 //
 //     T_ij^T = -T_jj^T sum over m = j+1..i of A_mj^T T_im^T
 //
 // in fp32 matrix products whose operands are accumulators as they stand: of A_mj, of
 // T_jj, and of T_im^T. A lane of T_ij^T holds four neighbours of a row of T, which
 // leave in 16-byte stores. For the forward T takes beta as factors of its columns.
+//
+// A wave is a long chain of short steps, which only other waves on its SIMD hide: four of
+// them by 114 registers. (Value heads that share a q/k head in one wave, k k^T kept for
+// them, were fewer waves with 40 registers spilled: packed t15872, two heads each, 70 us
+// for 51.) b4 t4096 h64 d128 takes 98 us, its bytes (k read, T written: 436 MB) 80 us.
 #include "delta_chunk.h"
 
 namespace kda {
@@ -82,25 +86,20 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaPrep p, int64_t
   const int wave = wave_id(), lane = threadIdx.x & 63, grp = lane >> 4, l16 = lane & 15;
   const int64_t item = (int64_t)blockIdx.x * 4 + wave;
   if (item >= items) return;
-  const int hk = (int)(item % p.Hk);
-  const int64_t slot = item / p.Hk;
+  const int h = (int)(item % p.H), hk = h / (p.H / p.Hk);
+  const int64_t slot = item / p.H;
   SegLoc sg;
   if (!locate_chunk(p, slot, C, sg)) return;
-  const int L = (int)(sg.hi - sg.lo), G = p.H / p.Hk;
+  const int L = (int)(sg.hi - sg.lo);
   float *const sD = sAll[wave], *const tab = sD + F::WAVE;
 
-  const int64_t row0 = sg.lo * p.H + hk * G;
-  float fg = 0.f, fb = 0.f;
-  auto fetch = [&](int j) {
-    if (p.g) fg = row_scalar(p.g + row0 + j, lane, L, p.H);
-    fb = row_scalar(p.beta + row0 + j, lane, L, p.H);
-  };
-  fetch(0);
+  const int64_t row0 = sg.lo * p.H + h;
+  const float g = p.g ? row_scalar(p.g + row0, lane, L, p.H) : 0.f, beta = row_scalar(p.beta + row0, lane, L, p.H);
 
   // ---- k k^T: block (i, j), row 4 grp + e of tile i, column l16 of tile j ----
-  f32x4_t gram[NB];
+  f32x4_t A[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) gram[b] = zero4();
+  for (int b = 0; b < NB; ++b) A[b] = zero4();
   {
     const int ldk = p.Hk * p.K;
     const T *const base = reinterpret_cast<const T *>(p.k) + (sg.lo * p.Hk + hk) * p.K;
@@ -123,91 +122,92 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaPrep p, int64_t
 #pragma unroll
       for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int j = 0; j <= i; ++j) gram[i * (i + 1) / 2 + j] = mma_parts(a[i], a[j], gram[i * (i + 1) / 2 + j]);
+        for (int j = 0; j <= i; ++j) A[i * (i + 1) / 2 + j] = mma_parts(a[i], a[j], A[i * (i + 1) / 2 + j]);
     }
   }
 
-  for (int jh = 0; jh < G; ++jh) {
-    const RowDecay d = row_decay(fg);
-    tab[lane] = d.hi;
-    tab[64 + lane] = d.lo;
-    tab[128 + lane] = fb;
-    if (jh + 1 < G) fetch(jh + 1);
-    lds_wave_order();
-    // -A: the diagonal blocks to LDS, the others in place
-    f32x4_t A[NB];
+  float kk[NC];  // |k|^2, on the diagonals
+  if (p.bound) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      const f32x4_t hr = *reinterpret_cast<const f32x4_t *>(tab + 16 * i + 4 * grp);
-      const f32x4_t lr = *reinterpret_cast<const f32x4_t *>(tab + 64 + 16 * i + 4 * grp);
-      const f32x4_t be = *reinterpret_cast<const f32x4_t *>(tab + 128 + 16 * i + 4 * grp);
+      const f32x4_t &x = A[i * (i + 1) / 2 + i];
+      kk[i] = (l16 & 2) ? ((l16 & 1) ? x[3] : x[2]) : ((l16 & 1) ? x[1] : x[0]);
+    }
+  }
+  const RowDecay d = row_decay(g);
+  tab[lane] = d.hi;
+  tab[64 + lane] = d.lo;
+  tab[128 + lane] = beta;
+  lds_wave_order();
+  // -A: the diagonal blocks to LDS, the others in place
 #pragma unroll
-      for (int j = 0; j <= i; ++j) {
-        const float hs = tab[16 * j + l16], ls = tab[64 + 16 * j + l16];
-        f32x4_t &x = A[i * (i + 1) / 2 + j];
+  for (int i = 0; i < NC; ++i) {
+    const f32x4_t hr = *reinterpret_cast<const f32x4_t *>(tab + 16 * i + 4 * grp);
+    const f32x4_t lr = *reinterpret_cast<const f32x4_t *>(tab + 64 + 16 * i + 4 * grp);
+    const f32x4_t be = *reinterpret_cast<const f32x4_t *>(tab + 128 + 16 * i + 4 * grp);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float w = fast_exp2((hr[e] - hs) + (lr[e] - ls)) * be[e];
-          x[e] = i != j || 4 * grp + e > l16 ? -gram[i * (i + 1) / 2 + j][e] * w : 0.f;
-          if (i == j) sD[(16 * i + 4 * grp + e) * LDD + l16] = x[e];
-        }
+    for (int j = 0; j <= i; ++j) {
+      const float hs = tab[16 * j + l16], ls = tab[64 + 16 * j + l16];
+      f32x4_t &x = A[i * (i + 1) / 2 + j];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w = fast_exp2((hr[e] - hs) + (lr[e] - ls)) * be[e];
+        x[e] = i != j || 4 * grp + e > l16 ? -x[e] * w : 0.f;
+        if (i == j) sD[(16 * i + 4 * grp + e) * LDD + l16] = x[e];
       }
     }
-    lds_wave_order();
-    // T_ii, and transposed
-    f32x4_t D[NC], Tt[NB];
+  }
+  lds_wave_order();
+  // T_ii, and transposed
+  f32x4_t D[NC], Tt[NB];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) unit_inverse16(sD + 16 * i * LDD, LDD, D[i]);
-    lds_wave_order();
+  for (int i = 0; i < NC; ++i) unit_inverse16(sD + 16 * i * LDD, LDD, D[i]);
+  lds_wave_order();
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
+  for (int i = 0; i < NC; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sD[(16 * i + 4 * grp + e) * LDD + l16] = D[i][e];
-    lds_wave_order();
+    for (int e = 0; e < 4; ++e) sD[(16 * i + 4 * grp + e) * LDD + l16] = D[i][e];
+  lds_wave_order();
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
-      Tt[i * (i + 1) / 2 + i] = *reinterpret_cast<const f32x4_t *>(sD + (16 * i + l16) * LDD + 4 * grp);
+  for (int i = 0; i < NC; ++i)
+    Tt[i * (i + 1) / 2 + i] = *reinterpret_cast<const f32x4_t *>(sD + (16 * i + l16) * LDD + 4 * grp);
 #pragma unroll
-    for (int n = 1; n < NC; ++n)
+  for (int n = 1; n < NC; ++n)
 #pragma unroll
-      for (int j = 0; j + n < NC; ++j) {
-        const int i = j + n;
-        f32x4_t P = zero4();
+    for (int j = 0; j + n < NC; ++j) {
+      const int i = j + n;
+      f32x4_t P = zero4();
 #pragma unroll
-        for (int m = j + 1; m <= i; ++m) P = mma_block(A[m * (m + 1) / 2 + j], Tt[i * (i + 1) / 2 + m], P);
-        Tt[i * (i + 1) / 2 + j] = mma_block(D[j], P, zero4());
-      }
-    if (p.bound) {
-      // a step I - beta k k^T enlarges by |1 - beta |k|^2| if that is above one: by nothing
-      // for rows of norm one; |k|^2 lies on the diagonals of k k^T
-      float grow = 0.f;
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const f32x4_t &x = gram[i * (i + 1) / 2 + i];
-        const float kk = (l16 & 2) ? ((l16 & 1) ? x[3] : x[2]) : ((l16 & 1) ? x[1] : x[0]);
-        const float f = fabsf(1.f - tab[128 + 16 * i + l16] * kk);
-        grow += grp == (l16 >> 2) && !(f <= 1.f) ? fast_log2(f) : 0.f;
-      }
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) grow += __shfl_xor(grow, off);
-      if (lane == 0) p.bound[slot * p.H + hk * G + jh] = tab[63] + tab[127] + grow;
+      for (int m = j + 1; m <= i; ++m) P = mma_block(A[m * (m + 1) / 2 + j], Tt[i * (i + 1) / 2 + m], P);
+      Tt[i * (i + 1) / 2 + j] = mma_block(D[j], P, zero4());
     }
-    // out: row l16 of tile i, columns 4 grp + e of tile j
-    char *const dst = p.inv + (slot * p.H + hk * G + jh) * delta_inverse_bytes(C) + lane * 16;
+  if (p.bound) {
+    // a step I - beta k k^T enlarges by |1 - beta |k|^2| if that is above one: by nothing
+    // for rows of norm one
+    float grow = 0.f;
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      f32x4_t be{1.f, 1.f, 1.f, 1.f};
-      if (p.fold) be = *reinterpret_cast<const f32x4_t *>(tab + 128 + 16 * j + 4 * grp);
-#pragma unroll
-      for (int i = j; i < NC; ++i)
-        *reinterpret_cast<f32x4_t *>(dst + (i * (i + 1) / 2 + j) * 1024) = Tt[i * (i + 1) / 2 + j] * be;
+    for (int i = 0; i < NC; ++i) {
+      const float f = fabsf(1.f - tab[128 + 16 * i + l16] * kk[i]);
+      grow += grp == (l16 >> 2) && !(f <= 1.f) ? fast_log2(f) : 0.f;
     }
-    lds_wave_order();
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) grow += __shfl_xor(grow, off);
+    if (lane == 0) p.bound[slot * p.H + h] = tab[63] + tab[127] + grow;
+  }
+  // out: row l16 of tile i, columns 4 grp + e of tile j
+  char *const dst = p.inv + (slot * p.H + h) * delta_inverse_bytes(C) + lane * 16;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    f32x4_t be{1.f, 1.f, 1.f, 1.f};
+    if (p.fold) be = *reinterpret_cast<const f32x4_t *>(tab + 128 + 16 * j + 4 * grp);
+#pragma unroll
+    for (int i = j; i < NC; ++i)
+      *reinterpret_cast<f32x4_t *>(dst + (i * (i + 1) / 2 + j) * 1024) = Tt[i * (i + 1) / 2 + j] * be;
   }
 }
 
 int64_t prep_items(const DeltaPrep &p) {
-  return delta_slots((int64_t)p.B * p.T, p.N, delta_chunk(linear_tile(p.K), p.is_bf16)) * p.Hk;
+  return delta_slots((int64_t)p.B * p.T, p.N, delta_chunk(linear_tile(p.K), p.is_bf16)) * p.H;
 }
 
 template <typename T, int PT>
