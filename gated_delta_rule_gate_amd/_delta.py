@@ -179,8 +179,9 @@ def _qk_args(q, k, q_weight, k_weight, positions, inv_freq, sections, spread, pa
     _require(q.dim() == 4 and k.dim() == 4 and q.shape[:2] == k.shape[:2] and q.shape[3] == k.shape[3],
              "q must be [B, T, H, D], k [B, T, Hk, D]")
     _require(q.dtype in (torch.bfloat16, torch.float32) and k.dtype is q.dtype, "q and k must share dtype bf16 or fp32")
-    _require(norm in QK_NORMS, "norm must be one of %s" % sorted(QK_NORMS))
-    _require(pairs in PAIRS, "pairs must be one of %s" % sorted(PAIRS))
+    if norm not in QK_NORMS or pairs not in PAIRS:
+        _require(norm in QK_NORMS, "norm must be one of %s" % sorted(QK_NORMS))
+        _require(False, "pairs must be one of %s" % sorted(PAIRS))
     _require((positions is None) == (inv_freq is None), "positions and inv_freq come together")
     B, T, H, D = q.shape
     Hk, dev = k.shape[2], q.get_device()
@@ -222,10 +223,16 @@ def qk_norm_rope(q, k, q_weight=None, k_weight=None, *, positions=None, inv_freq
     """
     a, dev, (pq, pk, pwq, pwk, pp, pf) = _qk_args(q, k, q_weight, k_weight, positions, inv_freq, sections, spread,
                                                   pairs, norm, eps)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-    po, a.qo_stride = _heads("q_out", q_out, q.shape, q.dtype, dev)
-    pko, a.ko_stride = _heads("k_out", k_out, k.shape, q.dtype, dev)
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        po = q_out.data_ptr()
+    else:
+        po, a.qo_stride = _heads("q_out", q_out, q.shape, q.dtype, dev)
+    if k_out is None:
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        pko = k_out.data_ptr()
+    else:
+        pko, a.ko_stride = _heads("k_out", k_out, k.shape, q.dtype, dev)
     _launch(dev, _lib().kda_qk_norm_rope_fwd, ctypes.byref(a), pq, pk, pwq, pwk, pp, pf, po, pko)
     return q_out, k_out
 
@@ -248,8 +255,8 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, *, posi
         need = int(L.kda_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(a)))
     pw, nw, _keep = _workspace(workspace, need, dev)
     like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
-    got = dict(dq=torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               dk=torch.empty(k.shape, dtype=k.dtype, device=k.device), dq_weight=like(q_weight),
+    got = dict(dq=torch.empty_like(q, memory_format=torch.contiguous_format),
+               dk=torch.empty_like(k, memory_format=torch.contiguous_format), dq_weight=like(q_weight),
                dk_weight=like(k_weight))
     ptr = {n: None if t is None else t.data_ptr() for n, t in got.items()}
     _launch(dev, L.kda_qk_norm_rope_bwd, ctypes.byref(a), pq, pk, pwq, pwk, pp, pf, pdq, pdk, ptr["dq"], ptr["dk"],

@@ -4,14 +4,17 @@
 //   n = w x rho,  rho = (mean x^2 + eps)^-1/2 (L2: sum);   y = R n
 //   dn = R^T dy;  dw = sum over rows of dn x rho;  dx = rho (w dn - x rho^2 mean(w dn x))  (L2: sum)
 //
-// Bound by the rows' bytes. A lane holds both channels of VEC pairs, so the
-// rotation never leaves it: its two vectors lie rot/2 channels apart (or next to
-// each other), channels that are not turned are dealt out the same way, and D /
-// (2 VEC) lanes hold a row. A group of lanes takes one token and every HS-th of
-// its heads, so that angles (fp64 products and reduction), their sine and cosine
-// and the weights are formed once for several rows. Weights' gradients stay in
-// registers over a workgroup's rows, leave as one part a workgroup, and are added
-// over workgroups in order.
+// A lane holds both channels of VEC pairs, so the rotation never leaves it: its two
+// vectors lie rot/2 channels apart (or next to each other), channels that are not turned
+// are dealt out the same way, and D / (2 VEC) lanes hold a row. A group of lanes takes one
+// token and every HS-th of its heads, the next row on its way beside the one at hand. A
+// workgroup's angles (fp64 products and reduction) with their sines and cosines are formed
+// once, one by each thread, and handed over in LDS: formed by every group for itself they
+// took b4 t4096 h32/8 d128 from 74 to 89 us. Weights' gradients stay in registers over a
+// workgroup's rows, leave as one part a workgroup, and are added over workgroups in order.
+//
+// Bound by the rows' bytes: at b4 t4096 h32/8 d128 the forward takes 70 us and the backward
+// 109 + 4 us, where their 336 and 503 MB would take 64 and 97 us at a large copy's 5.2 TB/s.
 #include "../../include/kda_rope.h"
 #include "kda_device.h"
 #include "linear_launch.h"
@@ -85,16 +88,14 @@ __device__ __forceinline__ Place place_of(const QkRope &p, int j) {
   return l;
 }
 
-// Cosine and sine of the lane's angles at a token: turns in fp64, whole turns taken off there.
-template <int VEC>
-__device__ __forceinline__ void angles(const QkRope &p, const Place &l, int64_t token, float (&c)[VEC], float (&s)[VEC]) {
-  int pos[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int a = 0; a < 4; ++a)
-    if (a < p.axes) pos[a] = p.pos[a * p.tokens + token];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    const int i = l.j * VEC + e;
+// Cosines and sines of `count` tokens from t0 on, each angle by one thread, to LDS: turns in
+// fp64, whole turns taken off there.
+__device__ __forceinline__ void angles(const QkRope &p, int64_t t0, int count, float *cs) {
+  const int half = p.rot / 2;
+  for (int idx = threadIdx.x; idx < count * half; idx += 256) {
+    const int tk = idx / half, i = idx - tk * half;
+    const int64_t token = t0 + tk;
+    if (token >= p.tokens) break;
     int at = 0;
     if (p.axes > 1) {
       if (p.spread) {
@@ -105,10 +106,20 @@ __device__ __forceinline__ void angles(const QkRope &p, const Place &l, int64_t 
         at = (i >= p.sec[0]) + (i >= p.sec[1]) + (i >= p.sec[2]);
       }
     }
-    const int x = at == 0 ? pos[0] : (at == 1 ? pos[1] : (at == 2 ? pos[2] : pos[3]));
-    double t = ((double)x * (double)p.freq[i]) * 0.15915494309189533577;
+    double t = ((double)p.pos[at * p.tokens + token] * (double)p.freq[i]) * 0.15915494309189533577;
     t -= rint(t);
-    sincospif(2.0f * (float)t, &s[e], &c[e]);
+    sincospif(2.0f * (float)t, &cs[count * half + idx], &cs[idx]);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void read_angles(const QkRope &p, const Place &l, int tk, int count, const float *cs, float (&c)[VEC],
+                                            float (&s)[VEC]) {
+  const float *src = cs + tk * (p.rot / 2) + l.j * VEC;
+#pragma unroll
+  for (int e = 0; e < VEC; e += 4) {
+    const f32x4_t x = *reinterpret_cast<const f32x4_t *>(src + e), y = *reinterpret_cast<const f32x4_t *>(src + count * (p.rot / 2) + e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[e + i] = x[i], s[e + i] = y[i];
   }
 }
 
@@ -155,51 +166,59 @@ __global__ __launch_bounds__(256) void qk_rope_fwd_kernel(QkRope p, int HS) {
   const int g = threadIdx.x / GL, tpb = 256 / GL / HS;  // tokens of a workgroup at a time
   const Place l = place_of<VEC>(p, threadIdx.x % GL);
   const float inv = p.l2 ? 1.0f : 1.0f / (float)p.D;
-  for (int64_t t0 = (int64_t)blockIdx.x * tpb; t0 < p.tokens; t0 += (int64_t)gridDim.x * tpb) {
+  extern __shared__ __align__(16) float angle_lds[];  // two iterations' cosines and sines
+  const int rows = p.H + p.Hk;
+  int turn_no = 0;
+  for (int64_t t0 = (int64_t)blockIdx.x * tpb; t0 < p.tokens; t0 += (int64_t)gridDim.x * tpb, turn_no ^= 1) {
     const int64_t token = t0 + g / HS;
-    if (token >= p.tokens) break;  // (a whole group; no barrier follows)
+    const bool live = token < p.tokens && l.in;
+    const T *const q = reinterpret_cast<const T *>(p.q) + token * p.qs, *const k = reinterpret_cast<const T *>(p.k) + token * p.ks;
+    T *const qo = reinterpret_cast<T *>(p.qo) + token * p.qos, *const ko = reinterpret_cast<T *>(p.ko) + token * p.kos;
+    Raw<T, VEC> ra, rb;
+    auto fetch = [&](int r) {  // a row: q's heads, then k's
+      if (r < rows && live) {
+        const T *in = r < p.H ? q + (int64_t)r * p.D : k + (int64_t)(r - p.H) * p.D;
+        ra.load(in + l.a);
+        rb.load(in + l.b);
+      }
+    };
+    int r = g % HS;
+    fetch(r);
     float c[VEC], s[VEC];
-    if (l.turned) angles<VEC>(p, l, token, c, s);
-    int h = g % HS;  // q's heads, then k's
-    for (int part = 0; part < 2; ++part) {
-      const int heads = part ? p.Hk : p.H;
-      const T *in = reinterpret_cast<const T *>(part ? p.k : p.q) + token * (part ? p.ks : p.qs);
-      T *out = reinterpret_cast<T *>(part ? p.ko : p.qo) + token * (part ? p.kos : p.qos);
-      float wa[VEC], wb[VEC];
-      weight_of<VEC>(part ? p.k_weight : p.q_weight, l, wa, wb);
-      Raw<T, VEC> ra, rb;
-      if (h < heads && l.in) {
-        ra.load(in + (int64_t)h * p.D + l.a);
-        rb.load(in + (int64_t)h * p.D + l.b);
-      }
-      for (; h < heads; h += HS) {
-        float a[VEC], b[VEC];
-        ra.get(a);
-        rb.get(b);
-        if (h + HS < heads && l.in) {  // the next row on its way
-          ra.load(in + (int64_t)(h + HS) * p.D + l.a);
-          rb.load(in + (int64_t)(h + HS) * p.D + l.b);
-        }
-        float rho = 1.f;
-        if (p.normed) {
-          float ss = 0.f;
+    if (p.rot) {
+      float *const cs = angle_lds + turn_no * tpb * p.rot;
+      angles(p, t0, tpb, cs);
+      __syncthreads();
+      if (l.turned && live) read_angles<VEC>(p, l, g / HS, tpb, cs, c, s);
+    }
+    if (token >= p.tokens) continue;  // (a whole group)
+    float wa[VEC], wb[VEC];
+    weight_of<VEC>(r < p.H ? p.q_weight : p.k_weight, l, wa, wb);
+    for (; r < rows; r += HS) {
+      float a[VEC], b[VEC];
+      ra.get(a);
+      rb.get(b);
+      fetch(r + HS);  // the next row on its way
+      float rho = 1.f;
+      if (p.normed) {
+        float ss = 0.f;
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) ss += a[e] * a[e] + b[e] * b[e];
-          ss = row_sum<GL>(l.in ? ss : 0.f);
-          rho = 1.0f / sqrtf(ss * inv + p.eps);
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          a[e] = a[e] * rho * wa[e];
-          b[e] = b[e] * rho * wb[e];
-        }
-        if (l.turned) turn<VEC>(p.adjacent, 1.f, c, s, a, b);
-        if (l.in) {
-          Raw<T, VEC>::store(out + (int64_t)h * p.D + l.a, a);
-          Raw<T, VEC>::store(out + (int64_t)h * p.D + l.b, b);
-        }
+        for (int e = 0; e < VEC; ++e) ss += a[e] * a[e] + b[e] * b[e];
+        ss = row_sum<GL>(l.in ? ss : 0.f);
+        rho = 1.0f / sqrtf(ss * inv + p.eps);
       }
-      h -= heads;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        a[e] = a[e] * rho * wa[e];
+        b[e] = b[e] * rho * wb[e];
+      }
+      if (l.turned) turn<VEC>(p.adjacent, 1.f, c, s, a, b);
+      if (l.in) {
+        T *const out = r < p.H ? qo + (int64_t)r * p.D : ko + (int64_t)(r - p.H) * p.D;
+        Raw<T, VEC>::store(out + l.a, a);
+        Raw<T, VEC>::store(out + l.b, b);
+      }
+      if (r < p.H && r + HS >= p.H) weight_of<VEC>(p.k_weight, l, wa, wb);
     }
   }
 }
@@ -212,68 +231,84 @@ __global__ __launch_bounds__(256) void qk_rope_bwd_kernel(QkRope p, int HS) {
   float acc[2][2][VEC];  // weights' gradients of q and k
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[0][0][e] = acc[0][1][e] = acc[1][0][e] = acc[1][1][e] = 0.f;
-  for (int64_t t0 = (int64_t)blockIdx.x * tpb; t0 < p.tokens; t0 += (int64_t)gridDim.x * tpb) {
+  extern __shared__ __align__(16) float angle_lds[];
+  const int rows = p.H + p.Hk;
+  int turn_no = 0;
+  for (int64_t t0 = (int64_t)blockIdx.x * tpb; t0 < p.tokens; t0 += (int64_t)gridDim.x * tpb, turn_no ^= 1) {
     const int64_t token = t0 + g / HS;
-    if (token >= p.tokens) break;
-    float c[VEC], s[VEC];
-    if (l.turned) angles<VEC>(p, l, token, c, s);
-    int h = g % HS;
-#pragma unroll
-    for (int part = 0; part < 2; ++part) {
-      const int heads = part ? p.Hk : p.H;
-      const T *in = reinterpret_cast<const T *>(part ? p.k : p.q) + token * (part ? p.ks : p.qs);
-      const T *dy = reinterpret_cast<const T *>(part ? p.dko : p.dqo) + token * (part ? p.kos : p.qos);
-      T *out = reinterpret_cast<T *>(part ? p.ko : p.qo) + token * heads * p.D;
-      float wa[VEC], wb[VEC];
-      weight_of<VEC>(part ? p.k_weight : p.q_weight, l, wa, wb);
-      Raw<T, VEC> ra, rb, da, db;
-      auto fetch = [&](int hh) {
-        if (hh < heads && l.in) {
-          ra.load(in + (int64_t)hh * p.D + l.a);
-          rb.load(in + (int64_t)hh * p.D + l.b);
-          da.load(dy + (int64_t)hh * p.D + l.a);
-          db.load(dy + (int64_t)hh * p.D + l.b);
-        }
-      };
-      fetch(h);
-      for (; h < heads; h += HS) {
-        float a[VEC], b[VEC], ga[VEC], gb[VEC];
-        ra.get(a);
-        rb.get(b);
-        da.get(ga);
-        db.get(gb);
-        fetch(h + HS);
-        if (!l.in) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) a[e] = b[e] = ga[e] = gb[e] = 0.f;
-        }
-        if (l.turned) turn<VEC>(p.adjacent, -1.f, c, s, ga, gb);
-        float rho = 1.f, m = 0.f;
-        if (p.normed) {
-          float ss = 0.f, dot = 0.f;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            ss += a[e] * a[e] + b[e] * b[e];
-            dot += ga[e] * wa[e] * a[e] + gb[e] * wb[e] * b[e];
-          }
-          ss = row_sum<GL>(ss);
-          dot = row_sum<GL>(dot);
-          rho = 1.0f / sqrtf(ss * inv + p.eps);
-          m = dot * inv * rho * rho;
-        }
-        if (l.in) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            acc[part][0][e] += ga[e] * (a[e] * rho);
-            acc[part][1][e] += gb[e] * (b[e] * rho);
-            a[e] = rho * (ga[e] * wa[e] - a[e] * m);
-            b[e] = rho * (gb[e] * wb[e] - b[e] * m);
-          }
-          Raw<T, VEC>::store(out + (int64_t)h * p.D + l.a, a);
-          Raw<T, VEC>::store(out + (int64_t)h * p.D + l.b, b);
-        }
+    const bool live = token < p.tokens && l.in;
+    const T *const q = reinterpret_cast<const T *>(p.q) + token * p.qs, *const k = reinterpret_cast<const T *>(p.k) + token * p.ks;
+    const T *const dqo = reinterpret_cast<const T *>(p.dqo) + token * p.qos, *const dko = reinterpret_cast<const T *>(p.dko) + token * p.kos;
+    Raw<T, VEC> ra, rb, da, db;
+    auto fetch = [&](int r) {  // a row: q's heads, then k's
+      if (r < rows && live) {
+        const bool of_k = r >= p.H;
+        const int64_t at = (int64_t)(of_k ? r - p.H : r) * p.D;
+        const T *const in = (of_k ? k : q) + at, *const dy = (of_k ? dko : dqo) + at;
+        ra.load(in + l.a);
+        rb.load(in + l.b);
+        da.load(dy + l.a);
+        db.load(dy + l.b);
       }
-      h -= heads;
+    };
+    int r = g % HS;
+    fetch(r);
+    float c[VEC], s[VEC];
+    if (p.rot) {
+      float *const cs = angle_lds + turn_no * tpb * p.rot;
+      angles(p, t0, tpb, cs);
+      __syncthreads();
+      if (l.turned && live) read_angles<VEC>(p, l, g / HS, tpb, cs, c, s);
+    }
+    if (token >= p.tokens) continue;  // (a whole group)
+    float wa[VEC], wb[VEC];
+    weight_of<VEC>(r < p.H ? p.q_weight : p.k_weight, l, wa, wb);
+    for (; r < rows; r += HS) {
+      float a[VEC], b[VEC], ga[VEC], gb[VEC];
+      ra.get(a);
+      rb.get(b);
+      da.get(ga);
+      db.get(gb);
+      fetch(r + HS);
+      if (!l.in) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) a[e] = b[e] = ga[e] = gb[e] = 0.f;
+      }
+      if (l.turned) turn<VEC>(p.adjacent, -1.f, c, s, ga, gb);
+      float rho = 1.f, m = 0.f;
+      if (p.normed) {
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          ss += a[e] * a[e] + b[e] * b[e];
+          dot += ga[e] * wa[e] * a[e] + gb[e] * wb[e] * b[e];
+        }
+        ss = row_sum<GL>(ss);
+        dot = row_sum<GL>(dot);
+        rho = 1.0f / sqrtf(ss * inv + p.eps);
+        m = dot * inv * rho * rho;
+      }
+      if (l.in) {
+        auto add = [&](float (&to)[2][VEC]) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            to[0][e] += ga[e] * (a[e] * rho);
+            to[1][e] += gb[e] * (b[e] * rho);
+          }
+        };
+        if (r < p.H) add(acc[0]);
+        else add(acc[1]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          a[e] = rho * (ga[e] * wa[e] - a[e] * m);
+          b[e] = rho * (gb[e] * wb[e] - b[e] * m);
+        }
+        T *const out = r < p.H ? reinterpret_cast<T *>(p.qo) + (token * p.H + r) * p.D
+                               : reinterpret_cast<T *>(p.ko) + (token * p.Hk + r - p.H) * p.D;
+        Raw<T, VEC>::store(out + l.a, a);
+        Raw<T, VEC>::store(out + l.b, b);
+      }
+      if (r < p.H && r + HS >= p.H) weight_of<VEC>(p.k_weight, l, wa, wb);
     }
   }
   if (!p.part) return;
@@ -308,26 +343,29 @@ __global__ __launch_bounds__(256) void qk_rope_bwd_kernel(QkRope p, int HS) {
   }
 }
 
-// Sums over the workgroups' parts in a fixed order: 64 channels a workgroup, sixteen
-// waves each taking every sixteenth part, eight parts in flight; added in fp64.
+// Sums over the workgroups' parts in a fixed order and fp64: 16 channels a workgroup, 64
+// lanes of a channel each taking every 64th part, eight of them in flight.
 __global__ __launch_bounds__(1024) void qk_rope_params_kernel(QkRope p, int blocks) {
-  __shared__ double red[16][64];
+  __shared__ double red[16][16];
   float *out = blockIdx.y ? p.dk_weight : p.dq_weight;
   if (!out) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  const int c = blockIdx.x * 16 + (threadIdx.x & 15), first = threadIdx.x >> 4;
   const float *src = p.part + (int64_t)blockIdx.y * p.D + min(c, p.D - 1);
   double s = 0.0;
-  for (int b = wave; b < blocks; b += 128) {
+  for (int b = first; b < blocks; b += 512) {
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = src[(int64_t)min(b + 16 * i, blocks - 1) * 2 * p.D];
+    for (int i = 0; i < 8; ++i) v[i] = src[(int64_t)min(b + 64 * i, blocks - 1) * 2 * p.D];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += b + 16 * i < blocks ? (double)v[i] : 0.0;
+    for (int i = 0; i < 8; ++i) s += b + 64 * i < blocks ? (double)v[i] : 0.0;
   }
-  red[wave][lane] = s;
+  s += __shfl_xor(s, 16);
+  s += __shfl_xor(s, 32);
+  if (lane < 16) red[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && c < p.D) {
+  if (threadIdx.x < 16 && c < p.D) {
+    s = red[0][lane];
     for (int w = 1; w < 16; ++w) s += red[w][lane];
     out[c] = (float)s;
   }
@@ -342,13 +380,15 @@ int group_of(const QkRope &p) {
   return gl;
 }
 
-// Groups that share a token: all of a workgroup's, halved while a group has fewer
-// than eight rows to form its angles for and the device stays full.
+// Groups that share a token: all of a workgroup's, halved while a group has fewer than
+// eight rows and the device stays full. b4 t4096 with 40 heads of 128 channels (a lane row
+// has 8 lanes, a workgroup 32 groups), forward and backward kernel: 4 groups a token 70 and
+// 109 us, 32 groups 155 and 211, 8 groups 74 and 117, 1 group 82 and 138. 64 tokens: 32
+// groups 7 us, 8 groups 10, 1 group 40.
 int heads_split(const QkRope &p, int groups) {
+  const int rows = p.H + p.Hk;
   int hs = groups;
-  while (hs > 1 && ((p.H + p.Hk) / hs < 4 || hs > p.H + p.Hk) &&
-         (p.tokens * (hs / 2) / groups >= 8 * device_cus() || hs / 2 >= p.H + p.Hk))
-    hs /= 2;
+  while (hs > 1 && rows < 8 * hs && (p.tokens * (hs / 2) / groups >= 8 * device_cus() || hs / 2 >= rows)) hs /= 2;
   return hs;
 }
 
@@ -364,12 +404,13 @@ int bwd_blocks(const QkRope &p) {
 template <typename T, int VEC, int GL>
 hipError_t launch_gl(const QkRope &p, bool bwd, hipStream_t st) {
   const int groups = 256 / GL, hs = heads_split(p, groups);
+  const unsigned lds = 2u * (groups / hs) * p.rot * sizeof(float);  // at most 32 KB: rot channels are a group's lanes' pairs
   if (bwd) {
-    hipLaunchKernelGGL((qk_rope_bwd_kernel<T, VEC, GL>), dim3(bwd_blocks(p)), dim3(256), 0, st, p, hs);
+    hipLaunchKernelGGL((qk_rope_bwd_kernel<T, VEC, GL>), dim3(bwd_blocks(p)), dim3(256), lds, st, p, hs);
   } else {
     const int64_t need = fwd_blocks(p, groups, hs), most = most_blocks(256);
     if (need == 0) return hipSuccess;
-    hipLaunchKernelGGL((qk_rope_fwd_kernel<T, VEC, GL>), dim3((unsigned)(need < most ? need : most)), dim3(256), 0, st, p, hs);
+    hipLaunchKernelGGL((qk_rope_fwd_kernel<T, VEC, GL>), dim3((unsigned)(need < most ? need : most)), dim3(256), lds, st, p, hs);
   }
   return hipGetLastError();
 }
@@ -403,7 +444,7 @@ hipError_t launch_qk_rope_fwd(const QkRope &p, hipStream_t st) { return launch_t
 hipError_t launch_qk_rope_bwd(const QkRope &p, hipStream_t st) {
   const hipError_t e = launch_types(p, true, st);
   if (e != hipSuccess || !p.part) return e;
-  hipLaunchKernelGGL(qk_rope_params_kernel, dim3((p.D + 63) / 64, 2), dim3(1024), 0, st, p, bwd_blocks(p));
+  hipLaunchKernelGGL(qk_rope_params_kernel, dim3((p.D + 15) / 16, 2), dim3(1024), 0, st, p, bwd_blocks(p));
   return hipGetLastError();
 }
 

@@ -11,7 +11,7 @@
  *
  * with positions on one to four axes (time, height and width of images and
  * video), every frequency i reading one of them. Angles and their reduction are
- * fp64 (an int32 position times an fp32 frequency is exact there), norms,
+ * fp64 (three roundings: an angle of 2^31 is off by less than 2^-22 turns), norms,
  * products and weights' gradients fp32 or wider; y is rounded once. It makes
  * the q and k rows of the attention operators: with norm L2 and rot 0 the l2
  * norm that kda_chunk_fwd and kda_delta_chunk_fwd expect. Conventions as in kda.h: device
