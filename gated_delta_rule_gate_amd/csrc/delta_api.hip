@@ -280,6 +280,7 @@ extern "C" kda_status kda_delta_chunk_bwd(const kda_delta_args *a, const void *q
   d.dv = dv;
   d.dg = dg;
   d.dbeta = dbeta;
+  d.from_zero = !h0;
   hipError_t e = kda::launch_delta_prep(p, st);
   if (e == hipSuccess) e = kda::launch_delta_walk(f, st);
   if (e == hipSuccess) e = kda::launch_delta_walk_rev(r, st);

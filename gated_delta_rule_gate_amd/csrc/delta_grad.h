@@ -37,7 +37,7 @@ template <typename T, int PT_>
 struct GradCfg {
   static constexpr bool F32 = sizeof(T) == 4;
   static constexpr int PT = PT_, IN = F32 ? 3 : 1, C = delta_chunk(PT, !F32), NC = C / 16, KS = C / 32;
-  static constexpr int HW = 64, NH = PT / HW;  // channels at a time, and how many times
+  static constexpr int HW = 64;  // channels at a time
   static constexpr int NWV = 4, THREADS = 64 * NWV;
   static constexpr int RPT = 8 * C / THREADS;  // rows of a slab of a thread
   static constexpr int NB = NC * (NC + 1) / 2, MB = (NB + NWV - 1) / NWV;
@@ -93,6 +93,7 @@ __global__ __launch_bounds__((GradCfg<T, PT>::THREADS), 2) void delta_grad_kerne
   struct Item {
     int64_t slot, lo;
     int h, L;
+    bool first;  // of its sequence
   };
   auto find = [&](int64_t at, Item &it) {  // the next item at or after `at` (a slot may hold no chunk)
     for (; at < items; at += gridDim.x) {
@@ -102,6 +103,7 @@ __global__ __launch_bounds__((GradCfg<T, PT>::THREADS), 2) void delta_grad_kerne
       it.h = (int)(at % p.H);
       it.lo = sg.lo;
       it.L = (int)(sg.hi - sg.lo);
+      it.first = sg.lo == sg.a;
       break;
     }
     return at;
@@ -172,7 +174,7 @@ __global__ __launch_bounds__((GradCfg<T, PT>::THREADS), 2) void delta_grad_kerne
 #pragma unroll
     for (int i = 0; i < NC; ++i) dot_a[i] = dot_f[i] = dot_w[i] = 0.f;
 
-    for (int half = 0; half < F::NH; ++half) {
+    for (int half = 0; half * F::HW < K; ++half) {  // (a part past K would have a negative count of columns)
       const int ch0 = half * F::HW;
       // the lane's offsets are made anew for every item: kept over the loop they would spill
       int own = tid;
@@ -220,7 +222,7 @@ __global__ __launch_bounds__((GradCfg<T, PT>::THREADS), 2) void delta_grad_kerne
         for (int x = 0; x < 2; ++x) s += (f.h[x][0] * f.d[x][0] + f.h[x][1] * f.d[x][1]) + (f.h[x][2] * f.d[x][2] + f.h[x][3] * f.d[x][3]);
         hd += (double)s;
         if (v0 + 32 < V) fetch(it, v0 + 32, ch0);
-        else if (half + 1 < F::NH) fetch(it, 0, ch0 + F::HW);
+        else if (ch0 + F::HW < K) fetch(it, 0, ch0 + F::HW);
         else if (next_at < items) fetch(next, 0, 0);
         __syncthreads();
         // ---- its products ----
@@ -438,7 +440,8 @@ __global__ __launch_bounds__((GradCfg<T, PT>::THREADS), 2) void delta_grad_kerne
       const double end = whole * (double)fast_exp2(tab[C - 1] + tab[64 + C - 1]) + through;
       if (lane < L) {
         const int64_t to = (it.lo + lane) * p.H + h;
-        if (p.dg) p.dg[to] = (float)((all - upto) + a + end);
+        // (the first decay of a sequence that starts from zero scales nothing: no remainder of the sums)
+        if (p.dg) p.dg[to] = it.first && p.from_zero && lane == 0 ? 0.f : (float)((all - upto) + a + end);
         p.dbeta[to] = sVec[lane] - w;
       }
       if (next_at < items) put_table(ng, nbeta);

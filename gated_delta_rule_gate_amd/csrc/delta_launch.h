@@ -98,6 +98,7 @@ struct DeltaGrad {
   bool qk_f32;
   void *dv;
   float *dg, *dbeta;
+  bool from_zero;         // no h0
   int B, T, H, K, V, N, Hk;
   float scale;
   bool is_bf16;

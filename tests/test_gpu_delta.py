@@ -597,3 +597,22 @@ def test_errors(shape, dtype):
         if got[name].dtype == BF16:  # one rounding, evenly spread over half a step: 1/sqrt(3) of the largest
             most += ref.HALF[BF16] / 3 ** 0.5
         assert off <= most, (name, off, most)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_first_decay_of_a_sequence_from_zero(dtype):
+    """It scales a state of zeros: its gradient is zero, not what rounding leaves of the sums. Decays of sequences
+    with a start state, and all later ones, have one."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import chunk_gated_delta_bwd
+
+    lens = [1, 70, 0, 1, 2]
+    d = make(1, sum(lens), 3, 3, 64, 64, dtype, lens=lens, states=False)
+    at = [0, 1, 71, 72]
+    dg = on(dev(d), chunk_gated_delta_bwd, dev(d)["do"])["dg"].cpu()
+    assert (dg[0, at] == 0).all()
+    rest = [i for i in range(sum(lens)) if i not in at]
+    assert (dg[0, rest] != 0).all()
+    d["h0"] = torch.ones(len(lens), 3, 64, 64)
+    dg = on(dev(d), chunk_gated_delta_bwd, dev(d)["do"])["dg"].cpu()
+    assert (dg[0, at] != 0).all()
