@@ -616,3 +616,48 @@ def test_first_decay_of_a_sequence_from_zero(dtype):
     d["h0"] = torch.ones(len(lens), 3, 64, 64)
     dg = on(dev(d), chunk_gated_delta_bwd, dev(d)["do"])["dg"].cpu()
     assert (dg[0, at] != 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("lens", [None, [100, 1500, 0, 400]], ids=["dense", "packed"])
+def test_long_heads_of_every_decay(lens, dtype):
+    """Heads side by side whose segments leave all of the state before them, some of it, nothing, and a head that
+    is reset here and there."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import chunk_gated_delta
+
+    d = make(1, 2000, 4, 2, 64, 72, dtype, lens, seed=81, strength=1.0)
+    d["g"] *= torch.tensor([0.0, 0.01, 3.0, 0.02])
+    d["g"][0, 333::500, 3] = -float("inf")
+    o, ht, inside = check_forward(d, chunk_gated_delta, None)
+    g = dev(d)
+    o2, h2 = on(g, chunk_gated_delta, final_state=g["h0"])
+    assert torch.equal(o2[:, inside], o[:, inside]) and torch.equal(h2, ht)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_long_rows_hold_up_the_decays(dtype):
+    """One key of norm 2 and beta 0.9: a step takes the state's part along it times 1 - 3.6, and decays of 1 / 2.6
+    leave it as it is for good, though they sum to far under what counts as zero.
+
+    Bound. Along the key a step's size is one, across it less, so roundings add up as with short rows; but a
+    written row is |k| |u|, |u| <= |v| + |k| M, and an entry of the chunk's inverse at most 3.6 instead of one:
+    sizes times 16."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import chunk_gated_delta
+
+    d = make(1, 1500, 2, 2, 8, 64, dtype, seed=82)
+    d["k"][:] = 0
+    d["k"][..., 3] = 2.0
+    d["q"][:] = 0
+    d["q"][..., 3] = 1.0
+    d["beta"][:] = 0.9
+    d["g"][:] = -float(np.log(2.6))
+    d["v"] *= 0.01  # so that the start still counts at the end
+    g = dev(d)
+    o, ht = on(g, chunk_gated_delta, output_final_state=True)
+    want, size = ref.delta(*inputs64(d)), ref.sizes(*inputs64(d))
+    assert want[1][0, :, 3].norm() > 0.2 * d["h0"][0, :, 3].norm()
+    n = ref.roundings(8, 64, 1500)
+    within(o, want[0], 16 * size[0], dtype, n, "o", ref.LEFT_OUT[dtype])
+    within(ht, want[1], 16 * size[1], FP32, n, "ht")
