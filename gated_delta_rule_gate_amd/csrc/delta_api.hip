@@ -173,7 +173,6 @@ extern "C" kda_status kda_delta_chunk_fwd(const kda_delta_args *a, const void *q
   }
   w.v = v;
   w.inv = static_cast<const char *>(workspace);
-  w.fold = true;
   w.s0 = h0;
   w.sT = ht;
   w.o = o;

@@ -40,7 +40,7 @@ struct DeltaWalk {
   const void *q, *k, *v;  // v: d_o in the gradient's walk
   const float *g, *beta;
   const int32_t *cu;
-  const char *inv;        // of every chunk; with o: times beta's diagonal
+  const char *inv;        // of every chunk; with o, and of a segment: times beta's diagonal
   const float *s0;        // [N, H, K, V] or null
   float *sT;              // [N, H, K, V] or null
   void *o;                // forward, or null: nothing but the state (and what is kept)
@@ -56,11 +56,9 @@ struct DeltaWalk {
   // the boundary behind it; a second chains them; then every segment is walked from its
   // boundary.
   int seg;
-  bool fold;              // inv is times beta's diagonal (with o it is)
   const float *bound;     // of every chunk (delta_prep.hip)
   float *seg_state;       // [boundary, H, K, V]
   float *seg_map;         // [boundary, H, K, K]
-  float *seg_map_t;       // transposed, or null
   int *seg_zero;          // [boundary, H]: whether the map is zero, and not written
   float *seg_first;       // copies of s0 where sT is s0 itself, [N, H, K, V], or null
 };
@@ -73,9 +71,8 @@ inline int64_t delta_walk_blocks(const DeltaWalk &p, int ncb) {
   const int64_t items = p.N + (p.seg ? ((int64_t)p.B * p.T) / p.seg : 0);
   return (items * p.Hk + 7) / 8 * 8 * (p.H / p.Hk) * ncb;
 }
-// The states at the boundaries from the segments' own, in place: forward S += M S of the
-// boundary before, in reverse (transposed maps) of the one behind.
-hipError_t launch_delta_chain(const DeltaWalk &p, bool rev, hipStream_t st);
+// The states at the boundaries from the segments' own, in place: S += M S of the boundary before.
+hipError_t launch_delta_chain(const DeltaWalk &p, hipStream_t st);
 bool delta_walk_fits(const DeltaWalk &p);
 hipError_t launch_delta_walk_bf16(const DeltaWalk &p, hipStream_t st);
 hipError_t launch_delta_walk_f32(const DeltaWalk &p, hipStream_t st);

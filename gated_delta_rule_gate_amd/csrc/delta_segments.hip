@@ -8,13 +8,15 @@ namespace kda {
 
 namespace {
 
-// The state at every boundary of a sequence from its segments' own, S_j = B_j + M_j S_{j-1}
-// (in reverse B_j + M_{j+1}^T S_{j+1}), in place. One workgroup takes a (sequence, head, 16
-// columns): its four waves share out the 16-row tiles, each an fp32-accurate product of
-// M's rows (three bf16 parts, split as they are loaded, the next boundary's in flight)
-// with the last state, which passes between the waves through LDS as operands.
+// The state at every boundary of a sequence from its segments' own, S_j = B_j + M_j S_{j-1},
+// in place. One workgroup takes a (sequence, head, 16 columns): its four waves share out the
+// 16-row tiles, each an fp32-accurate product of M's rows (three bf16 parts, split as they
+// are loaded, the next boundary's in flight) with the last state, which passes between the
+// waves through LDS as operands. A chain of short steps, about 3 us a boundary (1 x 32768
+// tokens, 16 heads: 48 us for 16 of them); the next boundary's state and M's parts formed
+// a boundary ahead as well took 49.
 template <int PT>
-__global__ __launch_bounds__(256) void delta_chain_kernel(DeltaWalk p, bool rev) {
+__global__ __launch_bounds__(256) void delta_chain_kernel(DeltaWalk p) {
   constexpr int NT = PT / 16, PS = PT / 32, TW = NT / 4;
   constexpr bool AHEAD = PT <= 128;  // 256 rows of M leave no registers for more
   __shared__ __align__(16) bf16_t sB[2][PS * 3 * 512];
@@ -25,16 +27,14 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaWalk p, bool rev)
   const int64_t nb = sr.len > 0 ? (sr.len - 1) / p.seg : 0;  // boundaries inside the sequence
   if (nb < 2) return;
   const int K = p.K, V = p.V, q = 16 * cb + l16;
-  const int64_t d = rev ? -1 : 1;
-  int64_t j = sr.t0 / p.seg + (rev ? nb : 1);
-  const float *const maps = rev ? p.seg_map_t : p.seg_map;
+  int64_t j = sr.t0 / p.seg + 1;
 
   // tiles 4 x + wave of this wave: rows state_channel(t, grp) + e; as the product's rows
   // a lane's is the one that lies at l16 there
   auto row_of = [&](int t) { return state_channel(t, l16 >> 2) + (l16 & 3); };
   f32x4_t m[TW][PS][2];
   auto fetch_map = [&](int64_t at) {
-    const auto rs = tile_rsrc(maps + (at * p.H + h) * K * K, (uint32_t)(K * K * 4));
+    const auto rs = tile_rsrc(p.seg_map + (at * p.H + h) * K * K, (uint32_t)(K * K * 4));
 #pragma unroll
     for (int x = 0; x < TW; ++x)
 #pragma unroll
@@ -65,21 +65,20 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaWalk p, bool rev)
     }
   };
   fetch_state(j);
-  // the map of the segment between boundaries j and j + d: left behind it, at the later one
-  auto map_to = [&](int64_t to) { return rev ? to + 1 : to; };
-  auto is_zero = [&](int64_t to) { return p.seg_zero[map_to(to) * p.H + h] != 0; };
-  bool zero = is_zero(j + d);
-  if (AHEAD && !zero) fetch_map(map_to(j + d));
+  // whether the map of the segment that ends at a boundary is zero
+  auto is_zero = [&](int64_t to) { return p.seg_zero[to * p.H + h] != 0; };
+  bool zero = is_zero(j + 1);
+  if (AHEAD && !zero) fetch_map(j + 1);
   hand_over(0);
   for (int64_t i = 1; i < nb; ++i) {
-    j += d;
+    ++j;
     const int buf = (int)(i - 1) & 1;
     fetch_state(j);
-    if (!AHEAD && !zero) fetch_map(map_to(j));
+    if (!AHEAD && !zero) fetch_map(j);
     __syncthreads();
-    const bool next_zero = i + 1 < nb && is_zero(j + d);
+    const bool next_zero = i + 1 < nb && is_zero(j + 1);
     if (zero) {  // the segment's own state is all there is
-      if (AHEAD && i + 1 < nb && !next_zero) fetch_map(map_to(j + d));
+      if (AHEAD && i + 1 < nb && !next_zero) fetch_map(j + 1);
       zero = next_zero;
       hand_over(buf ^ 1);
       continue;
@@ -97,7 +96,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaWalk p, bool rev)
         split_pair<3>(m[x][s][0], m[x][s][1], a);
         own[x] = mma_parts(a, b[s], own[x]);
       }
-    if (AHEAD && i + 1 < nb && !next_zero) fetch_map(map_to(j + d));
+    if (AHEAD && i + 1 < nb && !next_zero) fetch_map(j + 1);
     zero = next_zero;
     hand_over(buf ^ 1);
     const auto rs = tile_rsrc(state_at(j), (uint32_t)(K * V * 4));
@@ -115,13 +114,13 @@ int64_t chain_blocks(const DeltaWalk &p) { return (int64_t)p.N * p.H * ((p.V + 1
 
 }  // namespace
 
-hipError_t launch_delta_chain(const DeltaWalk &p, bool rev, hipStream_t st) {
+hipError_t launch_delta_chain(const DeltaWalk &p, hipStream_t st) {
   const int64_t grid = chain_blocks(p);
   if (grid > most_blocks(256)) return hipErrorInvalidValue;
   switch (linear_tile(p.K)) {
-    case 64: hipLaunchKernelGGL((delta_chain_kernel<64>), dim3((unsigned)grid), dim3(256), 0, st, p, rev); break;
-    case 128: hipLaunchKernelGGL((delta_chain_kernel<128>), dim3((unsigned)grid), dim3(256), 0, st, p, rev); break;
-    default: hipLaunchKernelGGL((delta_chain_kernel<256>), dim3((unsigned)grid), dim3(256), 0, st, p, rev); break;
+    case 64: hipLaunchKernelGGL((delta_chain_kernel<64>), dim3((unsigned)grid), dim3(256), 0, st, p); break;
+    case 128: hipLaunchKernelGGL((delta_chain_kernel<128>), dim3((unsigned)grid), dim3(256), 0, st, p); break;
+    default: hipLaunchKernelGGL((delta_chain_kernel<256>), dim3((unsigned)grid), dim3(256), 0, st, p); break;
   }
   return hipGetLastError();
 }

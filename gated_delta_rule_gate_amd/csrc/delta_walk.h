@@ -40,7 +40,7 @@ struct DeltaCfg {
   static constexpr unsigned nX = OUT ? 2u * IN * XPL : 0u, nZ = 2u * IN * XPL, rows = nX + nZ;
   static constexpr unsigned nT = InverseMove<C>::bytes;
   static constexpr unsigned nP = OUT ? NF * OPL * 1024u : 0u;  // scores, as pieces like the inverse's
-  static constexpr unsigned tab = 4u * (6 * 64 + 4);  // hi, lo, a scale, c, beta a (with o: a), beta; the chunk's decay
+  static constexpr unsigned tab = 4u * (6 * 64 + 4);  // hi, lo, a scale, c, a (with u kept: beta a, beta); the chunk's decay
   static constexpr unsigned oB = 2 * (nT + nP + tab);
   // two chunks of everything; one chunk's q and k rows where two do not fit
   static constexpr int NBUF = 2 * rows + oB <= 160 * 1024 ? 2 : 1;
@@ -53,7 +53,7 @@ __global__ __launch_bounds__(64 * (NW + 4)) __attribute__((amdgpu_waves_per_eu((
 void delta_walk_kernel(DeltaWalk p) {
   using F = DeltaCfg<T, PT, NW, OPL, MODE>;
   constexpr int C = F::C, NC = F::NC, KS = F::KS, IN = F::IN, QT = F::QT, NB = NC * (NC + 1) / 2;
-  constexpr bool OUT = F::OUT;
+  constexpr bool OUT = F::OUT, KEEP = MODE == kDeltaKeep;
   using MX = RowsMove<T, F::HT, C, PT>;
   extern __shared__ __align__(16) char smem[];
 
@@ -127,7 +127,7 @@ void delta_walk_kernel(DeltaWalk p) {
       MX::load(fz, zf, ldx, L, K, gx, rx);
       if (hw == DW) {
         if (p.g) fg = row_scalar(gf, lane, L, p.H);
-        if constexpr (!OUT) fb = row_scalar(bf, lane, L, p.H);
+        if constexpr (KEEP) fb = row_scalar(bf, lane, L, p.H);
       }
       xf += (int64_t)C * ldx;
       zf += (int64_t)C * ldx;
@@ -147,9 +147,8 @@ void delta_walk_kernel(DeltaWalk p) {
         t[64 + lane] = d.lo;
         t[128 + lane] = d.from * p.scale;
         t[192 + lane] = d.rest;
-        const float be = OUT || p.fold ? 1.f : fb;
-        t[256 + lane] = be * d.from;
-        if constexpr (!OUT) t[320 + lane] = be;
+        t[256 + lane] = KEEP ? fb * d.from : d.from;
+        if constexpr (KEEP) t[320 + lane] = fb;
         if (lane == 0) t[384] = d.all;
       }
       MI::template put<false>(ft, inverse_at(cc), hw, lane);
@@ -243,7 +242,7 @@ void delta_walk_kernel(DeltaWalk p) {
   const uint32_t gv = qin && !map ? (uint32_t)((4 * grp * ldv + wcol + l16) * SZ) : kOffNone;
   T *yc = reinterpret_cast<T *>(p.o) + vrow;
   const uint32_t gy = wcol + 4 * grp < ncol ? (uint32_t)((l16 * ldv + wcol + 4 * grp) * SZ) : kOffNone;
-  float *uc = MODE == kDeltaKeep ? p.rows_out + vrow : nullptr;
+  float *uc = KEEP ? p.rows_out + vrow : nullptr;
 
   ColumnRows<T, NC> fv;
   auto fetch_v = [&](int cc) {
@@ -290,7 +289,7 @@ void delta_walk_kernel(DeltaWalk p) {
     const bf16_t *const sX = rows_at(cc), *const sZ = sX + F::nX / 2, *const sT = inverse_at(cc);
     const float *const tab = tab_at(cc);
 
-    if constexpr (MODE == kDeltaKeep) {  // the state at the chunk's start
+    if constexpr (KEEP) {  // the state at the chunk's start
       const int64_t slot = delta_slot(p.N, n, sg.a, sg.lo + (int64_t)cc * C, C);
       store_state<F::NT>(p.states + (slot * p.H + h) * K * V, K, V, grp, q, S);
     }
@@ -338,7 +337,7 @@ void delta_walk_kernel(DeltaWalk p) {
       }
     }
 
-    // ---- u = T r, r = beta (v - a z) (with o, T has taken beta) ----
+    // ---- u = T r, r = beta (v - a z) (unless u is kept, T has taken beta) ----
     InverseTimes<C, false> ti;
     f32x4_t za[NC], u[NC];
     bf16x8_t rb[KS][3], uc3[KS][3];
@@ -354,7 +353,7 @@ void delta_walk_kernel(DeltaWalk p) {
       for (int half = 0; half < 2; ++half) {
         const int i = 2 * s + half;
         f32x4_t v = fv.get(i);
-        if constexpr (!OUT) v *= *reinterpret_cast<const f32x4_t *>(tab + 320 + 16 * i + 4 * grp);
+        if constexpr (KEEP) v *= *reinterpret_cast<const f32x4_t *>(tab + 320 + 16 * i + 4 * grp);
         r[half] = v - za[i] * z[i];
       }
       split_pair<3>(r[0], r[1], rb[s]);
@@ -371,7 +370,7 @@ void delta_walk_kernel(DeltaWalk p) {
 #pragma unroll
     for (int t = 0; t < F::NT; ++t) S[t] *= dec;
     if constexpr (KS > 1) ti.add(rb[KS - 1], u, KS - 1);
-    if constexpr (MODE == kDeltaKeep) {
+    if constexpr (KEEP) {
       const auto rs = tile_rsrc(uc, (uint32_t)(((L - 1) * ldv + ncol) * 4));
       uc += (int64_t)C * ldv;
       uint32_t off = qin ? (uint32_t)((4 * grp * ldv + wcol + l16) * 4) : kOffNone;
@@ -433,12 +432,6 @@ void delta_walk_kernel(DeltaWalk p) {
   if constexpr (MODE == kDeltaState) {
     const int64_t at = (int64_t)sg.out * p.H + h;
     store_state<F::NT>((map ? p.seg_map : p.seg_state) + at * K * V, K, V, grp, q, S);
-    if (map && p.seg_map_t && qin) {
-#pragma unroll
-      for (int t = 0; t < F::NT; ++t)
-        if (state_channel(t, grp) < K)
-          *reinterpret_cast<f32x4_t *>(p.seg_map_t + at * K * K + (int64_t)q * K + state_channel(t, grp)) = S[t];
-    }
   } else if (sg.out < 0) {
     if (p.sT && !(nch == 0 && p.sT == p.s0)) store_state<F::NT>(p.sT + sbase, K, V, grp, q, S);
   }
@@ -466,7 +459,7 @@ template <typename T, int PT, int NW, int OPL>
 hipError_t launch_delta_mode(const DeltaWalk &p, hipStream_t st) {
   if (p.seg) {
     hipError_t e = launch_delta_one<T, PT, NW, 1, kDeltaState>(p, st);
-    if (e == hipSuccess) e = launch_delta_chain(p, false, st);
+    if (e == hipSuccess) e = launch_delta_chain(p, st);
     if (e != hipSuccess) return e;
   }
   return p.o ? launch_delta_one<T, PT, NW, OPL, kDeltaOut>(p, st) : launch_delta_one<T, PT, NW, OPL, kDeltaKeep>(p, st);
