@@ -151,11 +151,12 @@ bool delta_walk_fits(const DeltaWalk &p) {
 // columns: 6.3 or 3.9 (4.8 or 3.1 alone on the device) with o, 0.8 of that in the state
 // pass, whose segments (all but a sequence's last) walk V and, but for the first, K
 // columns; two chunks for a segment's start and end; two more launches and a boundary's step of the chain 2.5 us. With decays most
-// maps are zero and not walked (delta_walk.h): an eighth is counted. How it chooses,
-// walks and chain together: 1 x 32768 tokens, 16 heads: 17 segments, 550 us (none: 1560);
-// 15872 tokens in 10 slots, 32 heads, segments of 12, 16, 20 (its choice), 24, 28, 32, 40,
-// 48 chunks, none: 578, 511, 472, 519, 562, 451, 498, 545, 497 us (steps of the slots'
-// own lengths); fp32, 2 x 1000 tokens, 8 heads: 4 segments, 65 us (none: 84).
+// maps are zero and not walked (delta_walk.h): an eighth is counted. (That states are then
+// walked from a segment's last chunks on only is not: the pass waits for the slowest head.)
+// How it chooses, all kernels together: 1 x 32768 tokens, 16 heads: 17 segments, 500 us
+// (none: 1560); 15872 tokens in 10 slots, 32 heads, segments of 10, 13, 16, 20 (its
+// choice), 24, 30 chunks: 555, 536, 483, 495, 468, 503 us (steps of the slots' own
+// lengths; none: 540); fp32, 2 x 1000 tokens, 8 heads: 4 segments, 65 us (none: 84).
 int delta_segment(const DeltaWalk &p, bool packed, bool gated) {
   const int C = delta_chunk(linear_tile(p.K), p.is_bf16);
   const double room = device_cus(), maps = gated ? 0.12 : 1.0;

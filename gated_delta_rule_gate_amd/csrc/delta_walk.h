@@ -58,9 +58,10 @@ void delta_walk_kernel(DeltaWalk p) {
   extern __shared__ __align__(16) char smem[];
 
   // Workgroups that read the same q/k rows go to one XCD, next to each other; whole
-  // segments come before the sequences' first, which may be short. Maps come before all
-  // states, a head's dealt over the XCDs: most are not walked and end at once, while those
-  // that are would else start behind a round of states, or on one XCD.
+  // segments come before the sequences' first, which may be short. Of a state pass, maps
+  // come before all states, and a head's segments are dealt over the XCDs: most maps are
+  // not walked and most states only from a segment's last chunks on, while those of a head
+  // that decays slowly would else start behind a round of others, or on one XCD.
   const int G = p.H / p.Hk, nvb = (p.V + QT - 1) / QT;
   const int64_t n_items = p.N + (p.seg ? ((int64_t)p.B * p.T) / p.seg : 0);
   const int64_t maps = MODE == kDeltaState ? (n_items * p.Hk + 7) / 8 * 8 * G * ((p.K + QT - 1) / QT) : 0;  // workgroups
@@ -70,24 +71,41 @@ void delta_walk_kernel(DeltaWalk p) {
   const int64_t unit = (block >> 3) / U * 8 + (block & 7);
   const int member = (int)((block >> 3) % U);
   const int64_t item = n_items - 1 - unit / p.Hk;
-  const int hk = (int)((map ? unit + item : unit) % p.Hk), h = hk * G + member / ncb, cb = member % ncb;
+  const int hk = (int)((MODE == kDeltaState ? unit + item : unit) % p.Hk), h = hk * G + member / ncb, cb = member % ncb;
   SegLoc sg;
   if (item < 0 || !locate_part(p, item, p.seg, sg)) return;
   if (MODE == kDeltaState && sg.out < 0) return;  // nothing follows the last segment
   if (map && sg.in < 0) return;                   // a first segment starts from its own state
-  const int n = sg.n, len = (int)(sg.hi - sg.lo);
-  if (map) {
-    // A map whose decays leave nothing (under 2^-160, the chunks' bounds summed) is zero:
-    // most heads of a gated model over a few thousand tokens.
-    float b = 0.f;
-    for (int c = threadIdx.x & 63; c < len / C; c += 64)
-      b += p.bound[delta_slot(p.N, n, sg.a, sg.lo + (int64_t)c * C, C) * p.H + h];
+  const int n = sg.n;
+  int skip = 0;
+  if constexpr (MODE == kDeltaState) {
+    // What lies before a chunk from which on the decays leave nothing (under 2^-160, the
+    // chunks' bounds summed) does not reach the segment's end: its state is walked from
+    // there on, and its map is zero. So it is for most heads of a gated model over a few
+    // thousand tokens.
+    const int ln = threadIdx.x & 63, chunks = (int)(sg.hi - sg.lo) / C;
+    float behind = 0.f;
+    for (int base = (chunks - 1) / 64 * 64; base >= 0 && skip == 0; base -= 64) {
+      const int c = base + ln;
+      float b = c < chunks ? p.bound[delta_slot(p.N, n, sg.a, sg.lo + (int64_t)c * C, C) * p.H + h] : 0.f;
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) b += __shfl_xor(b, off);
-    const bool zero = b <= -160.f;
-    if (cb == 0 && threadIdx.x == 0) p.seg_zero[(int64_t)sg.out * p.H + h] = zero;
-    if (zero) return;
+      for (int off = 1; off < 64; off <<= 1) {  // of this chunk and those behind it
+        const float x = __shfl_down(b, off);
+        b += ln + off < 64 ? x : 0.f;
+      }
+      b += behind;
+      const unsigned long long none = __ballot(c < chunks && b <= -160.f);
+      if (none) skip = base + 64 - __clzll(none);  // one past the last such chunk's place
+      behind = __shfl(b, 0);
+    }
+    if (map) {
+      if (cb == 0 && threadIdx.x == 0) p.seg_zero[(int64_t)sg.out * p.H + h] = skip > 0;
+      if (skip) return;
+    } else if (skip) {
+      sg.lo += (int64_t)(skip - 1) * C;
+    }
   }
+  const int len = (int)(sg.hi - sg.lo);
 
   const int tid = threadIdx.x, lane = tid & 63, wave = wave_id();
   const int grp = lane >> 4, l16 = lane & 15;
@@ -232,6 +250,10 @@ void delta_walk_kernel(DeltaWalk p) {
         for (int e = 0; e < 4; ++e) S[t][e] = state_channel(t, grp) + e == q ? 1.f : 0.f;
     }
     if (MODE == kDeltaState && sg.in < 0 && p.seg_first) store_state<F::NT>(p.seg_first + sbase, K, V, grp, q, S);
+    if (skip) {
+#pragma unroll
+      for (int t = 0; t < F::NT; ++t) S[t] = zero4();
+    }
   }
 
   const int ax = l16 * F::LDX + 8 * grp;  // a row of q or k as an operand
