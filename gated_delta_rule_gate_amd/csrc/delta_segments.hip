@@ -145,7 +145,6 @@ bool delta_walk_fits(const DeltaWalk &p) {
   return delta_walk_blocks(p, ncb) <= most_blocks(64 * (qt / 16 + 4)) && (!p.seg || chain_blocks(p) <= most_blocks(256));
 }
 
-
 // Segments pay where whole sequences leave compute units idle or wait for the longest.
 // Costs in microseconds a chunk and workgroup as measured for bf16, 128 x 128, by 128 or 64
 // columns: 6.3 or 3.9 (4.8 or 3.1 alone on the device) with o, 0.8 of that in the state
@@ -153,10 +152,10 @@ bool delta_walk_fits(const DeltaWalk &p) {
 // columns; two chunks for a segment's start and end; two more launches and a boundary's step of the chain 2.5 us. With decays most
 // maps are zero and not walked (delta_walk.h): an eighth is counted. (That states are then
 // walked from a segment's last chunks on only is not: the pass waits for the slowest head.)
-// How it chooses, all kernels together: 1 x 32768 tokens, 16 heads: 17 segments, 500 us
+// How it chooses, walks and chain together: 1 x 32768 tokens, 16 heads: 17 segments, 420 us
 // (none: 1560); 15872 tokens in 10 slots, 32 heads, segments of 10, 13, 16, 20 (its
-// choice), 24, 30 chunks: 555, 536, 483, 495, 468, 503 us (steps of the slots' own
-// lengths; none: 540); fp32, 2 x 1000 tokens, 8 heads: 4 segments, 65 us (none: 84).
+// choice), 24, 30 chunks: 504, 485, 432, 444, 417, 452 us (steps of the slots' own
+// lengths; none: 497); fp32, 2 x 1000 tokens, 8 heads: 4 segments, 65 us (none: 84).
 int delta_segment(const DeltaWalk &p, bool packed, bool gated) {
   const int C = delta_chunk(linear_tile(p.K), p.is_bf16);
   const double room = device_cus(), maps = gated ? 0.12 : 1.0;

@@ -16,6 +16,12 @@
 // Arithmetic as in linear_walk.h: products on the bf16 matrix cores, an fp32
 // operand as a sum of bf16 parts. What reaches the state takes three parts (24
 // bits); the scores and what multiplies them in o take OPL.
+//
+// Bound by the chain of a chunk's steps, which one or two state waves a SIMD hide little of
+// (matrix cores busy 47% of the time, vector units 45%): a chunk of 128 x 128 takes 6.3 us
+// with every compute unit at work, at a clock that falls under this load, 4.8 us alone.
+// b4 t4096 h64 d128: 400 to 415 us (the case's bytes take 215), in two periods a chunk with
+// two barriers 497; u and states kept, b4 t2048 h32 d128: 135 to 140 us for 700 MB.
 #pragma once
 
 #include "delta_chunk.h"

@@ -37,6 +37,7 @@
  *     makes outputs of its (sequence, head) non-finite, from the start of the
  *     64-token chunk that holds it (the backward: throughout the sequence), and
  *     no other sequence's or head's, but for dq and dk of a shared q/k head.
+ *     Behind tokens whose decays together are under 2^-160 they may be finite again.
  *   - With T == 0 the per-token tensors may be NULL and every final state is
  *     its h0.
  */
@@ -80,7 +81,9 @@ kda_status kda_delta_chunk_fwd(const kda_delta_args *args, const void *q, const 
 
 /* Bytes of device workspace that kda_delta_chunk_bwd needs (0 when the arguments are invalid or
  * there are no tokens). It holds the state at the start and its gradient at the end of every
- * chunk: 8 K V bytes a chunk and head, and 8 V bytes a token and head. */
+ * chunk (64 tokens; 32 of fp32 inputs or with K over 128), 8 K V bytes a chunk and head, 8 V
+ * bytes a token and head, the chunks' inverses (10 KB a chunk and head; of 32 tokens 3 KB) and,
+ * where value heads share q/k heads, 8 K bytes a token and value head. */
 size_t kda_delta_chunk_bwd_workspace_bytes(const kda_delta_args *args);
 
 /*
