@@ -155,7 +155,7 @@ bool delta_walk_fits(const DeltaWalk &p) {
 // How it chooses, walks and chain together: 1 x 32768 tokens, 16 heads: 17 segments, 420 us
 // (none: 1560); 15872 tokens in 10 slots, 32 heads, segments of 10, 13, 16, 20 (its
 // choice), 24, 30 chunks: 504, 485, 432, 444, 417, 452 us (steps of the slots' own
-// lengths; none: 497); fp32, 2 x 1000 tokens, 8 heads: 4 segments, 65 us (none: 84).
+// lengths; none: 497); fp32, 2 x 1000 tokens, 8 heads: 7 segments, 58 us (none: 84).
 int delta_segment(const DeltaWalk &p, bool packed, bool gated) {
   const int C = delta_chunk(linear_tile(p.K), p.is_bf16);
   const double room = device_cus(), maps = gated ? 0.12 : 1.0;

@@ -54,8 +54,10 @@ struct DeltaCfg {
   static_assert(total <= 160 * 1024, "LDS");
 };
 
+// One workgroup a compute unit, with all its registers; but a state pass by 64 columns,
+// which needs fewer, may share one (fp32, 2 x 1000 tokens, 8 heads of 72 x 40: 24 us for 31).
 template <typename T, int PT, int NW, int OPL, int MODE>
-__global__ __launch_bounds__(64 * (NW + 4)) __attribute__((amdgpu_waves_per_eu((NW + 7) / 4, (NW + 7) / 4)))
+__global__ __launch_bounds__(64 * (NW + 4)) __attribute__((amdgpu_waves_per_eu((NW + 7) / 4, MODE == kDeltaState && NW == 4 ? 4 : (NW + 7) / 4)))
 void delta_walk_kernel(DeltaWalk p) {
   using F = DeltaCfg<T, PT, NW, OPL, MODE>;
   constexpr int C = F::C, NC = F::NC, KS = F::KS, IN = F::IN, QT = F::QT, NB = NC * (NC + 1) / 2;
