@@ -661,3 +661,24 @@ def test_long_rows_hold_up_the_decays(dtype):
     n = ref.roundings(8, 64, 1500)
     within(o, want[0], 16 * size[0], dtype, n, "o", ref.LEFT_OUT[dtype])
     within(ht, want[1], 16 * size[1], FP32, n, "ht")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("K", [8, 72, 136, 192, 200, 256])
+def test_chunks_of_one_row(K, dtype):
+    """Every width of key rows with a last chunk of one token, alone in its sequence or not."""
+    need_gpu()
+    from gated_delta_rule_gate_amd import chunk_gated_delta
+
+    d = make(1, 98, 2, 1, K, 24, dtype, lens=[65, 33], seed=83)
+    check_forward(d, chunk_gated_delta, None)
+    check_backward(d)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_long_backward(dtype):
+    """Many chunks, on heads that forget nothing, a little, and all of it."""
+    need_gpu()
+    d = make(1, 1100, 3, 3, 64, 40, dtype, seed=84, strength=1.0)
+    d["g"] *= torch.tensor([0.0, 0.01, 3.0])
+    check_backward(d)
