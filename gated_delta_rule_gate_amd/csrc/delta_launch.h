@@ -21,7 +21,7 @@ inline __host__ __device__ int64_t delta_slots(int64_t rows, int N, int chunk) {
 // diagonal, row by row of blocks, fp32; lane l of a block has row l % 16, columns 4 (l /
 // 16).. of it. In LDS the walks hold 16 x 32 pieces in bf16 parts.
 inline __host__ __device__ constexpr int delta_frags(int chunk) { return chunk == 64 ? 6 : 2; }
-inline __host__ __device__ constexpr int64_t delta_inverse_bytes(int chunk) { return chunk == 64 ? 10240 : 3072; }
+inline __host__ __device__ constexpr int64_t delta_inverse_bytes(int chunk) { return (chunk == 64 ? 10 : 3) * 1024; }
 
 struct DeltaPrep {
   const void *k;
