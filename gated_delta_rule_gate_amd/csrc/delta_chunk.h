@@ -229,6 +229,14 @@ __device__ __forceinline__ void store_state(float *dst, int K, int V, int grp, i
     for (int e = 0; e < 4; ++e)
       __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[t][e]), rs, (int)(off + (state_channel(t, 0) + e) * V * 4), 0, 0);
 }
+// Two tiles of it.
+__device__ __forceinline__ void store_tiles(const __amdgpu_buffer_rsrc_t &rs, int K, int V, int grp, int q, int t, const f32x4_t &a, const f32x4_t &b) {
+  uint32_t off = q < V ? (uint32_t)((8 * grp * V + q) * 4) : kOffNone;
+  asm volatile("" : "+v"(off));
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(e < 4 ? a[e & 3] : b[e & 3]), rs, (int)(off + (16 * t + e) * V * 4), 0, 0);
+}
 
 // A chunk's rows of one [rows, heads, V] tensor in the layout of accumulators: of this
 // lane's column, rows 16 i + 4 grp + e; rows past the chunk and columns past V are zero.

@@ -11,10 +11,12 @@
 // needed at its start, so a chunk has two periods: its rows are put to LDS in the first
 // of the chunk before, its scores formed in the second.
 //
-// Bound by the chain of a chunk's steps, as the forward walk: b4 t2048 h32 d128 161 to
-// 172 us (600 MB). With the helpers ahead of the state waves in priority, which the forward
-// walk's like, it takes 226; with d_o, scores and inverse handed over through single
-// buffers in LDS 204.
+// Bound by the chain of a chunk's steps, as the forward walk: b4 t2048 h32 d128 155 to
+// 168 us (600 MB). D leaves tile by tile as it is done: stored whole at a chunk's start it
+// takes 173 to 177. With the helpers ahead of the state waves in priority, which the forward
+// walk's like, it took 226; with d_o, scores and inverse handed over through single buffers
+// in LDS 204; with three chunks of rows and one barrier a chunk, where they fit, packed t4999
+// by 64 channels 81 for 83 us and registers spilled at other widths.
 #pragma once
 
 #include "delta_chunk.h"
@@ -197,7 +199,13 @@ void delta_rev_kernel(DeltaWalk p) {
   auto fetch_o = [&](int cc) {
     fo.load(tile_rsrc(oc + start_of(cc) * ldv, (uint32_t)(((rows_of(cc) - 1) * ldv + ncol) * SZ)), go, ldv);
   };
-  if (nch > 0) fetch_o(0);
+  auto states_at = [&](int cc) {  // behind chunk cc of the walk
+    return p.states + (delta_slot(p.N, n, sr.t0, sr.t0 + start_of(cc), C) * p.H + h) * K * V;
+  };
+  if (nch > 0) {
+    store_state<F::NT>(states_at(0), K, V, grp, q, S);
+    fetch_o(0);
+  }
   __syncthreads();
   __syncthreads();
   __syncthreads();
@@ -206,7 +214,6 @@ void delta_rev_kernel(DeltaWalk p) {
     const int64_t t0 = start_of(cc);
     const bf16_t *const sX = rows_at(cc), *const sZ = sX + F::nX / 2, *const sT = inverse_at(cc), *const sP = scores_at(cc);
     const float *const tab = tab_at(cc);
-    store_state<F::NT>(p.states + (delta_slot(p.N, n, sr.t0, sr.t0 + t0, C) * p.H + h) * K * V, K, V, grp, q, S);
 
     // as in the forward walk, what LDS has is asked for before its use and the order pinned
     bf16x8_t kf[NC][IN], sb[2][3];
@@ -330,12 +337,15 @@ void delta_rev_kernel(DeltaWalk p) {
           __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(u[i][e]), rs, (int)(off + (16 * i + e) * ldv * 4), 0, 0);
     }
     if constexpr (F::NBUF == 2) __syncthreads();
-    // ---- the state's gradient ----
+    // ---- the state's gradient, which leaves for the next chunk as it is done ----
+    const auto rs_next = tile_rsrc(cc + 1 < nch ? states_at(cc + 1) : nullptr, cc + 1 < nch ? (uint32_t)(K * V * 4) : 0u);
 #pragma unroll
     for (int t = 0; t < F::NT; t += 2) {
       add_channels(wu, t);
       if (t + 2 < F::NT) read_channels(sZ, t + 2);
+      if (t > 0) store_tiles(rs_next, K, V, grp, q, t - 2, S[t - 2], S[t - 1]);
     }
+    store_tiles(rs_next, K, V, grp, q, F::NT - 2, S[F::NT - 2], S[F::NT - 1]);
     pin();
     if constexpr (F::NBUF == 1) {
       __syncthreads();  // q and k are done with
