@@ -141,10 +141,6 @@ struct InverseMove {
 #pragma unroll
     for (int it = 0; it < IT; ++it) buf[it] = tile_load16(rs, (uint32_t)((it * 256 + ht) * 16));
   }
-  // once: the halves of pieces beyond the triangle, which no block fills
-  static __device__ __forceinline__ void clear(bf16_t *s, int ht) {
-    for (int i = ht; i < (int)(bytes / 4); i += 256) reinterpret_cast<unsigned *>(s)[i] = 0u;
-  }
   template <bool TR>
   static __device__ __forceinline__ void put(const u32x4_t (&buf)[IT], bf16_t *s, int hw, int lane) {
 #pragma unroll
