@@ -13,9 +13,11 @@
 // one barrier a chunk hands over q, k, T and scores, which four helper waves bring and
 // form a chunk ahead; a chunk's scores meet its u in the next one's time.
 //
-// Arithmetic as in linear_walk.h: products on the bf16 matrix cores, an fp32
-// operand as a sum of bf16 parts. What reaches the state takes three parts (24
-// bits); the scores and what multiplies them in o take OPL.
+// Products on the bf16 matrix cores, an fp32 operand as a sum of three bf16 parts (24
+// bits), of whose products with those of another the ones of at most 2^-24 are left out. So with o
+// of bf16 inputs too: with two parts in the state's copy, the scores and u (16 bits), 0.3%
+// of its values were rounded to the neighbour of the nearest bf16 value, in place of 0.01%,
+// for 4 to 8% of the time (b4 t4096 h64 d128: 40 us).
 //
 // Bound by the chain of a chunk's steps, which one or two state waves a SIMD hide little of
 // (matrix cores busy 47% of the time, vector units 45%): a chunk of 128 x 128 takes 6.3 us
@@ -34,10 +36,10 @@ namespace {
 // state, or the map, left at the boundary behind it.
 enum DeltaMode : int { kDeltaOut = 0, kDeltaKeep = 1, kDeltaState = 2 };
 
-template <typename T, int PT_, int NW_, int OPL_, int MODE_>
+template <typename T, int PT_, int NW_, int MODE_>
 struct DeltaCfg {
   static constexpr bool F32 = sizeof(T) == 4;
-  static constexpr int PT = PT_, NW = NW_, OPL = OPL_, MODE = MODE_;
+  static constexpr int PT = PT_, NW = NW_, MODE = MODE_;
   static constexpr int IN = F32 ? 3 : 1, C = delta_chunk(PT, !F32);
   static constexpr int NC = C / 16, KS = C / 32, PS = PT / 32, NT = PT / 16, QT = 16 * NW, NF = delta_frags(C);
   static constexpr int HELPERS = 4, THREADS = 64 * (NW + HELPERS), HT = 64 * HELPERS;
@@ -45,7 +47,7 @@ struct DeltaCfg {
   static constexpr bool OUT = MODE == kDeltaOut;
   static constexpr unsigned nX = OUT ? 2u * IN * XPL : 0u, nZ = 2u * IN * XPL, rows = nX + nZ;
   static constexpr unsigned nT = InverseMove<C>::bytes;
-  static constexpr unsigned nP = OUT ? NF * OPL * 1024u : 0u;  // scores, as pieces like the inverse's
+  static constexpr unsigned nP = OUT ? NF * 3 * 1024u : 0u;  // scores, as pieces like the inverse's
   static constexpr unsigned tab = 4u * (6 * 64 + 4);  // hi, lo, a scale, c, a (with u kept: beta a, beta); the chunk's decay
   static constexpr unsigned oB = 2 * (nT + nP + tab);
   // two chunks of everything; one chunk's q and k rows where two do not fit
@@ -56,10 +58,10 @@ struct DeltaCfg {
 
 // One workgroup a compute unit, with all its registers; but a state pass by 64 columns,
 // which needs fewer, may share one (fp32, 2 x 1000 tokens, 8 heads of 72 x 40: 24 us for 31).
-template <typename T, int PT, int NW, int OPL, int MODE>
+template <typename T, int PT, int NW, int MODE>
 __global__ __launch_bounds__(64 * (NW + 4)) __attribute__((amdgpu_waves_per_eu((NW + 7) / 4, MODE == kDeltaState && NW == 4 ? 4 : (NW + 7) / 4)))
 void delta_walk_kernel(DeltaWalk p) {
-  using F = DeltaCfg<T, PT, NW, OPL, MODE>;
+  using F = DeltaCfg<T, PT, NW, MODE>;
   constexpr int C = F::C, NC = F::NC, KS = F::KS, IN = F::IN, QT = F::QT, NB = NC * (NC + 1) / 2;
   constexpr bool OUT = F::OUT, KEEP = MODE == kDeltaKeep;
   using MX = RowsMove<T, F::HT, C, PT>;
@@ -212,7 +214,7 @@ void delta_walk_kernel(DeltaWalk p) {
             v[e] = keep ? acc[e] * (fast_exp2((hr - hs[e]) + (lr - ls[e])) * p.scale) : 0.f;
           }
           const int f = C == 32 ? i : (i < 2 ? i : 2 * i - 2 + (j >> 1));
-          put_parts<OPL>(v, sP + (f * OPL * 64 + lane) * 8 + 4 * (j & 1), 512);
+          put_parts<3>(v, sP + (f * 192 + lane) * 8 + 4 * (j & 1), 512);
         }
       }
     };
@@ -280,7 +282,7 @@ void delta_walk_kernel(DeltaWalk p) {
     vc += (int64_t)C * ldv;
   };
   f32x4_t y[OUT ? NC : 1];
-  bf16x8_t ub[KS][OPL];
+  bf16x8_t ub[KS][3];
   // o of chunk cc: y, which holds 2^b q S by then, and its scores times u; a lane has
   // four neighbouring columns of row l16 of each tile
   auto finish = [&](int cc) {
@@ -290,9 +292,9 @@ void delta_walk_kernel(DeltaWalk p) {
 #pragma unroll
       for (int i = 0; i < NC; ++i)
         if (s <= i / 2) {
-          bf16x8_t a[OPL];
+          bf16x8_t a[3];
 #pragma unroll
-          for (int pl = 0; pl < OPL; ++pl) a[pl] = row_frag(sP + ((frag_index<C>(i, s, false) * OPL + pl) * 64 + lane) * 8);
+          for (int pl = 0; pl < 3; ++pl) a[pl] = row_frag(sP + ((frag_index<C>(i, s, false) * 3 + pl) * 64 + lane) * 8);
           y[i] = mma_parts(ub[s], a, y[i]);
         }
   };
@@ -359,10 +361,7 @@ void delta_walk_kernel(DeltaWalk p) {
       if (s + 1 < F::PS) read_rows(kf, sZ, s + 1);
       if constexpr (OUT) {
         if (s + 1 < F::PS) split_state(s + 1);
-        bf16x8_t so[OPL];
-#pragma unroll
-        for (int pl = 0; pl < OPL; ++pl) so[pl] = sb[s & 1][pl];
-        mma_rows<NC>(so, qf, y);
+        mma_rows<NC>(sb[s & 1], qf, y);
         pin();
       }
     }
@@ -428,7 +427,7 @@ void delta_walk_kernel(DeltaWalk p) {
     for (int s = 0; s < KS; ++s) {
       const f32x4_t c0 = *reinterpret_cast<const f32x4_t *>(tab + 192 + 32 * s + 4 * grp);
       const f32x4_t c1 = *reinterpret_cast<const f32x4_t *>(tab + 192 + 32 * s + 16 + 4 * grp);
-      if constexpr (OUT) split_pair<OPL>(u[2 * s], u[2 * s + 1], ub[s]);
+      if constexpr (OUT) split_pair<3>(u[2 * s], u[2 * s + 1], ub[s]);
       split_pair<3>(u[2 * s] * c0, u[2 * s + 1] * c1, uc3[s]);
     }
     pin();
@@ -467,10 +466,10 @@ void delta_walk_kernel(DeltaWalk p) {
   }
 }
 
-template <typename T, int PT, int NW, int OPL, int MODE>
+template <typename T, int PT, int NW, int MODE>
 hipError_t launch_delta_one(const DeltaWalk &p, hipStream_t st) {
-  using F = DeltaCfg<T, PT, NW, OPL, MODE>;
-  auto kern = delta_walk_kernel<T, PT, NW, OPL, MODE>;
+  using F = DeltaCfg<T, PT, NW, MODE>;
+  auto kern = delta_walk_kernel<T, PT, NW, MODE>;
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kern), hipFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)F::total);
   if (e != hipSuccess) {
@@ -485,32 +484,32 @@ hipError_t launch_delta_one(const DeltaWalk &p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <typename T, int PT, int NW, int OPL>
+template <typename T, int PT, int NW>
 hipError_t launch_delta_mode(const DeltaWalk &p, hipStream_t st) {
   if (p.seg) {
-    hipError_t e = launch_delta_one<T, PT, NW, 1, kDeltaState>(p, st);
+    hipError_t e = launch_delta_one<T, PT, NW, kDeltaState>(p, st);
     if (e == hipSuccess) e = launch_delta_chain(p, st);
     if (e != hipSuccess) return e;
   }
-  return p.o ? launch_delta_one<T, PT, NW, OPL, kDeltaOut>(p, st) : launch_delta_one<T, PT, NW, OPL, kDeltaKeep>(p, st);
+  return p.o ? launch_delta_one<T, PT, NW, kDeltaOut>(p, st) : launch_delta_one<T, PT, NW, kDeltaKeep>(p, st);
 }
 
-template <typename T, int PT, int OPL>
+template <typename T, int PT>
 hipError_t launch_delta_cols(const DeltaWalk &p, hipStream_t st) {
   int ncb;
   const int cols = delta_cols(p, &ncb);
   if constexpr (sizeof(T) == 2) {
-    if (cols == 128) return launch_delta_mode<T, PT, 8, OPL>(p, st);
+    if (cols == 128) return launch_delta_mode<T, PT, 8>(p, st);
   }
-  return launch_delta_mode<T, PT, 4, OPL>(p, st);
+  return launch_delta_mode<T, PT, 4>(p, st);
 }
 
-template <typename T, int OPL>
+template <typename T>
 hipError_t launch_delta_width(const DeltaWalk &p, hipStream_t st) {
   switch (linear_tile(p.K)) {
-    case 64: return launch_delta_cols<T, 64, OPL>(p, st);
-    case 128: return launch_delta_cols<T, 128, OPL>(p, st);
-    default: return launch_delta_cols<T, 256, OPL>(p, st);
+    case 64: return launch_delta_cols<T, 64>(p, st);
+    case 128: return launch_delta_cols<T, 128>(p, st);
+    default: return launch_delta_cols<T, 256>(p, st);
   }
 }
 

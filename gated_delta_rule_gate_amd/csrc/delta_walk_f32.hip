@@ -3,6 +3,6 @@
 
 namespace kda {
 
-hipError_t launch_delta_walk_f32(const DeltaWalk &p, hipStream_t st) { return launch_delta_width<float, 3>(p, st); }
+hipError_t launch_delta_walk_f32(const DeltaWalk &p, hipStream_t st) { return launch_delta_width<float>(p, st); }
 
 }  // namespace kda
