@@ -3,9 +3,10 @@ a lost term cannot pass."""
 import pytest
 import torch
 
+import delta_norms as norms
 import delta_ref as ref
 from kda_testlib import need_gpu
-from test_gpu_delta import BF16, FP32, IN, _id, dev, f64, inputs64, make, on
+from test_gpu_delta import BF16, FP32, IN, SHAPES, _id, dev, f64, inputs64, make, on
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +34,67 @@ def test_bf16_outputs_round_an_fp32_result(shape):
     wrong, wrong32 = (int((x.cpu() != want).sum()) for x in (o, o32))
     print("of %d outputs %d, fp32 rounded %d" % (want.numel(), wrong, wrong32))
     assert wrong <= 3 * wrong32 + 5 * (3 * wrong32) ** 0.5 + 5
+
+
+def check_norms(d, backward=True):
+    """Every result's error, in the 2-norm of each sequence and head, below delta_norms.bounds."""
+    from gated_delta_rule_gate_amd import chunk_gated_delta, chunk_gated_delta_bwd
+
+    B, T = d["q"].shape[:2]
+    g, cu, end = dev(d), d["cu"], T if d["cu"] is None else int(d["cu"][-1])
+    o, ht = on(g, chunk_gated_delta, output_final_state=True)
+    got, do, dht = dict(o=o, ht=ht), None, f64(d["dht"])
+    if backward:
+        got.update(on(g, chunk_gated_delta_bwd, g["do"], dht=g["dht"]))
+        do = f64(d["do"]).clone()
+        do[:, end:] = 0
+        want = norms.reference(inputs64(d), do, dht, cu=cu)
+    else:
+        want = dict(zip(norms.NAMES, ref.delta(*inputs64(d), cu=cu)))
+    bound = norms.bounds(*inputs64(d), cu=cu, do=do, dht=dht)
+    for name in norms.NAMES if backward else norms.NAMES[:2]:
+        if name == "dg" and d["g"] is None:
+            continue
+        states = name in ("ht", "dh0")
+        over, most = norms.exceeded(got[name], want[name], bound[name], B, T, cu, states=states)
+        print("%s %.2f of %.0e" % (name, over, most), end=" ")
+        assert over <= 1.0, (name, over, most)
+
+
+@pytest.mark.parametrize("decay", [True, False], ids=["decay", "plain"])
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=_id)
+def test_norms(shape, dtype, decay):
+    need_gpu()
+    check_norms(make(*shape[:6], dtype, shape[6], states=shape[1] != 97, seed=91, decay=decay))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("K", [8, 72, 136, 192, 200, 256])
+def test_norms_of_chunks_of_one_row(K, dtype):
+    need_gpu()
+    check_norms(make(1, 98, 2, 1, K, 24, dtype, lens=[65, 33], seed=92))
+
+
+def test_norms_of_many_heads_and_slots():
+    need_gpu()
+    lens = [1, 70, 0, 33, 64, 128, 7, 100, 3, 17]
+    check_norms(make(1, sum(lens) + 2, 48, 16, 64, 72, BF16, lens=lens, seed=93))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_norms_where_tokens_write_nothing(dtype):
+    need_gpu()
+    d = make(1, 140, 2, 1, 72, 64, dtype, seed=94)
+    d["beta"][0, ::3] = 0.0
+    d["beta"][0, 64:128, 1] = 0.0
+    check_norms(d)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_norms_of_long_gradients(dtype):
+    """Many chunks, on heads that forget nothing, a little, and all of it."""
+    need_gpu()
+    d = make(1, 1100, 3, 3, 64, 40, dtype, seed=95)
+    d["g"] *= torch.tensor([0.0, 0.01, 3.0])
+    check_norms(d)
