@@ -101,3 +101,51 @@ def reference(ins, do, dht, cu=None, scale=None):
     """All of NAMES in 64 bits."""
     o, ht = ref.delta(*ins, cu=cu, scale=scale)
     return dict(zip(NAMES, [o, ht] + ref.grads(*ins, do, dht, cu=cu, scale=scale)))
+
+
+IN = ("q", "k", "v", "g", "beta", "h0")
+
+
+def step_of(which, ins, want, seed=9):
+    """A direction with as much of the gradient in it as of a random one: along it the loss changes by far more than
+    its errors, and a gradient that is wrong in any part shows."""
+    gen = torch.Generator().manual_seed(seed)
+    r = torch.randn(want.shape, generator=gen, dtype=torch.float64)
+    return ((r / r.norm() + want / want.norm()) * 2.0).float()
+
+
+def check_differences(which, ins, do, dht, loss, gradient):
+    """The gradient along a direction against central differences of the loss and against 64 bits. ins: float64
+    inputs by name (those of IN); loss(x): the loss with input `which` replaced by x (fp32); gradient: of it.
+
+    An error of o of norm b changes the loss by at most b |do|; that of the gradient, along d, by at most b |d|.
+    q, v and h0 enter the loss linearly: differences are the gradient. k, beta and g bend it: the same differences
+    of the definition in 64 bits say by how much."""
+    args = [ins[x] for x in IN]
+    want = reference(args, do, dht)["d" + which]
+    d = step_of(which, ins, want)
+    x = ins[which].float()
+    b = bounds(*args, do=do, dht=dht)
+    noise = (b["o"].norm() * do.norm() + b["ht"].norm() * dht.norm()).item()
+    off = (b["d" + which].norm() * d.double().norm()).item()
+    at = (want * d.double()).sum().item()
+    along = (gradient.detach().cpu().double() * d.double()).sum().item()
+    h = 1.0 if which in ("q", "v", "h0") else 1 / 8
+    plus, minus = x + h * d, x - h * d
+
+    def exact(y):
+        o, ht = ref.delta(*[y.double() if n == which else ins[n] for n in IN])
+        return ((o * do).sum() + (ht * dht).sum()).item()
+
+    # what is stepped by is what the fp32 sums are
+    real = ((plus.double() - minus.double()) * want).sum().item() / (2 * h)
+    true, mine = (exact(plus) - exact(minus)) / (2 * h), (loss(plus) - loss(minus)) / (2 * h)
+    if which in ("q", "v", "h0"):
+        assert abs(true - real) <= 1e-9 * abs(real)
+    # (errors of both losses; states are larger by the step: twice)
+    tol = 2 * noise / h
+    assert tol <= 0.01 * abs(at) and off <= 0.01 * abs(at), (which, tol, off, at)
+    assert abs(true - at) <= 0.2 * abs(at), (which, true, at)  # the step is small beside the bend
+    assert abs(mine - true) <= tol, (which, mine, true, tol)
+    assert abs(along - at) <= off, (which, along, at, off)
+    assert abs(along - mine) <= off + tol + abs(true - at), (which, along, mine)

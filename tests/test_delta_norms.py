@@ -57,3 +57,21 @@ def test_planted_mistakes(name, shape):
     for wrong in (torch.zeros_like(w), -w, tail, w * (1 + 2.0 ** -10)):
         over, _ = _ratio(name, wrong.float(), want, bound, d)
         assert over > 1.0, (name, over)
+
+
+@pytest.mark.parametrize("which", norms.IN)
+def test_differences_see_a_wrong_gradient(which):
+    d = make(1, 150, 2, 1, 72, 40, FP32, seed=8)
+    ins, do, dht = dict(zip(norms.IN, inputs64(d))), f64(d["do"]), f64(d["dht"])
+    want = norms.reference([ins[x] for x in norms.IN], do, dht)["d" + which]
+
+    def loss(x, sign=1.0):
+        o, ht = ref.delta(*[x.double() if n == which else ins[n] for n in norms.IN])
+        return sign * ((o.float().double() * do).sum() + (ht.float().double() * dht).sum()).item()
+
+    norms.check_differences(which, ins, do, dht, loss, want.float())
+    for wrong in (torch.zeros_like(want), -want, want * 1.02):
+        with pytest.raises(AssertionError):
+            norms.check_differences(which, ins, do, dht, loss, wrong.float())
+    with pytest.raises(AssertionError):
+        norms.check_differences(which, ins, do, dht, lambda x: loss(x, 0.98), want.float())

@@ -98,3 +98,19 @@ def test_norms_of_long_gradients(dtype):
     d = make(1, 1100, 3, 3, 64, 40, dtype, seed=95)
     d["g"] *= torch.tensor([0.0, 0.01, 3.0])
     check_norms(d)
+
+
+@pytest.mark.parametrize("which", norms.IN)
+def test_gradient_against_close_differences(which):
+    need_gpu()
+    from gated_delta_rule_gate_amd import chunk_gated_delta, chunk_gated_delta_bwd
+
+    d = make(1, 150, 2, 1, 72, 40, FP32, seed=8)
+    g, do, dht = dev(d), f64(d["do"]), f64(d["dht"])
+
+    def loss(x):
+        o, ht = on(dict(g, **{which: x.cuda()}), chunk_gated_delta, output_final_state=True)
+        return ((f64(o) * do).sum() + (f64(ht) * dht).sum()).item()
+
+    norms.check_differences(which, dict(zip(IN, inputs64(d))), do, dht, loss,
+                            on(g, chunk_gated_delta_bwd, g["do"], dht=g["dht"])["d" + which])
