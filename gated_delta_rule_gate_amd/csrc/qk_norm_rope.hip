@@ -89,7 +89,8 @@ __device__ __forceinline__ Place place_of(const QkRope &p, int j) {
 }
 
 // Cosines and sines of `count` tokens from t0 on, each angle by one thread, to LDS: turns in
-// fp64, whole turns taken off there.
+// fp64, whole quarters taken off there, so that what is rounded to fp32 is at most an eighth
+// of a turn (2^-28 of a turn off; half a turn would be 2^-26 off, more than the sines are).
 __device__ __forceinline__ void angles(const QkRope &p, int64_t t0, int count, float *cs) {
   const int half = p.rot / 2;
   for (int idx = threadIdx.x; idx < count * half; idx += 256) {
@@ -108,7 +109,13 @@ __device__ __forceinline__ void angles(const QkRope &p, int64_t t0, int count, f
     }
     double t = ((double)p.pos[at * p.tokens + token] * (double)p.freq[i]) * 0.15915494309189533577;
     t -= rint(t);
-    sincospif(2.0f * (float)t, &cs[count * half + idx], &cs[idx]);
+    const double quarters = rint(4.0 * t);
+    float sn, c;
+    sincospif(2.0f * (float)(t - 0.25 * quarters), &sn, &c);
+    const int n = (int)quarters & 3;
+    const float x = n & 1 ? sn : c, y = n & 1 ? c : sn;
+    cs[idx] = n == 1 || n == 2 ? -x : x;
+    cs[count * half + idx] = n & 2 ? -y : y;
   }
 }
 template <int VEC>

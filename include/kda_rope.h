@@ -10,8 +10,9 @@
  *         t = position inv_freq[i], pair i = channels (i, i + rot/2), or (2i, 2i + 1)
  *
  * with positions on one to four axes (time, height and width of images and
- * video), every frequency i reading one of them. Angles and their reduction are
- * fp64 (three roundings: an angle of 2^31 is off by less than 2^-22 turns), norms,
+ * video), every frequency i reading one of them. Angles and their reduction to
+ * an eighth of a turn and less are fp64 (three roundings: an angle of 2^31 is off
+ * by less than 2^-22 turns), their sines and cosines fp32, within 2^-23, norms,
  * products and weights' gradients fp32 or wider; y is rounded once. It makes
  * the q and k rows of the attention operators: with norm L2 and rot 0 the l2
  * norm that kda_chunk_fwd and kda_delta_chunk_fwd expect. Conventions as in kda.h: device
