@@ -49,7 +49,7 @@ struct DeltaWalk {
   int B, T, H, K, V, N, Hk;
   float scale;
   bool is_bf16;
-  // Long sequences on few heads: cut into segments of seg tokens (0: whole
+  // Long sequences on few heads, with o: cut into segments of seg tokens (0: whole
   // sequences) that are walked side by side. A segment maps the state that enters it
   // affinely, S -> M S + B: a first pass walks it from zeros (B; a sequence's first from
   // its own start) and, with no rows written, from the identity (M), and leaves both at

@@ -73,7 +73,8 @@ void delta_walk_kernel(DeltaWalk p) {
   // not walked and most states only from a segment's last chunks on, while those of a head
   // that decays slowly would else start behind a round of others, or on one XCD.
   const int G = p.H / p.Hk, nvb = (p.V + QT - 1) / QT;
-  const int64_t n_items = p.N + (p.seg ? ((int64_t)p.B * p.T) / p.seg : 0);
+  const int seg = KEEP ? 0 : p.seg;
+  const int64_t n_items = p.N + (seg ? ((int64_t)p.B * p.T) / seg : 0);
   const int64_t maps = MODE == kDeltaState ? (n_items * p.Hk + 7) / 8 * 8 * G * ((p.K + QT - 1) / QT) : 0;  // workgroups
   const bool map = MODE == kDeltaState && blockIdx.x < maps;  // columns of M, not of B
   const int64_t block = map ? blockIdx.x : blockIdx.x - maps;
@@ -83,7 +84,7 @@ void delta_walk_kernel(DeltaWalk p) {
   const int64_t item = n_items - 1 - unit / p.Hk;
   const int hk = (int)((MODE == kDeltaState ? unit + item : unit) % p.Hk), h = hk * G + member / ncb, cb = member % ncb;
   SegLoc sg;
-  if (item < 0 || !locate_part(p, item, p.seg, sg)) return;
+  if (item < 0 || !locate_part(p, item, seg, sg)) return;
   if (MODE == kDeltaState && sg.out < 0) return;  // nothing follows the last segment
   if (map && sg.in < 0) return;                   // a first segment starts from its own state
   const int n = sg.n;
@@ -486,12 +487,13 @@ hipError_t launch_delta_one(const DeltaWalk &p, hipStream_t st) {
 
 template <typename T, int PT, int NW>
 hipError_t launch_delta_mode(const DeltaWalk &p, hipStream_t st) {
+  if (!p.o) return launch_delta_one<T, PT, NW, kDeltaKeep>(p, st);
   if (p.seg) {
     hipError_t e = launch_delta_one<T, PT, NW, kDeltaState>(p, st);
     if (e == hipSuccess) e = launch_delta_chain(p, st);
     if (e != hipSuccess) return e;
   }
-  return p.o ? launch_delta_one<T, PT, NW, kDeltaOut>(p, st) : launch_delta_one<T, PT, NW, kDeltaKeep>(p, st);
+  return launch_delta_one<T, PT, NW, kDeltaOut>(p, st);
 }
 
 template <typename T, int PT>
