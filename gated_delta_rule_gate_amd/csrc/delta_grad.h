@@ -19,9 +19,10 @@
 // the next slab, or of the next item's first, are in flight beside the products of this
 // one. Then m and n go to LDS in the slab's place and meet q and k. The steps of an item
 // wait on each other, so two workgroups share a compute unit and fill each other's
-// pauses: at b4 t2048 h32 d128 396 us, where one workgroup of eight waves and all 128
-// channels with two slabs in flight took 473 us, of sixteen 567 us. The bytes (304 KB a
-// chunk and head, 1.25 GB) would take 225 us, the matrix cores 85 us.
+// pauses: at b4 t2048 h32 d128 389 us, where one workgroup of eight waves and all 128
+// channels with two slabs in flight took 473 us, of sixteen 567 us. Bound by bytes first:
+// 304 KB a chunk and head, 1.28 GB, and as u, du and d_o are read once for each 64 channels
+// 0.34 GB again, together 310 us at the rate of a copy (5.2 TB/s); the matrix cores 85 us.
 #pragma once
 
 #include <algorithm>

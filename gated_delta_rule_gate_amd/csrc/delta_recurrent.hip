@@ -8,7 +8,7 @@
 //
 // so a token costs one pass over the state and one sum across the workgroup.
 // Bound by the state's bytes, read and written once: 256 x 1 tokens, 64 heads of 128 x 128,
-// 379 us, 5.7 TB/s; one token of 16 heads 4 us. A thread holds RPT rows
+// 377 us, 5.7 TB/s; one token of 16 heads 4 us. A thread holds RPT rows
 // of four adjacent columns, so a wave's 16-byte state accesses cover whole
 // runs of a row; they bypass the caches' retention (touched once a call).
 // A column's sums over K run over the lanes that share it, then over the four

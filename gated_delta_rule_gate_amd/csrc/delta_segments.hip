@@ -12,8 +12,8 @@ namespace {
 // in place. One workgroup takes a (sequence, head, 16 columns): its four waves share out the
 // 16-row tiles, each an fp32-accurate product of M's rows (three bf16 parts, split as they
 // are loaded, the next boundary's in flight) with the last state, which passes between the
-// waves through LDS as operands. A chain of short steps, about 3 us a boundary (1 x 32768
-// tokens, 16 heads: 48 us for 16 of them); the next boundary's state and M's parts formed
+// waves through LDS as operands. A chain of short steps, 3.4 us a boundary (1 x 32768
+// tokens, 16 heads: 47 us for 14 of them); the next boundary's state and M's parts formed
 // a boundary ahead as well took 49.
 template <int PT>
 __global__ __launch_bounds__(256) void delta_chain_kernel(DeltaWalk p) {
@@ -127,9 +127,9 @@ hipError_t launch_delta_chain(const DeltaWalk &p, hipStream_t st) {
 
 // Columns of a workgroup: 128, a wave on every SIMD beside another; 64 where V has no
 // more, for fp32 inputs, whose three parts leave no registers for more, and where 128
-// would leave half the compute units idle (a chunk of 128 x 128 then takes 3.1 us
-// instead of 4.8: 128 (sequence, head) pairs of 2048 tokens 147 us by 64, 211 us by
-// 128; with 256 pairs of 4096 tokens 497 us by 64, 403 us by 128).
+// would leave half the compute units idle (a chunk of 128 x 128 then takes 3.9 us
+// instead of 5.7: calls on 128 (sequence, head) pairs of 2048 tokens 163 us by 64, 219 us
+// by 128; on 256 pairs of 4096 tokens 602 us by 64, 543 us by 128).
 int delta_cols(const DeltaWalk &p, int *ncb) {
   const int64_t parts = p.seg ? (int64_t)p.B * p.T / p.seg : p.N;
   const int64_t wide = std::max<int64_t>(parts, p.N) * p.H * ((p.V + 127) / 128);
@@ -147,15 +147,22 @@ bool delta_walk_fits(const DeltaWalk &p) {
 
 // Segments pay where whole sequences leave compute units idle or wait for the longest.
 // Costs in microseconds a chunk and workgroup as measured for bf16, 128 x 128, by 128 or 64
-// columns: 6.3 or 3.9 (4.8 or 3.1 alone on the device) with o, 0.8 of that in the state
-// pass, whose segments (all but a sequence's last) walk V and, but for the first, K
-// columns; two chunks for a segment's start and end; two more launches and a boundary's step of the chain 2.5 us. With decays most
-// maps are zero and not walked (delta_walk.h): an eighth is counted. (That states are then
-// walked from a segment's last chunks on only is not: the pass waits for the slowest head.)
-// How it chooses, walks and chain together: 1 x 32768 tokens, 16 heads: 17 segments, 420 us
-// (none: 1560); 15872 tokens in 10 slots, 32 heads, segments of 10, 13, 16, 20 (its
-// choice), 24, 30 chunks: 504, 485, 432, 444, 417, 452 us (steps of the slots' own
-// lengths; none: 497); fp32, 2 x 1000 tokens, 8 heads: 7 segments, 58 us (none: 84).
+// columns when o took two parts: 6.3 or 3.9 (4.8 or 3.1 alone on the device) with o, 0.8 of
+// that in the state pass, whose segments (all but a sequence's last) walk V and, but for the
+// first, K columns. They serve every width and type, and what o takes now (7.1, 5.7) would
+// move the choices below by a chunk at most. Two chunks for a segment's start and end; two
+// more launches and a boundary's step of the chain 2.5 us. With decays most maps are zero
+// and not walked (delta_walk.h): an eighth is counted. (That states are then walked from a
+// segment's last chunks on only is not: the pass waits for the slowest head.)
+// What it chooses, and whole calls: 1 x 32768 tokens, 16 heads: 35 chunks, 428 us (31: 509,
+// 32: 416, 64: 401, none: 1690); fp32, 2 x 1000 tokens, 8 heads: 5 chunks, 65 us (8: 62,
+// none: 91). 15872 packed tokens, 32 heads: 18 chunks whatever the 10 slots' lengths are:
+//                              10   13   16   18   20   24   30  none
+//     random cuts             496  477  450  450  440  448  483   558 us
+//     equal slots             471  392  418  433  448  482  360   342
+//     one of 14972, nine 100  597  544  537  539  512  555  530  1308
+// Chosen without the slots' own lengths, it bounds what a long one costs, and takes a
+// quarter more than the best for equal ones.
 int delta_segment(const DeltaWalk &p, bool packed, bool gated) {
   const int C = delta_chunk(linear_tile(p.K), p.is_bf16);
   const double room = device_cus(), maps = gated ? 0.12 : 1.0;

@@ -14,16 +14,17 @@
 // form a chunk ahead; a chunk's scores meet its u in the next one's time.
 //
 // Products on the bf16 matrix cores, an fp32 operand as a sum of three bf16 parts (24
-// bits), of whose products with those of another the ones of at most 2^-24 are left out. So with o
-// of bf16 inputs too: with two parts in the state's copy, the scores and u (16 bits), 0.3%
-// of its values were rounded to the neighbour of the nearest bf16 value, in place of 0.01%,
-// for 4 to 8% of the time (b4 t4096 h64 d128: 40 us).
+// bits), of whose products with another's those of at most 2^-24 are left out. So for o of
+// bf16 inputs too: with two parts in the state's copy, the scores and u (16 bits), 0.3% of
+// its values were rounded to the neighbour of the nearest bf16 value, in place of 0.01%; it
+// costs 4 to 8% of a call (b4 t4096 h64 d128: 40 us).
 //
 // Bound by the chain of a chunk's steps, which one or two state waves a SIMD hide little of
-// (matrix cores busy 47% of the time, vector units 45%): a chunk of 128 x 128 takes 6.3 us
-// with every compute unit at work, at a clock that falls under this load, 4.8 us alone.
-// b4 t4096 h64 d128: 400 to 415 us (the case's bytes take 215), in two periods a chunk with
-// two barriers 497; u and states kept, b4 t2048 h32 d128: 135 to 140 us for 700 MB.
+// (matrix cores busy 46% of the time, vector units 41%): a chunk of 128 x 128 takes 7.1 us
+// with every compute unit at work, at a clock that falls under this load, 5.7 us where half
+// of them are. b4 t4096 h64 d128: 440 to 460 us (the case's bytes take 215); in two periods
+// a chunk with two barriers 497 when one took 405. u and states kept, b4 t2048 h32 d128: 135
+// to 140 us for 700 MB.
 #pragma once
 
 #include "delta_chunk.h"
@@ -134,8 +135,8 @@ void delta_walk_kernel(DeltaWalk p) {
   if (wave >= NW) {
     // =================================== helper waves ===================================
     // What a helper holds up, all state waves wait for. With two state waves to a helper on
-    // a SIMD (b4 t4096 h64) 400 us for 405; with one each the state wave is the later one
-    // (b4 t2048 h32, u and states kept: 140 us without, 150 with).
+    // a SIMD (b4 t4096 h64) a call takes 543 us for 546; with one each the state wave is the
+    // later one (b4 t2048 h32, u and states kept: 140 us without, 150 with).
     if constexpr (NW == 8) __builtin_amdgcn_s_setprio(2);
     const int hw = wave - NW, ht = tid - 64 * NW;
     const int ldx = p.Hk * K;  // row stride, elements

@@ -13,8 +13,9 @@
 // took b4 t4096 h32/8 d128 from 74 to 89 us. Weights' gradients stay in registers over a
 // workgroup's rows, leave as one part a workgroup, and are added over workgroups in order.
 //
-// Bound by the rows' bytes: at b4 t4096 h32/8 d128 the forward takes 70 us and the backward
-// 109 + 4 us, where their 336 and 503 MB would take 64 and 97 us at a large copy's 5.2 TB/s.
+// Bound by the rows' bytes: at b4 t4096 h32/8 d128 the forward takes 72 us and the backward
+// 105 + 5 us, where their 336 and 503 MB would take 64 and 97 us at a large copy's 5.2 TB/s;
+// the fp32 forward 138 us for 129.
 #include "../../include/kda_rope.h"
 #include "kda_device.h"
 #include "linear_launch.h"

@@ -30,7 +30,8 @@
  *   - State, decays and their sums are held in fp32 or wider. Products run on
  *     the bf16 matrix cores with every fp32 operand taken as a sum of bf16
  *     parts, so fp32 results (states, dg, dbeta, and every output of fp32
- *     calls) carry fp32 rounding, not bf16's.
+ *     calls) carry fp32 rounding, not bf16's, and bf16 results are such results
+ *     rounded once.
  *   - Outputs must not overlap inputs, other than ht on h0 itself.
  *   - fp32 inputs above 3.38e38 (bf16's largest value) count as infinite.
  *   - A NaN or infinity in q, k, v or beta, or a g that is NaN or +infinity,
